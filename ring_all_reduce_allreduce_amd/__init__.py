@@ -18,6 +18,12 @@ Functions carry the C names without the ``ringsim_`` prefix:
     debug_tree(nranks, rank); debug_tree_model(nranks, tree_channels, bytes_per_rank)
     debug_flag_steps(coll, algo, nranks, nchannels, chunk_bytes, count, dtype, proto)
 
+and, for what a rank computes next to its collectives (``operators.py``; C ABI
+in ``include/ringsim_ops.h``):
+
+    rms_norm(x, weight=None, residual=None, ...); rms_norm_backward(grad_out, h, weight=None, ...)
+    grad_norm(grads, ...); scale_grads(grads, norm, max_norm, ...); clip_grads(grads, max_norm, ...)
+
 ``sendbufs``/``recvbufs`` are lists (one per simulated rank) of CUDA/HIP
 tensors of one dtype, or of raw device addresses (ints; then ``dtype`` and the
 count must be given). Every call is asynchronous on ``stream`` (default: the
@@ -36,6 +42,7 @@ from typing import Sequence
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libringsim.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "ringsim.h")
+OPS_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "ringsim_ops.h")
 
 SUCCESS = 0
 RESULT_NAMES = {
@@ -128,6 +135,7 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m ring_all_reduce_allreduce_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
     vp, i, sz, res = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
+    i64, f32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "ringsim_config_default": (res, [ctypes.POINTER(Config)]),
         "ringsim_comm_init": (res, [ctypes.POINTER(vp), i, i, i]),
@@ -148,6 +156,14 @@ def lib() -> ctypes.CDLL:
         "ringsim_debug_tree_model": (res, [i, i, sz, ctypes.POINTER(ctypes.c_double)]),
         "ringsim_allreduce_noalloc": (res, [i, i, _c_ptrs, _c_ptrs, sz, i, i, vp]),
         "ringsim_debug_flag_steps": (res, [i, i, i, i, sz, sz, i, i, ctypes.POINTER(ctypes.c_uint64)]),
+        # include/ringsim_ops.h
+        "ringsim_rms_norm": (res, [vp, vp]),
+        "ringsim_rms_norm_backward": (res, [vp, vp]),
+        "ringsim_rms_norm_backward_workspace": (res, [i64, i64, ctypes.POINTER(sz)]),
+        "ringsim_grad_norm": (res, [i, vp, vp, vp, f32, vp, vp, sz, vp]),
+        "ringsim_grad_norm_workspace": (res, [i, ctypes.POINTER(sz)]),
+        "ringsim_scale_grads": (res, [i, vp, vp, vp, vp, f32, vp, f32, f32, vp]),
+        "ringsim_clip_grads": (res, [i, vp, vp, vp, vp, f32, f32, f32, vp, vp, sz, vp]),
     }
     for name, (rt, args) in sig.items():
         f = getattr(L, name)
@@ -408,3 +424,17 @@ def header_exports() -> list[str]:
     with open(HEADER_PATH) as f:
         text = f.read()
     return sorted(set(re.findall(r"\b(ringsim_[a-z_]+)\s*\(", text)))
+
+
+# The step operators need torch's types, so they load with their first use
+# (the collectives' host-only calls work before torch is imported).
+_OPERATORS = ("rms_norm", "rms_norm_backward", "grad_norm", "scale_grads", "clip_grads")
+
+
+def __getattr__(name: str):
+    if name in _OPERATORS:
+        from . import operators
+
+        globals()[name] = getattr(operators, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -24,6 +24,10 @@ SOURCES = [
     ("ring_lines_inst.hip", "ring_lines_multi", ["-DRINGSIM_LINE_MODE=kLinesMulti", "-DRINGSIM_LINE_NAME=multi"]),
     ("tree.hip", "tree", []),
     ("copy.hip", "copy", []),
+    ("ringsim_ops.hip", "ringsim_ops", []),
+    ("rms_norm.hip", "rms_norm", []),
+    ("rms_norm_backward.hip", "rms_norm_backward", []),
+    ("grad_norm.hip", "grad_norm", []),
 ]
 ARCH = "gfx950"
 

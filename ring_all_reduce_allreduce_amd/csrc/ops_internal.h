@@ -1,0 +1,98 @@
+// ops_internal.h -- kernel arguments and launch rules of the step operators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ringsim_ops.h"
+
+namespace ringsim {
+
+constexpr int kComputeUnits = 256;  // of one MI355X
+
+inline int op_dtype_size(int dtype) {
+  switch (dtype) {
+    case RINGSIM_FLOAT32: return 4;
+    case RINGSIM_BFLOAT16: return 2;
+    case RINGSIM_FLOAT16: return 2;
+    case RINGSIM_FLOAT8_E4M3: return 1;
+    default: return 0;
+  }
+}
+
+// A [outer, inner, cols] tensor: row r is at p + (r / inner) * s0 + (r % inner) * s1 elements.
+struct RowsIn {
+  const void* p;
+  int64_t s0, s1;
+};
+struct RowsOut {
+  void* p;
+  int64_t s0, s1;
+};
+
+enum WeightKind : int { kWeightNone = 0, kWeightSame = 1, kWeightF32 = 2 };
+
+struct RmsNormArgs {
+  RowsIn x, residual;        // residual.p null: none
+  const void* weight;
+  RowsOut out, residual_out;
+  float* scales;             // null: out has the input's type
+  uint32_t rows, inner;
+  int cols, groups, group;   // group 0: one scale a row
+  int weight_kind;
+  float eps, inv_cols;
+};
+
+struct RmsNormBackwardArgs {
+  RowsIn grad_out, h, grad_residual;  // grad_residual.p null: none
+  const void* weight;
+  RowsOut grad_in;
+  float* partial;            // [workgroups, cols] sums of grad_out * h * r; null: not wanted
+  uint32_t rows, inner;
+  int cols;
+  int weight_kind;
+  float eps, inv_cols;
+};
+
+// How a row is laid over lanes: `lanes` lanes of a workgroup hold a row,
+// `packs` packs of eight elements each.
+struct RowShape {
+  int lanes, packs;
+};
+RowShape norm_shape(int64_t rows, int64_t cols);
+RowShape norm_backward_shape(int64_t rows, int64_t cols);
+int norm_backward_workgroups(int64_t rows, int64_t cols);
+
+hipError_t launch_rms_norm(const RmsNormArgs& a, int dtype, hipStream_t s);
+hipError_t launch_rms_norm_backward(const RmsNormBackwardArgs& a, int dtype, hipStream_t s);
+// grad_weight[c] = sum over `parts` rows of partial, in a fixed order.
+hipError_t launch_rms_norm_weight_sum(const float* partial, int parts, int cols, void* grad_weight, int dtype,
+                                      hipStream_t s);
+
+// A launch's tensors and the tiles they are cut into: tensor i holds tiles
+// [tile0[i], tile0[i + 1]) of kGradTileBytes each, its last one shorter.
+// The table travels as a kernel argument (below 4 KiB), which a graph's
+// capture keeps by itself.
+constexpr int kGradTileBytes = 16384;
+constexpr int kGradTensors = 128;
+constexpr int kGradWorkgroups = 2048;  // most of a launch
+struct GradTable {
+  const void* in[kGradTensors];
+  void* out[kGradTensors];         // norm: unused
+  uint32_t tile0[kGradTensors + 1];
+  uint16_t last[kGradTensors];     // elements of the tensor's last tile
+  uint8_t dtype[kGradTensors];
+  int ntensors;
+};
+
+hipError_t launch_grad_squares(const GradTable& t, double* partial, int workgroups, hipStream_t s);
+hipError_t launch_grad_norm_join(const double* partial, int parts, float scale, float* norm, hipStream_t s);
+struct GradFactor {
+  const double* partial;  // join these into the norm, or
+  int parts;
+  float* norm;            // partial null: read the norm here; else workgroup 0 writes it here, if not null
+  float scale, max_norm, eps;
+};
+hipError_t launch_grad_scale(const GradTable& t, const GradFactor& f, int in_place, int workgroups, hipStream_t s);
+
+}  // namespace ringsim

@@ -1,0 +1,196 @@
+// rms_norm.hip -- root-mean-square norm of rows, forward.
+//
+// For every row:  h = x (+ residual),  y = h / sqrt(mean(h^2) + eps) * w,
+// y in the input's type or in 8 bits with scales. The row is read once: its
+// lanes keep h in registers as fp32 between the sum of squares and the
+// product. What bounds it is memory: 4 x 2 bytes an element in bf16 with a
+// residual (x, residual, h, y) against about 6 operations.
+#include <algorithm>
+
+#include "ops_device.h"
+
+namespace ringsim {
+
+template <int DT, int TPR, int NP, bool Q>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNormArgs a) {
+  constexpr int kBlock = TPR < 256 ? 256 : TPR;
+  constexpr int kRows = kBlock / TPR;  // rows of a workgroup at a time
+  using T = typename OpElem<DT>::T;
+  __shared__ float sums[2][16];
+  __shared__ uint32_t tops[2][16];
+  int turn = 0, qturn = 0;
+  const int t = threadIdx.x % TPR;
+  float w[NP][kPack];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c = (k * TPR + t) * kPack;
+    load_weight<DT>(a.weight, a.weight_kind, c, a.cols - c, w[k]);
+  }
+  for (uint32_t row = blockIdx.x * kRows + threadIdx.x / TPR; row < a.rows; row += gridDim.x * kRows) {
+    const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
+    float h[NP][kPack];
+    Pack<DT> x[NP], res[NP];
+    const T* px = row_ptr<DT>(a.x, o, in);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      const int c = (k * TPR + t) * kPack;
+      x[k] = load_pack<DT>(px + c, a.cols - c);
+    }
+    if (a.residual.p) {
+      const T* pr = row_ptr<DT>(a.residual, o, in);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c = (k * TPR + t) * kPack;
+        res[k] = load_pack<DT>(pr + c, a.cols - c);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) unpack<DT>(x[k], h[k]);
+    if (a.residual.p) {
+      T* ph = row_ptr<T>(a.residual_out, o, in);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c = (k * TPR + t) * kPack;
+        float f[kPack];
+        unpack<DT>(res[k], f);
+#pragma unroll
+        for (int i = 0; i < kPack; ++i) h[k][i] += f[i];
+        store_pack<DT>(ph + c, to_pack<DT>(h[k]), a.cols - c);
+      }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+#pragma unroll
+      for (int i = 0; i < kPack; ++i) ss = __builtin_fmaf(h[k][i], h[k][i], ss);
+    }
+    ss = row_reduce<TPR, AddF32>(ss, sums, turn);
+    const float r = rsqrtf(__builtin_fmaf(ss, a.inv_cols, a.eps));
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+#pragma unroll
+      for (int i = 0; i < kPack; ++i) h[k][i] = h[k][i] * r * w[k][i];
+    }
+    if constexpr (!Q) {
+      T* py = row_ptr<T>(a.out, o, in);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c = (k * TPR + t) * kPack;
+        store_pack<DT>(py + c, to_pack<DT>(h[k]), a.cols - c);
+      }
+    } else {
+      // Largest |y| of the row, or of the 4, 8 or 16 lanes that hold a group
+      // (groups start at multiples of their width, lanes beyond the row hold 0).
+      uint32_t top[NP];
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c = (k * TPR + t) * kPack;
+        top[k] = 0;
+#pragma unroll
+        for (int i = 0; i < kPack; ++i)
+          if (c + i < a.cols) top[k] = MaxBits::of(top[k], __float_as_uint(h[k][i]) & 0x7fffffffu);
+      }
+      if (a.group == 0) {
+#pragma unroll
+        for (int k = 1; k < NP; ++k) top[0] = MaxBits::of(top[0], top[k]);
+        top[0] = row_reduce<TPR, MaxBits>(top[0], tops, qturn);
+#pragma unroll
+        for (int k = 1; k < NP; ++k) top[k] = top[0];
+      } else {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          top[k] = lanes_reduce<4, MaxBits>(top[k]);
+          if (a.group >= 64) top[k] = MaxBits::of(top[k], dpp<0x141>(top[k]));
+          if (a.group >= 128) top[k] = MaxBits::of(top[k], dpp<0x140>(top[k]));
+        }
+      }
+      uint8_t* py = row_ptr<uint8_t>(a.out, o, in);
+      float* ps = a.scales + (int64_t)row * a.groups;
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int c = (k * TPR + t) * kPack;
+        // Not fmaxf, which would drop a NaN.
+        float scale = __uint_as_float(top[k]) / 448.0f;
+        scale = scale < 0x1p-126f ? 0x1p-126f : scale;
+        if (a.group == 0) {
+          if (k == 0 && t == 0) ps[0] = scale;
+        } else if (c < a.cols && c % a.group == 0) {
+          ps[c / a.group] = scale;
+        }
+        // |y| * inv is at most 448 (1 + 2^-22), which rounds to 448, the
+        // largest e4m3 value: nothing to clamp.
+        const float inv = 1.0f / scale;
+        float q[kPack];
+#pragma unroll
+        for (int i = 0; i < kPack; ++i) q[i] = h[k][i] * inv;
+        u32x2 b;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          int v = 0;
+          v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * j], q[4 * j + 1], v, false);
+          v = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * j + 2], q[4 * j + 3], v, true);
+          b[j] = (uint32_t)v;
+        }
+        if (c + kPack <= a.cols) {
+          *reinterpret_cast<u32x2_e1*>(py + c) = b;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPack - 1; ++i)
+            if (c + i < a.cols) py[c + i] = (uint8_t)(b[i / 4] >> (8 * (i % 4)));
+        }
+      }
+    }
+  }
+}
+
+RowShape norm_shape(int64_t rows, int64_t cols) {
+  const int64_t packs = (cols + kPack - 1) / kPack;
+  if (packs <= 16) return {16, 1};
+  if (packs <= 64) return {64, 1};
+  if (packs <= 128) return {64, 2};
+  if (packs <= 256) return {256, 1};
+  if (packs <= 512) return {256, 2};
+  if (packs <= 1024) return {256, 4};
+  if (packs <= 2048) return {1024, 2};
+  return {1024, 4};
+}
+
+template <int DT, int TPR, int NP>
+static hipError_t launch_shape(const RmsNormArgs& a, hipStream_t s) {
+  constexpr int kBlock = TPR < 256 ? 256 : TPR;
+  constexpr int kRows = kBlock / TPR;
+  const int64_t need = ((int64_t)a.rows + kRows - 1) / kRows;
+  const dim3 grid((unsigned)std::min<int64_t>(need, (int64_t)kComputeUnits * (2048 / kBlock))), block(kBlock);
+  if (a.scales)
+    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, false>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+static hipError_t launch_type(const RmsNormArgs& a, hipStream_t s) {
+  const RowShape sh = norm_shape(a.rows, a.cols);
+  switch (sh.lanes * 16 + sh.packs) {
+    case 16 * 16 + 1: return launch_shape<DT, 16, 1>(a, s);
+    case 64 * 16 + 1: return launch_shape<DT, 64, 1>(a, s);
+    case 64 * 16 + 2: return launch_shape<DT, 64, 2>(a, s);
+    case 256 * 16 + 1: return launch_shape<DT, 256, 1>(a, s);
+    case 256 * 16 + 2: return launch_shape<DT, 256, 2>(a, s);
+    case 256 * 16 + 4: return launch_shape<DT, 256, 4>(a, s);
+    case 1024 * 16 + 2: return launch_shape<DT, 1024, 2>(a, s);
+    case 1024 * 16 + 4: return launch_shape<DT, 1024, 4>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_rms_norm(const RmsNormArgs& a, int dtype, hipStream_t s) {
+  switch (dtype) {
+    case RINGSIM_FLOAT32: return launch_type<RINGSIM_FLOAT32>(a, s);
+    case RINGSIM_BFLOAT16: return launch_type<RINGSIM_BFLOAT16>(a, s);
+    case RINGSIM_FLOAT16: return launch_type<RINGSIM_FLOAT16>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace ringsim
