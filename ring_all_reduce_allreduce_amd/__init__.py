@@ -135,7 +135,6 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m ring_all_reduce_allreduce_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
     vp, i, sz, res = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
-    i64, f32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "ringsim_config_default": (res, [ctypes.POINTER(Config)]),
         "ringsim_comm_init": (res, [ctypes.POINTER(vp), i, i, i]),
@@ -156,14 +155,6 @@ def lib() -> ctypes.CDLL:
         "ringsim_debug_tree_model": (res, [i, i, sz, ctypes.POINTER(ctypes.c_double)]),
         "ringsim_allreduce_noalloc": (res, [i, i, _c_ptrs, _c_ptrs, sz, i, i, vp]),
         "ringsim_debug_flag_steps": (res, [i, i, i, i, sz, sz, i, i, ctypes.POINTER(ctypes.c_uint64)]),
-        # include/ringsim_ops.h
-        "ringsim_rms_norm": (res, [vp, vp]),
-        "ringsim_rms_norm_backward": (res, [vp, vp]),
-        "ringsim_rms_norm_backward_workspace": (res, [i64, i64, ctypes.POINTER(sz)]),
-        "ringsim_grad_norm": (res, [i, vp, vp, vp, f32, vp, vp, sz, vp]),
-        "ringsim_grad_norm_workspace": (res, [i, ctypes.POINTER(sz)]),
-        "ringsim_scale_grads": (res, [i, vp, vp, vp, vp, f32, vp, f32, f32, vp]),
-        "ringsim_clip_grads": (res, [i, vp, vp, vp, vp, f32, f32, f32, vp, vp, sz, vp]),
     }
     for name, (rt, args) in sig.items():
         f = getattr(L, name)

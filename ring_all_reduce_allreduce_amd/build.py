@@ -1,4 +1,5 @@
-"""Builds libringsim.so in-tree with hipcc for gfx950.
+"""Builds libringsim.so, and the operators' Python extension on top of it,
+in-tree with hipcc for gfx950.
 
 Usage: python -m ring_all_reduce_allreduce_amd.build [--verbose]
 """
@@ -14,6 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libringsim.so")
+BINDING = os.path.join(PKG, "_ops_binding.so")
 # (source, object name, extra defines): the line kernel's instantiation unit
 # is compiled once per line mode.
 SOURCES = [
@@ -54,19 +56,43 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found: the ROCm toolchain is required to build libringsim")
 
 
+def binding_flags() -> list[str]:
+    """Host code only: where torch's and Python's headers are."""
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    return ["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+            f"-I{sysconfig.get_paths()['include']}"]
+
+
+def torch_lib_dir() -> str:
+    import torch
+
+    return os.path.join(os.path.dirname(torch.__file__), "lib")
+
+
 def build(verbose: bool = False) -> str:
-    """Compiles every source to an object, links libringsim.so, returns its path."""
+    """Compiles every source to an object, links libringsim.so and the
+    operators' Python extension, returns the library's path."""
     cc = hipcc()
     with tempfile.TemporaryDirectory(prefix="ringsim_build_") as tmp:
+        binding_obj = os.path.join(tmp, "ops_binding.o")
         objs = []
         procs = []
-        for src, name, defines in SOURCES:
-            obj = os.path.join(tmp, name + ".o")
-            cmd = [cc, *HIP_FLAGS, *defines, "-c", os.path.join(CSRC, src), "-o", obj]
+        jobs = [(name, [cc, *HIP_FLAGS, *defines, "-c", os.path.join(CSRC, src), "-o", os.path.join(tmp, name + ".o")])
+                for src, name, defines in SOURCES]
+        jobs.append(("ops_binding", [cc, *binding_flags(), "-c", os.path.join(CSRC, "ops_binding.cpp"), "-o",
+                                     binding_obj]))
+        for name, cmd in jobs:
+            obj = cmd[-1]
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-            objs.append(obj)
+            if obj != binding_obj:
+                objs.append(obj)
         failed = []
         for src, p in procs:
             out, _ = p.communicate()
@@ -82,6 +108,13 @@ def build(verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp_lib, LIB)
+        # Loaded by Python, so Python's symbols stay open; libringsim.so is found beside it.
+        cmd = [cc, "-shared", "-fPIC", "-o", BINDING + ".tmp", binding_obj, f"-L{torch_lib_dir()}", "-lc10",
+               "-lc10_hip", "-ltorch_cpu", "-ltorch_python", f"-L{PKG}", "-l:libringsim.so", "-Wl,-rpath,$ORIGIN"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 
