@@ -12,7 +12,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // The same vectors at an address that is only aligned to an element: gfx950
 // reads and writes them with one 128-bit access all the same.
 typedef u32x4 u32x4_e2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_e4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_e2 __attribute__((aligned(2)));
+typedef uint32_t u32_e2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_e1 __attribute__((aligned(1)));
 
 constexpr int kPack = 8;  // elements a lane holds side by side: 16 bytes of a 16-bit type, 32 of fp32
@@ -20,13 +21,13 @@ constexpr int kPack = 8;  // elements a lane holds side by side: 16 bytes of a 1
 template <int DT>
 struct OpElem {
   using T = uint16_t;
-  using V = u32x4_e2;
-  static constexpr int kVecs = 1;  // 16-byte vectors of a pack
+  static constexpr int kPerVec = 8;  // elements of a 16-byte vector
+  static constexpr int kVecs = 1;    // vectors of a pack
 };
 template <>
 struct OpElem<RINGSIM_FLOAT32> {
   using T = uint32_t;
-  using V = u32x4_e4;
+  static constexpr int kPerVec = 4;
   static constexpr int kVecs = 2;
 };
 
@@ -58,33 +59,96 @@ __device__ __forceinline__ typename OpElem<DT>::T f32_to_elem(float f) {
   }
 }
 
-// Elements [0, n) of a pack at p; the others become 0. n >= kPack reads whole
-// vectors, n <= 0 nothing.
-template <int DT>
-__device__ __forceinline__ Pack<DT> load_pack(const typename OpElem<DT>::T* p, int n) {
-  using E = OpElem<DT>;
-  Pack<DT> r;
-  if (n >= kPack) {
+// How a kernel reads its rows: through the caches, past them (data that the
+// Infinity Cache will not hold until it is needed again), or element by
+// element, for rows shorter than a vector.
+enum LoadKind : int { kLoadCached = 0, kLoadStream = 1, kLoadShort = 2 };
+
+// 16 bytes at byte `at` of a sequence of `bytes`, whose length need not be a
+// multiple of 16. No branch around the load: a vector that would pass the end
+// is read from where the last whole one starts, so every lane reads inside
+// the sequence and all loads of a thread are under way before the first one
+// is used; fix16 then moves the elements to their places and puts zeros
+// behind them. (Reading the rest element by element, the compiler made
+// dependent loads of it and waited after each.) `bytes` is at least 16 unless
+// the kind is kLoadShort; `at` may start at or past the end.
+template <int LK>
+__device__ __forceinline__ u32x4 load16(const void* p, int at, int bytes) {
+  const char* c = static_cast<const char*>(p);
+  if constexpr (LK == kLoadShort) {
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < E::kVecs; ++i) r.v[i] = reinterpret_cast<const typename E::V*>(p)[i];
+    for (int i = 0; i < 8; ++i)
+      if (at + 2 * i < bytes) w[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(c + at + 2 * i) << (16 * (i % 2));
+    return u32x4{w[0], w[1], w[2], w[3]};
   } else {
-    uint32_t w[4 * E::kVecs];
-#pragma unroll
-    for (int i = 0; i < 4 * E::kVecs; ++i) w[i] = 0;
-#pragma unroll
-    for (int i = 0; i < kPack - 1; ++i) {
-      if (i < n) {
-        if constexpr (E::kVecs == 2) {
-          w[i] = p[i];
-        } else {
-          w[i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < E::kVecs; ++i) r.v[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+    const int start = at < bytes - 16 ? at : bytes - 16;
+    const u32x4_e2* q = reinterpret_cast<const u32x4_e2*>(c + start);
+    return LK == kLoadStream ? __builtin_nontemporal_load(q) : *q;
   }
+}
+
+template <int LK>
+__device__ __forceinline__ u32x4 fix16(u32x4 v, int at, int bytes) {
+  const int over = at - (bytes - 16);  // bytes to move down by
+  if (LK == kLoadShort || over <= 0) return v;
+  if (over >= 16) return u32x4{0, 0, 0, 0};
+  if (over & 8) v = u32x4{v[2], v[3], 0, 0};
+  if (over & 4) v = u32x4{v[1], v[2], v[3], 0};
+  if (over & 2) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  return v;
+}
+
+// Writes what lies below `bytes` of 16 bytes at byte `at`. Whole vectors go
+// out non-temporally: written lines that stay out of the L2s leave them to
+// the reads. A 64 MiB copy over three buffer sets takes 20.2 us so and 24.5
+// us with plain stores; a kernel that reads the result next takes as much
+// longer as was saved at 32-128 MiB, and less at 512 MiB (272 us for the
+// pair against 294).
+__device__ __forceinline__ void store16(void* p, u32x4 v, int at, int bytes) {
+  char* c = static_cast<char*>(p) + at;
+  const int left = bytes - at;
+  if (left >= 16) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_e2*>(c));
+  } else if (left > 0) {
+    // 8, 4 and 2 bytes as the rest's length has them.
+    if (left & 8) {
+      *reinterpret_cast<u32x2_e2*>(c) = u32x2{v[0], v[1]};
+      v[0] = v[2];
+      v[1] = v[3];
+      c += 8;
+    }
+    if (left & 4) {
+      *reinterpret_cast<u32_e2*>(c) = v[0];
+      v[0] = v[1];
+      c += 4;
+    }
+    if (left & 2) *reinterpret_cast<uint16_t*>(c) = (uint16_t)v[0];
+  }
+}
+
+// The pack at element c of a row of `cols`; fix_pack before its elements count.
+template <int DT, int LK = kLoadCached>
+__device__ __forceinline__ Pack<DT> load_pack(const void* row, int c, int cols) {
+  constexpr int kSize = (int)sizeof(typename OpElem<DT>::T);
+  Pack<DT> r;
+#pragma unroll
+  for (int i = 0; i < OpElem<DT>::kVecs; ++i) r.v[i] = load16<LK>(row, c * kSize + 16 * i, cols * kSize);
   return r;
+}
+
+template <int DT, int LK = kLoadCached>
+__device__ __forceinline__ void fix_pack(Pack<DT>& r, int c, int cols) {
+  constexpr int kSize = (int)sizeof(typename OpElem<DT>::T);
+#pragma unroll
+  for (int i = 0; i < OpElem<DT>::kVecs; ++i) r.v[i] = fix16<LK>(r.v[i], c * kSize + 16 * i, cols * kSize);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_pack(void* row, const Pack<DT>& r, int c, int cols) {
+  constexpr int kSize = (int)sizeof(typename OpElem<DT>::T);
+#pragma unroll
+  for (int i = 0; i < OpElem<DT>::kVecs; ++i) store16(row, r.v[i], c * kSize + 16 * i, cols * kSize);
 }
 
 template <int DT>
@@ -125,27 +189,6 @@ __device__ __forceinline__ Pack<DT> to_pack(const float* f) {
     }
   }
   return r;
-}
-
-// Writes elements [0, n) of a pack to p.
-template <int DT>
-__device__ __forceinline__ void store_pack(typename OpElem<DT>::T* p, const Pack<DT>& r, int n) {
-  using E = OpElem<DT>;
-  if (n >= kPack) {
-#pragma unroll
-    for (int i = 0; i < E::kVecs; ++i) reinterpret_cast<typename E::V*>(p)[i] = r.v[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < kPack - 1; ++i) {
-      if (i < n) {
-        if constexpr (E::kVecs == 2) {
-          p[i] = r.v[i / 4][i % 4];
-        } else {
-          p[i] = (uint16_t)(r.v[0][i / 2] >> (16 * (i % 2)));
-        }
-      }
-    }
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -226,16 +269,40 @@ __device__ __forceinline__ T* row_ptr(const RowsOut& t, uint32_t o, uint32_t i) 
   return static_cast<T*>(t.p) + ((int64_t)o * t.s0 + (int64_t)i * t.s1);
 }
 
-// Eight weights as fp32.
-template <int DT>
-__device__ __forceinline__ void load_weight(const void* w, int kind, int c, int n, float* f) {
+// Eight weights as they lie in memory: in the rows' type or in fp32.
+struct WeightPack {
+  u32x4 v[2];
+};
+
+template <int DT, int LK>
+__device__ __forceinline__ WeightPack load_weight(const void* w, int kind, int c, int cols) {
+  constexpr int kSize = (int)sizeof(typename OpElem<DT>::T);
+  constexpr int kKind = LK == kLoadShort ? kLoadShort : kLoadCached;
+  WeightPack r;
+  r.v[0] = r.v[1] = u32x4{0, 0, 0, 0};
+  if (kind != kWeightNone) {
+    const int size = kind == kWeightF32 ? 4 : kSize;
+    r.v[0] = load16<kKind>(w, c * size, cols * size);
+    if (size == 4) r.v[1] = load16<kKind>(w, c * 4 + 16, cols * 4);
+  }
+  return r;
+}
+
+// The weights as fp32, zeros beyond the row (ones without a weight).
+template <int DT, int LK>
+__device__ __forceinline__ void unpack_weight(const WeightPack& r, int kind, int c, int cols, float* f) {
   if (kind == kWeightNone) {
 #pragma unroll
     for (int i = 0; i < kPack; ++i) f[i] = 1.0f;
   } else if (DT == RINGSIM_FLOAT32 || kind == kWeightF32) {
-    unpack<RINGSIM_FLOAT32>(load_pack<RINGSIM_FLOAT32>(static_cast<const uint32_t*>(w) + c, n), f);
+    Pack<RINGSIM_FLOAT32> p{{r.v[0], r.v[1]}};
+    fix_pack<RINGSIM_FLOAT32, LK>(p, c, cols);
+    unpack<RINGSIM_FLOAT32>(p, f);
   } else {
-    unpack<DT>(load_pack<DT>(static_cast<const typename OpElem<DT>::T*>(w) + c, n), f);
+    Pack<DT> p;
+    p.v[0] = r.v[0];
+    fix_pack<DT, LK>(p, c, cols);
+    unpack<DT>(p, f);
   }
 }
 

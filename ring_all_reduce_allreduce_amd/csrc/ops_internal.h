@@ -20,6 +20,10 @@ inline int op_dtype_size(int dtype) {
   }
 }
 
+// A call that moves more than the 256 MiB of the Infinity Cache reads its
+// inputs non-temporally: nothing of them will be found there again.
+constexpr int64_t kStreamBytes = 256ll << 20;
+
 // A [outer, inner, cols] tensor: row r is at p + (r / inner) * s0 + (r % inner) * s1 elements.
 struct RowsIn {
   const void* p;
@@ -71,21 +75,36 @@ hipError_t launch_rms_norm_weight_sum(const float* partial, int parts, int cols,
 
 // A launch's tensors and the tiles they are cut into: tensor i holds tiles
 // [tile0[i], tile0[i + 1]) of kGradTileBytes each, its last one shorter.
-// The table travels as a kernel argument (below 4 KiB), which a graph's
-// capture keeps by itself.
+// Tables travel as kernel arguments (below 4 KiB), which a graph's capture
+// keeps by itself.
 constexpr int kGradTileBytes = 16384;
-constexpr int kGradTensors = 128;
-constexpr int kGradWorkgroups = 2048;  // most of a launch
+constexpr int kGradWorkgroups = 1024;  // most of a launch
+constexpr int kGradSquareTensors = 280;
+constexpr int kGradScaleTensors = 180;
+
+// Type and last tile of a tensor in 16 bits.
+enum GradType : int { kGradF32 = 0, kGradBF16 = 1, kGradF16 = 2 };
+constexpr int grad_type(int dtype) {
+  return dtype == RINGSIM_FLOAT32 ? kGradF32 : dtype == RINGSIM_BFLOAT16 ? kGradBF16 : kGradF16;
+}
+constexpr int kGradLastBits = 14;  // elements of a tensor's last tile: up to 8192
+
+template <int N>
 struct GradTable {
-  const void* in[kGradTensors];
-  void* out[kGradTensors];         // norm: unused
-  uint32_t tile0[kGradTensors + 1];
-  uint16_t last[kGradTensors];     // elements of the tensor's last tile
-  uint8_t dtype[kGradTensors];
+  static constexpr int kTensors = N;
+  const void* in[N];
+  uint32_t tile0[N + 1];
+  uint32_t meta[N / 2];  // two tensors a word: GradType << kGradLastBits | elements of the last tile
   int ntensors;
 };
+using GradSquareTable = GradTable<kGradSquareTensors>;
+struct GradScaleTable : GradTable<kGradScaleTensors> {
+  void* out[kGradScaleTensors];
+};
+static_assert(sizeof(GradSquareTable) <= 4000 && sizeof(GradScaleTable) <= 4000, "kernel arguments");
 
-hipError_t launch_grad_squares(const GradTable& t, double* partial, int workgroups, hipStream_t s);
+// The last `keep` tiles are read so that they stay in the Infinity Cache.
+hipError_t launch_grad_squares(const GradSquareTable& t, uint32_t keep, double* partial, int workgroups, hipStream_t s);
 hipError_t launch_grad_norm_join(const double* partial, int parts, float scale, float* norm, hipStream_t s);
 struct GradFactor {
   const double* partial;  // join these into the norm, or
@@ -93,6 +112,6 @@ struct GradFactor {
   float* norm;            // partial null: read the norm here; else workgroup 0 writes it here, if not null
   float scale, max_norm, eps;
 };
-hipError_t launch_grad_scale(const GradTable& t, const GradFactor& f, int in_place, int workgroups, hipStream_t s);
+hipError_t launch_grad_scale(const GradScaleTable& t, const GradFactor& f, int in_place, int workgroups, hipStream_t s);
 
 }  // namespace ringsim

@@ -98,38 +98,46 @@ bool valid_grads(int n, const void* const* grads, void* const* outs, const int64
 
 // Fills a table with the next tensors of the list that hold elements,
 // beginning with *next; advances *next. Returns the tiles in it.
-uint32_t fill_table(GradTable& t, int n, const void* const* grads, void* const* outs, const int64_t* counts,
-                    const int* dtypes, int* next) {
+template <typename TABLE>
+uint32_t fill_table(TABLE& t, int n, const void* const* grads, const int64_t* counts, const int* dtypes, int* next,
+                    int* index) {
   uint32_t tiles = 0;
   t.ntensors = 0;
   t.tile0[0] = 0;
-  for (; *next < n && t.ntensors < kGradTensors; ++*next) {
+  for (; *next < n && t.ntensors < TABLE::kTensors; ++*next) {
     const int i = *next;
     if (counts[i] == 0) continue;
     const int64_t k = tiles_of(counts[i], dtypes[i]);
+    const int64_t last = counts[i] - (k - 1) * (kGradTileBytes / op_dtype_size(dtypes[i]));
     const int j = t.ntensors++;
     t.in[j] = grads[i];
-    t.out[j] = outs ? outs[i] : const_cast<void*>(grads[i]);
-    t.dtype[j] = (uint8_t)dtypes[i];
-    t.last[j] = (uint16_t)(counts[i] - (k - 1) * (kGradTileBytes / op_dtype_size(dtypes[i])));
+    const uint32_t meta = (uint32_t)grad_type(dtypes[i]) << kGradLastBits | (uint32_t)last;
+    t.meta[j / 2] = j % 2 ? t.meta[j / 2] | meta << 16 : meta;
     tiles += (uint32_t)k;
     t.tile0[j + 1] = tiles;
+    if (index) index[j] = i;
   }
   return tiles;
 }
 
 int grad_workgroups(uint32_t tiles) { return (int)std::min<uint32_t>(tiles, kGradWorkgroups); }
 
-// Sums of squares of every launch's workgroups into the workspace.
+// Sums of squares of every launch's workgroups into the workspace. `keep`
+// bytes at the end are read so that they stay in the Infinity Cache.
 ringsim_result_t enqueue_squares(int n, const void* const* grads, const int64_t* counts, const int* dtypes,
-                                 double* partial, int* parts, hipStream_t s) {
+                                 int64_t keep, double* partial, int* parts, hipStream_t s) {
   *parts = 0;
+  int64_t left = 0;  // tiles of the whole list that are still to come
+  for (int i = 0; i < n; ++i) left += tiles_of(counts[i], dtypes[i]);
+  keep /= kGradTileBytes;
   for (int next = 0; next < n;) {
-    GradTable t;
-    const uint32_t tiles = fill_table(t, n, grads, nullptr, counts, dtypes, &next);
+    GradSquareTable t;
+    const uint32_t tiles = fill_table(t, n, grads, counts, dtypes, &next, nullptr);
     if (tiles == 0) continue;  // the rest of the list was empty
+    left -= tiles;
     const int g = grad_workgroups(tiles);
-    if (launch_grad_squares(t, partial + *parts, g, s) != hipSuccess) return RINGSIM_UNHANDLED_DEVICE_ERROR;
+    const uint32_t here = (uint32_t)std::min<int64_t>(tiles, std::max<int64_t>(0, keep - left));
+    if (launch_grad_squares(t, here, partial + *parts, g, s) != hipSuccess) return RINGSIM_UNHANDLED_DEVICE_ERROR;
     *parts += g;
   }
   return RINGSIM_SUCCESS;
@@ -138,9 +146,11 @@ ringsim_result_t enqueue_squares(int n, const void* const* grads, const int64_t*
 ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* outs, const int64_t* counts,
                                const int* dtypes, GradFactor f, hipStream_t s) {
   for (int next = 0; next < n;) {
-    GradTable t;
-    const uint32_t tiles = fill_table(t, n, grads, outs, counts, dtypes, &next);
-    if (tiles == 0) continue;  // the rest of the list was empty
+    GradScaleTable t;
+    int index[kGradScaleTensors];
+    const uint32_t tiles = fill_table(t, n, grads, counts, dtypes, &next, index);
+    if (tiles == 0) continue;
+    for (int j = 0; j < t.ntensors; ++j) t.out[j] = outs ? outs[index[j]] : const_cast<void*>(grads[index[j]]);
     if (launch_grad_scale(t, f, outs == nullptr, grad_workgroups(tiles), s) != hipSuccess)
       return RINGSIM_UNHANDLED_DEVICE_ERROR;
     if (f.partial) f.norm = nullptr;  // the first launch writes it
@@ -149,8 +159,12 @@ ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* out
 }
 
 size_t norm_workspace(int n) {
-  return sizeof(double) * kGradWorkgroups * (size_t)((n + kGradTensors - 1) / kGradTensors);
+  return sizeof(double) * kGradWorkgroups * (size_t)((n + kGradSquareTensors - 1) / kGradSquareTensors);
 }
+
+// What a pass over the gradients may leave for the next one in the Infinity
+// Cache of 256 MiB.
+constexpr int64_t kGradKeepBytes = 192ll << 20;
 
 bool valid_factor(float scale, float max_norm, float eps) {
   return std::isfinite(scale) && std::isfinite(max_norm) && max_norm >= 0.0f && std::isfinite(eps) && eps >= 0.0f;
@@ -278,7 +292,7 @@ ringsim_result_t ringsim_grad_norm(int ntensors, const void* const* grads, const
   hipStream_t s = static_cast<hipStream_t>(stream);
   double* const partial = static_cast<double*>(workspace);
   int parts = 0;
-  const ringsim_result_t res = enqueue_squares(ntensors, grads, counts, dtypes, partial, &parts, s);
+  const ringsim_result_t res = enqueue_squares(ntensors, grads, counts, dtypes, kGradKeepBytes, partial, &parts, s);
   if (res != RINGSIM_SUCCESS) return res;
   return result_of(launch_grad_norm_join(partial, parts, scale, norm, s));
 }
@@ -307,7 +321,7 @@ ringsim_result_t ringsim_clip_grads(int ntensors, const void* const* grads, void
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < norm_workspace(ntensors))
     return RINGSIM_INVALID_ARGUMENT;
   int parts = 0;
-  ringsim_result_t res = enqueue_squares(ntensors, grads, counts, dtypes, partial, &parts, s);
+  ringsim_result_t res = enqueue_squares(ntensors, grads, counts, dtypes, kGradKeepBytes, partial, &parts, s);
   if (res != RINGSIM_SUCCESS) return res;
   const GradFactor f{partial, parts, norm, scale, max_norm, eps};
   return enqueue_scale(ntensors, grads, outs, counts, dtypes, f, s);

@@ -11,7 +11,7 @@
 
 namespace ringsim {
 
-template <int DT, int TPR, int NP, bool Q>
+template <int DT, int TPR, int NP, bool Q, int LK>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNormArgs a) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR;
   constexpr int kRows = kBlock / TPR;  // rows of a workgroup at a time
@@ -20,42 +20,38 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNorm
   __shared__ uint32_t tops[2][16];
   int turn = 0, qturn = 0;
   const int t = threadIdx.x % TPR;
-  float w[NP][kPack];
+  WeightPack w[NP];
 #pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const int c = (k * TPR + t) * kPack;
-    load_weight<DT>(a.weight, a.weight_kind, c, a.cols - c, w[k]);
-  }
-  for (uint32_t row = blockIdx.x * kRows + threadIdx.x / TPR; row < a.rows; row += gridDim.x * kRows) {
+  for (int k = 0; k < NP; ++k) w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * TPR + t) * kPack, a.cols);
+  const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kRows + threadIdx.x / TPR;
+  if (row < a.rows) {
     const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
     float h[NP][kPack];
     Pack<DT> x[NP], res[NP];
     const T* px = row_ptr<DT>(a.x, o, in);
 #pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int c = (k * TPR + t) * kPack;
-      x[k] = load_pack<DT>(px + c, a.cols - c);
-    }
+    for (int k = 0; k < NP; ++k) x[k] = load_pack<DT, LK>(px, (k * TPR + t) * kPack, a.cols);
     if (a.residual.p) {
       const T* pr = row_ptr<DT>(a.residual, o, in);
 #pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int c = (k * TPR + t) * kPack;
-        res[k] = load_pack<DT>(pr + c, a.cols - c);
-      }
+      for (int k = 0; k < NP; ++k) res[k] = load_pack<DT, LK>(pr, (k * TPR + t) * kPack, a.cols);
     }
 #pragma unroll
-    for (int k = 0; k < NP; ++k) unpack<DT>(x[k], h[k]);
+    for (int k = 0; k < NP; ++k) {
+      fix_pack<DT, LK>(x[k], (k * TPR + t) * kPack, a.cols);
+      unpack<DT>(x[k], h[k]);
+    }
     if (a.residual.p) {
       T* ph = row_ptr<T>(a.residual_out, o, in);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const int c = (k * TPR + t) * kPack;
         float f[kPack];
+        fix_pack<DT, LK>(res[k], c, a.cols);
         unpack<DT>(res[k], f);
 #pragma unroll
         for (int i = 0; i < kPack; ++i) h[k][i] += f[i];
-        store_pack<DT>(ph + c, to_pack<DT>(h[k]), a.cols - c);
+        store_pack<DT>(ph, to_pack<DT>(h[k]), c, a.cols);
       }
     }
     float ss = 0.0f;
@@ -68,15 +64,17 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNorm
     const float r = rsqrtf(__builtin_fmaf(ss, a.inv_cols, a.eps));
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
+      float fw[kPack];
+      unpack_weight<DT, LK>(w[k], a.weight_kind, (k * TPR + t) * kPack, a.cols, fw);
 #pragma unroll
-      for (int i = 0; i < kPack; ++i) h[k][i] = h[k][i] * r * w[k][i];
+      for (int i = 0; i < kPack; ++i) h[k][i] = h[k][i] * r * fw[i];
     }
     if constexpr (!Q) {
       T* py = row_ptr<T>(a.out, o, in);
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const int c = (k * TPR + t) * kPack;
-        store_pack<DT>(py + c, to_pack<DT>(h[k]), a.cols - c);
+        store_pack<DT>(py, to_pack<DT>(h[k]), c, a.cols);
       }
     } else {
       // Largest |y| of the row, or of the 4, 8 or 16 lanes that hold a group
@@ -155,21 +153,29 @@ RowShape norm_shape(int64_t rows, int64_t cols) {
   return {1024, 4};
 }
 
-template <int DT, int TPR, int NP>
-static hipError_t launch_shape(const RmsNormArgs& a, hipStream_t s) {
+template <int DT, int TPR, int NP, int LK>
+static hipError_t launch_kind(const RmsNormArgs& a, hipStream_t s) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR;
   constexpr int kRows = kBlock / TPR;
   const int64_t need = ((int64_t)a.rows + kRows - 1) / kRows;
-  const dim3 grid((unsigned)std::min<int64_t>(need, (int64_t)kComputeUnits * (2048 / kBlock))), block(kBlock);
+  const unsigned gx = (unsigned)std::min<int64_t>(need, 1 << 20); const dim3 grid(gx, (unsigned)((need + gx - 1) / gx)), block(kBlock);
   if (a.scales)
-    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, true, LK>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, false, LK>), grid, block, 0, s, a);
   return hipGetLastError();
+}
+
+template <int DT, int TPR, int NP>
+static hipError_t launch_shape(const RmsNormArgs& a, hipStream_t s) {
+  const int64_t bytes = (int64_t)a.rows * a.cols * (int64_t)sizeof(typename OpElem<DT>::T) * (a.residual.p ? 4 : 2);
+  return bytes > kStreamBytes ? launch_kind<DT, TPR, NP, kLoadStream>(a, s)
+                              : launch_kind<DT, TPR, NP, kLoadCached>(a, s);
 }
 
 template <int DT>
 static hipError_t launch_type(const RmsNormArgs& a, hipStream_t s) {
+  if (a.cols < kPack) return launch_kind<DT, 16, 1, kLoadShort>(a, s);
   const RowShape sh = norm_shape(a.rows, a.cols);
   switch (sh.lanes * 16 + sh.packs) {
     case 16 * 16 + 1: return launch_shape<DT, 16, 1>(a, s);

@@ -15,7 +15,7 @@
 
 namespace ringsim {
 
-template <int DT, int TPR, int NP>
+template <int DT, int TPR, int NP, int LK>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kernel(RmsNormBackwardArgs a) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR;
   constexpr int kRows = kBlock / TPR;
@@ -25,9 +25,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kerne
   __shared__ float dws[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * NP * kPack : 1];
   const int t = threadIdx.x % TPR;
   int turn_hh = 0, turn_gh = 0;
+  WeightPack w[NP];
   float dw[NP][kPack];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
+    w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * TPR + t) * kPack, a.cols);
 #pragma unroll
     for (int i = 0; i < kPack; ++i) dw[k][i] = 0.0f;
   }
@@ -39,25 +41,24 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kerne
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c = (k * TPR + t) * kPack;
-      dy[k] = load_pack<DT>(pdy + c, a.cols - c);
-      h[k] = load_pack<DT>(ph + c, a.cols - c);
+      dy[k] = load_pack<DT, LK>(pdy, c, a.cols);
+      h[k] = load_pack<DT, LK>(ph, c, a.cols);
     }
     if (a.grad_residual.p) {
       const T* pr = row_ptr<DT>(a.grad_residual, o, in);
 #pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int c = (k * TPR + t) * kPack;
-        res[k] = load_pack<DT>(pr + c, a.cols - c);
-      }
+      for (int k = 0; k < NP; ++k) res[k] = load_pack<DT, LK>(pr, (k * TPR + t) * kPack, a.cols);
     }
     float g[NP][kPack], hh = 0.0f, gh = 0.0f;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c = (k * TPR + t) * kPack;
       float fh[kPack], fw[kPack];
+      fix_pack<DT, LK>(h[k], c, a.cols);
+      fix_pack<DT, LK>(dy[k], c, a.cols);
       unpack<DT>(h[k], fh);
       unpack<DT>(dy[k], g[k]);
-      load_weight<DT>(a.weight, a.weight_kind, c, a.cols - c, fw);
+      unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
 #pragma unroll
       for (int i = 0; i < kPack; ++i) {
         g[k][i] *= fw[i];
@@ -83,11 +84,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kerne
       }
       if (a.grad_residual.p) {
         float fr[kPack];
+        fix_pack<DT, LK>(res[k], c, a.cols);
         unpack<DT>(res[k], fr);
 #pragma unroll
         for (int i = 0; i < kPack; ++i) g[k][i] += fr[i];
       }
-      store_pack<DT>(pout + c, to_pack<DT>(g[k]), a.cols - c);
+      store_pack<DT>(pout, to_pack<DT>(g[k]), c, a.cols);
     }
   }
   if (!a.partial) return;
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kerne
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c = (k * TPR + t) * kPack;
-      store_pack<RINGSIM_FLOAT32>(reinterpret_cast<uint32_t*>(part) + c, to_pack<RINGSIM_FLOAT32>(dw[k]), a.cols - c);
+      store_pack<RINGSIM_FLOAT32>(part, to_pack<RINGSIM_FLOAT32>(dw[k]), c, a.cols);
     }
   } else {
     float* mine = dws[threadIdx.x / TPR];
@@ -168,15 +170,24 @@ int norm_backward_workgroups(int64_t rows, int64_t cols) {
   return (int)std::max<int64_t>(1, std::min(most, (rows + at_once - 1) / at_once));
 }
 
-template <int DT, int TPR, int NP>
-static hipError_t launch_shape(const RmsNormBackwardArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((rms_norm_backward_kernel<DT, TPR, NP>), dim3(norm_backward_workgroups(a.rows, a.cols)),
+template <int DT, int TPR, int NP, int LK>
+static hipError_t launch_kind(const RmsNormBackwardArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((rms_norm_backward_kernel<DT, TPR, NP, LK>), dim3(norm_backward_workgroups(a.rows, a.cols)),
                      dim3(TPR < 256 ? 256 : TPR), 0, s, a);
   return hipGetLastError();
 }
 
+template <int DT, int TPR, int NP>
+static hipError_t launch_shape(const RmsNormBackwardArgs& a, hipStream_t s) {
+  const int64_t bytes =
+      (int64_t)a.rows * a.cols * (int64_t)sizeof(typename OpElem<DT>::T) * (a.grad_residual.p ? 4 : 3);
+  return bytes > kStreamBytes ? launch_kind<DT, TPR, NP, kLoadStream>(a, s)
+                              : launch_kind<DT, TPR, NP, kLoadCached>(a, s);
+}
+
 template <int DT>
 static hipError_t launch_type(const RmsNormBackwardArgs& a, hipStream_t s) {
+  if (a.cols < kPack) return launch_kind<DT, 16, 1, kLoadShort>(a, s);
   const RowShape sh = norm_backward_shape(a.rows, a.cols);
   switch (sh.lanes * 16 + sh.packs) {
     case 16 * 16 + 1: return launch_shape<DT, 16, 1>(a, s);
