@@ -128,8 +128,9 @@ typedef struct {
 ringsim_result_t ringsim_rms_norm_backward(const ringsim_rms_norm_backward_t* args, ringsim_stream_t stream);
 
 /* Bytes of workspace ringsim_rms_norm_backward needs for `rows` = outer *
- * inner rows of `cols` elements when it writes grad_weight. Host only. */
-ringsim_result_t ringsim_rms_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
+ * inner rows of `cols` elements of `dtype` when it writes grad_weight (0 for
+ * few rows). Host only. */
+ringsim_result_t ringsim_rms_norm_backward_workspace(int64_t rows, int64_t cols, int dtype, size_t* bytes);
 
 /* The 2-norm of `ntensors` gradients together,
  *     *norm = |scale| * sqrt(sum over all elements of grad^2)
@@ -140,14 +141,15 @@ ringsim_result_t ringsim_rms_norm_backward_workspace(int64_t rows, int64_t cols,
  * a summing collective, 1 / the loss scale. Squares are summed in fp64, so
  * that neither large nor small values are lost; the result of no elements is
  * 0. A sharded gradient's norm takes the shards of all ranks in one call.
- * workspace: ringsim_grad_norm_workspace(ntensors) bytes of device memory,
- * 16-byte aligned. */
+ * workspace: ringsim_grad_norm_workspace bytes of device memory, 16-byte
+ * aligned. */
 ringsim_result_t ringsim_grad_norm(int ntensors, const void* const* grads, const int64_t* counts, const int* dtypes,
                                    float scale, float* norm, void* workspace, size_t workspace_bytes,
                                    ringsim_stream_t stream);
 
-/* Bytes of workspace ringsim_grad_norm and ringsim_clip_grads need. Host only. */
-ringsim_result_t ringsim_grad_norm_workspace(int ntensors, size_t* bytes);
+/* Bytes of workspace ringsim_grad_norm and ringsim_clip_grads need for a list
+ * (0 for short ones). Host only. */
+ringsim_result_t ringsim_grad_norm_workspace(int ntensors, const int64_t* counts, const int* dtypes, size_t* bytes);
 
 /* Scales gradients by what a norm known to the device leaves of them,
  *     outs[i] = grads[i] * scale * min(1, max_norm / (*norm + eps))

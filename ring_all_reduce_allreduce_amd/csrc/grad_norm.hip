@@ -15,7 +15,6 @@
 
 namespace ringsim {
 
-constexpr int kWaves = kThreads / 64;
 
 struct GradTile {
   int tensor;
@@ -54,13 +53,15 @@ struct TileFinder {
   }
 };
 
-// A tile in registers: four 16-byte vectors a thread, whatever the type.
+// A tile in registers: four 16-byte vectors a thread of 256, whatever the type.
 constexpr int kTileVecs = kGradTileBytes / 16 / kThreads;
 struct TileData {
   u32x4 v[kTileVecs];
 };
 
-__device__ __forceinline__ int vec_at(int i) { return (i * kThreads + (int)threadIdx.x) * 16; }
+constexpr int kWaves = kThreads / 64;
+__device__ __forceinline__ int tile_thread() { return (int)(threadIdx.x % kThreads); }
+__device__ __forceinline__ int vec_at(int i) { return (i * kThreads + tile_thread()) * 16; }
 
 template <int LK>
 __device__ __forceinline__ TileData load_tile(const char* tile, int bytes) {
@@ -76,30 +77,14 @@ __device__ __forceinline__ void fix_tile(TileData& d, int bytes) {
 }
 
 template <int DT>
-__device__ __forceinline__ void vec_to_f32(u32x4 v, float* f) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if constexpr (DT == RINGSIM_FLOAT32) {
-      f[j] = __uint_as_float(v[j]);
-    } else if constexpr (DT == RINGSIM_BFLOAT16) {
-      f[2 * j] = bf16_lo(v[j]);
-      f[2 * j + 1] = bf16_hi(v[j]);
-    } else {
-      f[2 * j] = elem_to_f32<DT>((uint16_t)(v[j] & 0xffffu));
-      f[2 * j + 1] = elem_to_f32<DT>((uint16_t)(v[j] >> 16));
-    }
-  }
-}
-
-template <int DT>
 __device__ __forceinline__ double tile_squares(const TileData& d) {
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < kTileVecs; ++i) {
-    float f[OpElem<DT>::kPerVec];
-    vec_to_f32<DT>(d.v[i], f);
+    float f[OpElem<DT>::kPack];
+    unpack<DT>(d.v[i], f);
 #pragma unroll
-    for (int j = 0; j < OpElem<DT>::kPerVec; ++j) s = __builtin_fma((double)f[j], (double)f[j], s);
+    for (int j = 0; j < OpElem<DT>::kPack; ++j) s = __builtin_fma((double)f[j], (double)f[j], s);
   }
   return s;
 }
@@ -117,6 +102,13 @@ __device__ __forceinline__ float grad_elem(const void* p, int type, int i) {
   if (type == kGradF32) return static_cast<const float*>(p)[i];
   const uint16_t e = static_cast<const uint16_t*>(p)[i];
   return type == kGradBF16 ? elem_to_f32<RINGSIM_BFLOAT16>(e) : elem_to_f32<RINGSIM_FLOAT16>(e);
+}
+
+// The squares of a tensor shorter than a vector, one element a thread.
+__device__ __forceinline__ double small_squares(const void* in, const GradTile& g) {
+  const int i = tile_thread(), n = g.bytes / (g.type == kGradF32 ? 4 : 2);
+  const double e = i < n ? (double)grad_elem(in, g.type, i) : 0.0;
+  return e * e;
 }
 
 // The squares of tiles t, t + step, ... below `end`; t is left at the first
@@ -138,11 +130,7 @@ __device__ __forceinline__ double walk_squares(const GradSquareTable& tab, const
     return load_tile<LK>(p, real ? g.bytes : 16);
   };
   const auto squares = [&](TileData& d, const GradTile& g) {
-    if (g.small) {
-      const int i = threadIdx.x, n = g.bytes / (g.type == kGradF32 ? 4 : 2);
-      const double e = i < n ? (double)grad_elem(tab.in[g.tensor], g.type, i) : 0.0;
-      return e * e;
-    }
+    if (g.small) return small_squares(tab.in[g.tensor], g);
     if (g.bytes != kGradTileBytes) fix_tile(d, g.bytes);
     return squares_of(d, g.type);
   };
@@ -163,7 +151,9 @@ __device__ __forceinline__ double walk_squares(const GradSquareTable& tab, const
   }
 }
 
-// Sum over the workgroup, known to every thread; the order is fixed.
+// Sum over a workgroup of `WAVES` waves, known to every thread; the order is
+// fixed.
+template <int WAVES>
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
   for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m, 64);
@@ -171,7 +161,7 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   __syncthreads();
   v = lds[0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) v += lds[i];
+  for (int i = 1; i < WAVES; ++i) v += lds[i];
   return v;
 }
 
@@ -183,8 +173,12 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t t = blockIdx.x;
   double s = walk_squares<kLoadStream>(tab, finder, t, tiles - keep, gridDim.x, partial);
   s += walk_squares<kLoadCached>(tab, finder, t, tiles, gridDim.x, partial);
-  s = block_sum(s, lds);
+  s = block_sum<kWaves>(s, lds);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+__device__ __forceinline__ float norm_of(double squares, float scale) {
+  return (float)(__builtin_fabs((double)scale) * __builtin_sqrt(squares));
 }
 
 // The norm from the workgroups' sums, in fp32, known to every thread.
@@ -200,8 +194,8 @@ __device__ __forceinline__ float join_norm(const double* partial, int parts, flo
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) s += v[i];
   }
-  s = block_sum(s, lds);
-  return (float)(__builtin_fabs((double)scale) * __builtin_sqrt(s));
+  s = block_sum<kWaves>(s, lds);
+  return norm_of(s, scale);
 }
 
 __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* partial, int parts, float scale,
@@ -215,23 +209,41 @@ template <int DT>
 __device__ __forceinline__ void tile_scale(const TileData& d, int bytes, char* out, float factor) {
 #pragma unroll
   for (int i = 0; i < kTileVecs; ++i) {
-    float f[OpElem<DT>::kPerVec];
-    vec_to_f32<DT>(d.v[i], f);
+    float f[OpElem<DT>::kPack];
+    unpack<DT>(d.v[i], f);
 #pragma unroll
-    for (int j = 0; j < OpElem<DT>::kPerVec; ++j) f[j] *= factor;
-    u32x4 v;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (DT == RINGSIM_FLOAT32) {
-        v[j] = __float_as_uint(f[j]);
-      } else if constexpr (DT == RINGSIM_BFLOAT16) {
-        v[j] = to_bf16x2(f[2 * j], f[2 * j + 1]);
-      } else {
-        v[j] = (uint32_t)f32_to_elem<DT>(f[2 * j]) | (uint32_t)f32_to_elem<DT>(f[2 * j + 1]) << 16;
-      }
-    }
-    store16(out, v, vec_at(i), bytes);
+    for (int j = 0; j < OpElem<DT>::kPack; ++j) f[j] *= factor;
+    store16<true>(out, to_pack<DT>(f), vec_at(i), bytes);
   }
+}
+
+// Writes a tile in registers, scaled.
+__device__ __forceinline__ void scale_tile(const TileData& d, const GradTile& g, const void* in, void* out, float f) {
+  if (g.small) {
+    const int i = tile_thread();
+    if (i >= g.bytes / (g.type == kGradF32 ? 4 : 2)) return;
+    const float e = grad_elem(in, g.type, i) * f;
+    if (g.type == kGradF32)
+      static_cast<float*>(out)[i] = e;
+    else
+      static_cast<uint16_t*>(out)[i] =
+          g.type == kGradBF16 ? f32_to_elem<RINGSIM_BFLOAT16>(e) : f32_to_elem<RINGSIM_FLOAT16>(e);
+    return;
+  }
+  char* to = static_cast<char*>(out) + g.first;
+  switch (g.type) {
+    case kGradF32: tile_scale<RINGSIM_FLOAT32>(d, g.bytes, to, f); break;
+    case kGradBF16: tile_scale<RINGSIM_BFLOAT16>(d, g.bytes, to, f); break;
+    default: tile_scale<RINGSIM_FLOAT16>(d, g.bytes, to, f); break;
+  }
+}
+
+// What the gradients are multiplied with: one rounding, of the whole factor.
+// A NaN norm fails the comparison and stays.
+__device__ __forceinline__ float factor_of(float norm, const GradFactor& fac) {
+  double c = (double)fac.max_norm / ((double)norm + (double)fac.eps);
+  c = c > 1.0 ? 1.0 : c;
+  return (float)(c * (double)fac.scale);
 }
 
 // Walks the tiles from the last to the first: what the norm's pass read last
@@ -246,36 +258,61 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(GradScaleTable tab
   } else {
     norm = *fac.norm;
   }
-  // One rounding, of the whole factor. A NaN norm fails the comparison and
-  // stays.
-  double c = (double)fac.max_norm / ((double)norm + (double)fac.eps);
-  c = c > 1.0 ? 1.0 : c;
-  const float f = (float)(c * (double)fac.scale);
+  const float f = factor_of(norm, fac);
   if (in_place && f == 1.0f) return;
   const uint32_t tiles = tab.tile0[tab.ntensors];
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const GradTile g = finder.find(tab, tiles - 1 - t);
     const void* in = tab.in[g.tensor];
-    void* out = tab.out[g.tensor];
-    if (g.small) {
-      const int i = threadIdx.x;
-      if (i >= g.bytes / (g.type == kGradF32 ? 4 : 2)) continue;
-      const float e = grad_elem(in, g.type, i) * f;
-      if (g.type == kGradF32)
-        static_cast<float*>(out)[i] = e;
-      else
-        static_cast<uint16_t*>(out)[i] =
-            g.type == kGradBF16 ? f32_to_elem<RINGSIM_BFLOAT16>(e) : f32_to_elem<RINGSIM_FLOAT16>(e);
+    TileData d;
+    if (!g.small) {
+      d = load_tile<kLoadStream>(static_cast<const char*>(in) + g.first, g.bytes);
+      if (g.bytes != kGradTileBytes) fix_tile(d, g.bytes);
+    }
+    scale_tile(d, g, in, tab.out[g.tensor], f);
+  }
+}
+
+// Norm and scaling of a list of at most kGradSmallTiles tiles by one
+// workgroup: every tile is read once and stays in registers until it is
+// scaled, and there is one launch instead of two. TODO
+__global__ void __launch_bounds__(kGradSmallThreads)
+    grad_small_kernel(GradSmallTable tab, GradFactor fac, int clip, int in_place) {
+  constexpr int kGroups = kGradSmallThreads / kThreads, kRounds = kGradSmallTiles / kGroups;
+  __shared__ double lds[kGradSmallThreads / 64];
+  const uint32_t tiles = tab.tile0[tab.ntensors];
+  const TileFinder<GradSmallTable> finder(tab);
+  const uint32_t group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+  TileData d[kRounds];
+  GradTile g[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const uint32_t t = group + k * kGroups;
+    if (t >= tiles) continue;
+    g[k] = finder.find(tab, t);
+    if (!g[k].small) d[k] = load_tile<kLoadCached>(static_cast<const char*>(tab.in[g[k].tensor]) + g[k].first, g[k].bytes);
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    if (group + k * kGroups >= tiles) continue;
+    if (g[k].small) {
+      s += small_squares(tab.in[g[k].tensor], g[k]);
       continue;
     }
-    TileData d = load_tile<kLoadStream>(static_cast<const char*>(in) + g.first, g.bytes);
-    if (g.bytes != kGradTileBytes) fix_tile(d, g.bytes);
-    char* to = static_cast<char*>(out) + g.first;
-    switch (g.type) {
-      case kGradF32: tile_scale<RINGSIM_FLOAT32>(d, g.bytes, to, f); break;
-      case kGradBF16: tile_scale<RINGSIM_BFLOAT16>(d, g.bytes, to, f); break;
-      default: tile_scale<RINGSIM_FLOAT16>(d, g.bytes, to, f); break;
-    }
+    if (g[k].bytes != kGradTileBytes) fix_tile(d[k], g[k].bytes);
+    s += squares_of(d[k], g[k].type);
+  }
+  s = block_sum<kGradSmallThreads / 64>(s, lds);
+  const float norm = norm_of(s, fac.scale);
+  if (threadIdx.x == 0) *fac.norm = norm;
+  if (!clip) return;
+  const float f = factor_of(norm, fac);
+  if (in_place && f == 1.0f) return;
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    if (group + k * kGroups >= tiles) continue;
+    scale_tile(d[k], g[k], tab.in[g[k].tensor], tab.out[g[k].tensor], f);
   }
 }
 
@@ -287,6 +324,11 @@ hipError_t launch_grad_squares(const GradSquareTable& t, uint32_t keep, double* 
 
 hipError_t launch_grad_norm_join(const double* partial, int parts, float scale, float* norm, hipStream_t s) {
   hipLaunchKernelGGL(grad_norm_join_kernel, dim3(1), dim3(kThreads), 0, s, partial, parts, scale, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_small(const GradSmallTable& t, const GradFactor& f, int clip, int in_place, hipStream_t s) {
+  hipLaunchKernelGGL(grad_small_kernel, dim3(1), dim3(kGradSmallThreads), 0, s, t, f, clip, in_place);
   return hipGetLastError();
 }
 

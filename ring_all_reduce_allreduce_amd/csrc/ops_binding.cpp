@@ -317,11 +317,13 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) 
         dw = &made_dw;
       }
       size_t bytes = 0;
-      check(ringsim_rms_norm_backward_workspace(a.outer * a.inner, a.cols, &bytes),
+      check(ringsim_rms_norm_backward_workspace(a.outer * a.inner, a.cols, a.dtype, &bytes),
             "ringsim_rms_norm_backward_workspace");
-      workspace = empty({(int64_t)bytes}, at::kByte, device);
+      if (bytes) {
+        workspace = empty({(int64_t)bytes}, at::kByte, device);
+        a.workspace = data(workspace);
+      }
       a.grad_weight = data(*dw);
-      a.workspace = data(workspace);
       a.workspace_bytes = bytes;
     }
     a.grad_out = data(dy);
@@ -392,10 +394,12 @@ float* norm_ptr(PyObject* o, at::Tensor& made, int device) {
   return static_cast<float*>(data(*t));
 }
 
-at::Tensor norm_workspace(int n, size_t* bytes, int device) {
-  check(ringsim_grad_norm_workspace(n, bytes), "ringsim_grad_norm_workspace");
-  return empty({(int64_t)*bytes}, at::kByte, device);
+// The workspace of a list, if it needs one; `bytes` are its size.
+at::Tensor norm_workspace(const GradList& g, size_t* bytes, int device) {
+  check(ringsim_grad_norm_workspace(g.size(), g.counts.data(), g.types.data(), bytes), "ringsim_grad_norm_workspace");
+  return *bytes ? empty({(int64_t)*bytes}, at::kByte, device) : at::Tensor();
 }
+void* address(const at::Tensor& t) { return t.defined() ? data(t) : nullptr; }
 
 // grad_norm(grads, scale, norm)
 PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
@@ -407,8 +411,8 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     at::Tensor made;
     float* norm = norm_ptr(args[2], made, device);
     size_t bytes = 0;
-    const at::Tensor ws = norm_workspace(g.size(), &bytes, device);
-    check(ringsim_grad_norm(g.size(), g.ptrs.data(), g.counts.data(), g.types.data(), scale, norm, data(ws), bytes,
+    const at::Tensor ws = norm_workspace(g, &bytes, device);
+    check(ringsim_grad_norm(g.size(), g.ptrs.data(), g.counts.data(), g.types.data(), scale, norm, address(ws), bytes,
                             current_stream(device)),
           "ringsim_grad_norm");
     return result(args[2], made);
@@ -447,9 +451,9 @@ PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     at::Tensor made;
     float* norm = norm_ptr(args[5], made, device);
     size_t bytes = 0;
-    const at::Tensor ws = norm_workspace(g.size(), &bytes, device);
+    const at::Tensor ws = norm_workspace(g, &bytes, device);
     check(ringsim_clip_grads(g.size(), g.ptrs.data(), o ? o->ptrs.data() : nullptr, g.counts.data(), g.types.data(),
-                             (float)number(args[3]), (float)number(args[1]), (float)number(args[4]), norm, data(ws),
+                             (float)number(args[3]), (float)number(args[1]), (float)number(args[4]), norm, address(ws),
                              bytes, current_stream(device)),
           "ringsim_clip_grads");
     return result(args[5], made);

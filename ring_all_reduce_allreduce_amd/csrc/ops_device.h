@@ -1,5 +1,5 @@
-// ops_device.h -- device building blocks of the step operators: packs of
-// eight elements in registers, rounding to the element types, and sums over
+// ops_device.h -- device building blocks of the step operators: 16-byte packs
+// of elements in registers, rounding to the element types, and sums over
 // lanes and waves.
 #pragma once
 
@@ -15,26 +15,21 @@ typedef u32x4 u32x4_e2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_e2 __attribute__((aligned(2)));
 typedef uint32_t u32_e2 __attribute__((aligned(2)));
 typedef u32x2 u32x2_e1 __attribute__((aligned(1)));
+typedef uint32_t u32_e1 __attribute__((aligned(1)));
 
-constexpr int kPack = 8;  // elements a lane holds side by side: 16 bytes of a 16-bit type, 32 of fp32
-
+// A lane holds 16 bytes side by side, whatever the type, so that a wave's
+// access covers 1024 bytes without gaps. (With 32 bytes a lane for fp32, each
+// non-temporal store left half-written lines: 236 us against TODO for the
+// gradients of 16384 rows of 4096.)
 template <int DT>
 struct OpElem {
   using T = uint16_t;
-  static constexpr int kPerVec = 8;  // elements of a 16-byte vector
-  static constexpr int kVecs = 1;    // vectors of a pack
+  static constexpr int kPack = 8;
 };
 template <>
 struct OpElem<RINGSIM_FLOAT32> {
   using T = uint32_t;
-  static constexpr int kPerVec = 4;
-  static constexpr int kVecs = 2;
-};
-
-// Eight consecutive elements as they lie in memory.
-template <int DT>
-struct Pack {
-  u32x4 v[OpElem<DT>::kVecs];
+  static constexpr int kPack = 4;
 };
 
 template <int DT>
@@ -99,17 +94,21 @@ __device__ __forceinline__ u32x4 fix16(u32x4 v, int at, int bytes) {
   return v;
 }
 
-// Writes what lies below `bytes` of 16 bytes at byte `at`. Whole vectors go
-// out non-temporally: written lines that stay out of the L2s leave them to
+// Writes what lies below `bytes` of 16 bytes at byte `at`. Results go out
+// non-temporally (NT): written lines that stay out of the L2s leave them to
 // the reads. A 64 MiB copy over three buffer sets takes 20.2 us so and 24.5
 // us with plain stores; a kernel that reads the result next takes as much
 // longer as was saved at 32-128 MiB, and less at 512 MiB (272 us for the
 // pair against 294).
+template <bool NT>
 __device__ __forceinline__ void store16(void* p, u32x4 v, int at, int bytes) {
   char* c = static_cast<char*>(p) + at;
   const int left = bytes - at;
   if (left >= 16) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_e2*>(c));
+    if constexpr (NT)
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_e2*>(c));
+    else
+      *reinterpret_cast<u32x4_e2*>(c) = v;
   } else if (left > 0) {
     // 8, 4 and 2 bytes as the rest's length has them.
     if (left & 8) {
@@ -127,68 +126,57 @@ __device__ __forceinline__ void store16(void* p, u32x4 v, int at, int bytes) {
   }
 }
 
+template <int DT>
+__device__ __forceinline__ int byte_of(int element) {
+  return element * (int)sizeof(typename OpElem<DT>::T);
+}
+
 // The pack at element c of a row of `cols`; fix_pack before its elements count.
-template <int DT, int LK = kLoadCached>
-__device__ __forceinline__ Pack<DT> load_pack(const void* row, int c, int cols) {
-  constexpr int kSize = (int)sizeof(typename OpElem<DT>::T);
-  Pack<DT> r;
-#pragma unroll
-  for (int i = 0; i < OpElem<DT>::kVecs; ++i) r.v[i] = load16<LK>(row, c * kSize + 16 * i, cols * kSize);
-  return r;
+template <int DT, int LK>
+__device__ __forceinline__ u32x4 load_pack(const void* row, int c, int cols) {
+  return load16<LK>(row, byte_of<DT>(c), byte_of<DT>(cols));
 }
-
-template <int DT, int LK = kLoadCached>
-__device__ __forceinline__ void fix_pack(Pack<DT>& r, int c, int cols) {
-  constexpr int kSize = (int)sizeof(typename OpElem<DT>::T);
-#pragma unroll
-  for (int i = 0; i < OpElem<DT>::kVecs; ++i) r.v[i] = fix16<LK>(r.v[i], c * kSize + 16 * i, cols * kSize);
+template <int DT, int LK>
+__device__ __forceinline__ u32x4 fix_pack(u32x4 v, int c, int cols) {
+  return fix16<LK>(v, byte_of<DT>(c), byte_of<DT>(cols));
 }
 
 template <int DT>
-__device__ __forceinline__ void store_pack(void* row, const Pack<DT>& r, int c, int cols) {
-  constexpr int kSize = (int)sizeof(typename OpElem<DT>::T);
+__device__ __forceinline__ void unpack(u32x4 v, float* f) {
 #pragma unroll
-  for (int i = 0; i < OpElem<DT>::kVecs; ++i) store16(row, r.v[i], c * kSize + 16 * i, cols * kSize);
-}
-
-template <int DT>
-__device__ __forceinline__ void unpack(const Pack<DT>& r, float* f) {
-#pragma unroll
-  for (int i = 0; i < OpElem<DT>::kVecs; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = r.v[i][j];
-      if constexpr (DT == RINGSIM_FLOAT32) {
-        f[4 * i + j] = __uint_as_float(w);
-      } else if constexpr (DT == RINGSIM_BFLOAT16) {
-        f[2 * j] = bf16_lo(w);
-        f[2 * j + 1] = bf16_hi(w);
-      } else {
-        f[2 * j] = elem_to_f32<DT>((uint16_t)(w & 0xffffu));
-        f[2 * j + 1] = elem_to_f32<DT>((uint16_t)(w >> 16));
-      }
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (DT == RINGSIM_FLOAT32) {
+      f[j] = __uint_as_float(v[j]);
+    } else if constexpr (DT == RINGSIM_BFLOAT16) {
+      f[2 * j] = bf16_lo(v[j]);
+      f[2 * j + 1] = bf16_hi(v[j]);
+    } else {
+      f[2 * j] = elem_to_f32<DT>((uint16_t)(v[j] & 0xffffu));
+      f[2 * j + 1] = elem_to_f32<DT>((uint16_t)(v[j] >> 16));
     }
   }
 }
 
-// Rounds eight floats to the type, to nearest even.
+// Rounds a pack of floats to the type, to nearest even.
 template <int DT>
-__device__ __forceinline__ Pack<DT> to_pack(const float* f) {
-  Pack<DT> r;
+__device__ __forceinline__ u32x4 to_pack(const float* f) {
+  u32x4 v;
 #pragma unroll
-  for (int i = 0; i < OpElem<DT>::kVecs; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (DT == RINGSIM_FLOAT32) {
-        r.v[i][j] = __float_as_uint(f[4 * i + j]);
-      } else if constexpr (DT == RINGSIM_BFLOAT16) {
-        r.v[i][j] = to_bf16x2(f[2 * j], f[2 * j + 1]);
-      } else {
-        r.v[i][j] = (uint32_t)f32_to_elem<DT>(f[2 * j]) | ((uint32_t)f32_to_elem<DT>(f[2 * j + 1]) << 16);
-      }
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (DT == RINGSIM_FLOAT32) {
+      v[j] = __float_as_uint(f[j]);
+    } else if constexpr (DT == RINGSIM_BFLOAT16) {
+      v[j] = to_bf16x2(f[2 * j], f[2 * j + 1]);
+    } else {
+      v[j] = (uint32_t)f32_to_elem<DT>(f[2 * j]) | (uint32_t)f32_to_elem<DT>(f[2 * j + 1]) << 16;
     }
   }
-  return r;
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_pack(void* row, u32x4 v, int c, int cols) {
+  store16<true>(row, v, byte_of<DT>(c), byte_of<DT>(cols));
 }
 
 // ---------------------------------------------------------------------------
@@ -210,6 +198,14 @@ __device__ __forceinline__ V dpp(V v) {
       V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
+// Joins each row of 16 lanes, whose lanes are equal, with its neighbour.
+template <typename OP, typename V>
+__device__ __forceinline__ V swap16_reduce(V v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return OP::of(__builtin_bit_cast(V, (uint32_t)s[0]), __builtin_bit_cast(V, (uint32_t)s[1]));
+}
+
 // The reduction of `LANES` neighbouring lanes (a power of two, 4 to 64),
 // known to each of them. Steps 1, 2, 4, 8 stay inside a row of 16 lanes and
 // are lane permutations of the vector unit (quad permutes, half-row and row
@@ -223,11 +219,7 @@ __device__ __forceinline__ V lanes_reduce(V v) {
   v = OP::of(v, dpp<0x4E>(v));                          // quad_perm [2,3,0,1]
   if constexpr (LANES >= 8) v = OP::of(v, dpp<0x141>(v));   // row_half_mirror
   if constexpr (LANES >= 16) v = OP::of(v, dpp<0x140>(v));  // row_mirror
-  if constexpr (LANES >= 32) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    v = OP::of(__builtin_bit_cast(V, (uint32_t)s[0]), __builtin_bit_cast(V, (uint32_t)s[1]));
-  }
+  if constexpr (LANES >= 32) v = swap16_reduce<OP>(v);
   if constexpr (LANES >= 64) {
     const uint32_t u = __builtin_bit_cast(uint32_t, v);
     const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
@@ -260,6 +252,28 @@ __device__ __forceinline__ V row_reduce(V v, V (*buf)[16], int& turn) {
   return v;
 }
 
+// Two sums over the lanes that hold a row, with one barrier.
+template <int TPR>
+__device__ __forceinline__ void row_reduce2(float& a, float& b, f32x2 (*buf)[16], int& turn) {
+  constexpr int kLanes = TPR < 64 ? TPR : 64;
+  a = lanes_reduce<kLanes, AddF32>(a);
+  b = lanes_reduce<kLanes, AddF32>(b);
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) buf[turn][threadIdx.x >> 6] = f32x2{a, b};
+    __syncthreads();
+    f32x2 v = buf[turn][0];
+    a = v.x;
+    b = v.y;
+#pragma unroll
+    for (int i = 1; i < TPR / 64; ++i) {
+      v = buf[turn][i];
+      a += v.x;
+      b += v.y;
+    }
+    turn ^= 1;
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ const typename OpElem<DT>::T* row_ptr(const RowsIn& t, uint32_t o, uint32_t i) {
   return static_cast<const typename OpElem<DT>::T*>(t.p) + ((int64_t)o * t.s0 + (int64_t)i * t.s1);
@@ -269,7 +283,8 @@ __device__ __forceinline__ T* row_ptr(const RowsOut& t, uint32_t o, uint32_t i) 
   return static_cast<T*>(t.p) + ((int64_t)o * t.s0 + (int64_t)i * t.s1);
 }
 
-// Eight weights as they lie in memory: in the rows' type or in fp32.
+// The weights of a pack as they lie in memory: in the rows' type, or in fp32
+// (twice the bytes of a pack of a 16-bit type).
 struct WeightPack {
   u32x4 v[2];
 };
@@ -283,7 +298,7 @@ __device__ __forceinline__ WeightPack load_weight(const void* w, int kind, int c
   if (kind != kWeightNone) {
     const int size = kind == kWeightF32 ? 4 : kSize;
     r.v[0] = load16<kKind>(w, c * size, cols * size);
-    if (size == 4) r.v[1] = load16<kKind>(w, c * 4 + 16, cols * 4);
+    if (kSize == 2 && size == 4) r.v[1] = load16<kKind>(w, c * 4 + 16, cols * 4);
   }
   return r;
 }
@@ -293,16 +308,13 @@ template <int DT, int LK>
 __device__ __forceinline__ void unpack_weight(const WeightPack& r, int kind, int c, int cols, float* f) {
   if (kind == kWeightNone) {
 #pragma unroll
-    for (int i = 0; i < kPack; ++i) f[i] = 1.0f;
+    for (int i = 0; i < OpElem<DT>::kPack; ++i) f[i] = 1.0f;
   } else if (DT == RINGSIM_FLOAT32 || kind == kWeightF32) {
-    Pack<RINGSIM_FLOAT32> p{{r.v[0], r.v[1]}};
-    fix_pack<RINGSIM_FLOAT32, LK>(p, c, cols);
-    unpack<RINGSIM_FLOAT32>(p, f);
+#pragma unroll
+    for (int i = 0; i < OpElem<DT>::kPack / 4; ++i)
+      unpack<RINGSIM_FLOAT32>(fix_pack<RINGSIM_FLOAT32, LK>(r.v[i], c + 4 * i, cols), f + 4 * i);
   } else {
-    Pack<DT> p;
-    p.v[0] = r.v[0];
-    fix_pack<DT, LK>(p, c, cols);
-    unpack<DT>(p, f);
+    unpack<DT>(fix_pack<DT, LK>(r.v[0], c, cols), f);
   }
 }
 

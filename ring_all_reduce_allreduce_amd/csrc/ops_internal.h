@@ -52,6 +52,8 @@ struct RmsNormBackwardArgs {
   const void* weight;
   RowsOut grad_in;
   float* partial;            // [workgroups, cols] sums of grad_out * h * r; null: not wanted
+  void* grad_weight;         // what a launch of one workgroup writes instead; null: not wanted
+  int weight_dtype;
   uint32_t rows, inner;
   int cols;
   int weight_kind;
@@ -59,13 +61,11 @@ struct RmsNormBackwardArgs {
 };
 
 // How a row is laid over lanes: `lanes` lanes of a workgroup hold a row,
-// `packs` packs of eight elements each.
+// `packs` packs of 16 bytes each.
 struct RowShape {
   int lanes, packs;
 };
-RowShape norm_shape(int64_t rows, int64_t cols);
-RowShape norm_backward_shape(int64_t rows, int64_t cols);
-int norm_backward_workgroups(int64_t rows, int64_t cols);
+int norm_backward_workgroups(int64_t rows, int64_t cols, int dtype);
 
 hipError_t launch_rms_norm(const RmsNormArgs& a, int dtype, hipStream_t s);
 hipError_t launch_rms_norm_backward(const RmsNormBackwardArgs& a, int dtype, hipStream_t s);
@@ -97,10 +97,18 @@ struct GradTable {
   uint32_t meta[N / 2];  // two tensors a word: GradType << kGradLastBits | elements of the last tile
   int ntensors;
 };
+// A list of at most this many tiles is one workgroup's: it keeps them in
+// registers, three for each 256 of its 1024 threads.
+constexpr int kGradSmallTiles = 12;
+constexpr int kGradSmallThreads = 1024;
+
 using GradSquareTable = GradTable<kGradSquareTensors>;
-struct GradScaleTable : GradTable<kGradScaleTensors> {
-  void* out[kGradScaleTensors];
+template <int N>
+struct GradOutTable : GradTable<N> {
+  void* out[N];
 };
+using GradScaleTable = GradOutTable<kGradScaleTensors>;
+using GradSmallTable = GradOutTable<kGradSmallTiles>;
 static_assert(sizeof(GradSquareTable) <= 4000 && sizeof(GradScaleTable) <= 4000, "kernel arguments");
 
 // The last `keep` tiles are read so that they stay in the Infinity Cache.
@@ -112,6 +120,8 @@ struct GradFactor {
   float* norm;            // partial null: read the norm here; else workgroup 0 writes it here, if not null
   float scale, max_norm, eps;
 };
+// Norm and, if `clip`, scaling of a small list in one launch; f.partial is not read.
+hipError_t launch_grad_small(const GradSmallTable& t, const GradFactor& f, int clip, int in_place, hipStream_t s);
 hipError_t launch_grad_scale(const GradScaleTable& t, const GradFactor& f, int in_place, int workgroups, hipStream_t s);
 
 }  // namespace ringsim

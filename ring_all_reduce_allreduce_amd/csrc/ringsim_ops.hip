@@ -120,15 +120,19 @@ uint32_t fill_table(TABLE& t, int n, const void* const* grads, const int64_t* co
   return tiles;
 }
 
+template <typename TABLE>
+void set_outs(TABLE& t, const void* const* grads, void* const* outs, const int* index) {
+  for (int j = 0; j < t.ntensors; ++j) t.out[j] = outs ? outs[index[j]] : const_cast<void*>(grads[index[j]]);
+}
+
 int grad_workgroups(uint32_t tiles) { return (int)std::min<uint32_t>(tiles, kGradWorkgroups); }
 
-// Sums of squares of every launch's workgroups into the workspace. `keep`
-// bytes at the end are read so that they stay in the Infinity Cache.
+// Sums of squares of every launch's workgroups into the workspace. `left`:
+// tiles still to come. `keep` bytes at the end are read so that they stay in
+// the Infinity Cache.
 ringsim_result_t enqueue_squares(int n, const void* const* grads, const int64_t* counts, const int* dtypes,
-                                 int64_t keep, double* partial, int* parts, hipStream_t s) {
+                                 int64_t left, int64_t keep, double* partial, int* parts, hipStream_t s) {
   *parts = 0;
-  int64_t left = 0;  // tiles of the whole list that are still to come
-  for (int i = 0; i < n; ++i) left += tiles_of(counts[i], dtypes[i]);
   keep /= kGradTileBytes;
   for (int next = 0; next < n;) {
     GradSquareTable t;
@@ -150,7 +154,7 @@ ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* out
     int index[kGradScaleTensors];
     const uint32_t tiles = fill_table(t, n, grads, counts, dtypes, &next, index);
     if (tiles == 0) continue;
-    for (int j = 0; j < t.ntensors; ++j) t.out[j] = outs ? outs[index[j]] : const_cast<void*>(grads[index[j]]);
+    set_outs(t, grads, outs, index);
     if (launch_grad_scale(t, f, outs == nullptr, grad_workgroups(tiles), s) != hipSuccess)
       return RINGSIM_UNHANDLED_DEVICE_ERROR;
     if (f.partial) f.norm = nullptr;  // the first launch writes it
@@ -158,8 +162,33 @@ ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* out
   return RINGSIM_SUCCESS;
 }
 
-size_t norm_workspace(int n) {
+// Tiles of the whole list.
+int64_t total_tiles(int n, const int64_t* counts, const int* dtypes) {
+  int64_t tiles = 0;
+  for (int i = 0; i < n; ++i) tiles += tiles_of(counts[i], dtypes[i]);
+  return tiles;
+}
+
+bool is_small(int64_t tiles) { return tiles <= kGradSmallTiles; }
+
+size_t norm_workspace(int n, int64_t tiles) {
+  if (is_small(tiles)) return 0;
   return sizeof(double) * kGradWorkgroups * (size_t)((n + kGradSquareTensors - 1) / kGradSquareTensors);
+}
+
+bool valid_workspace(const void* ws, size_t bytes, int n, int64_t tiles) {
+  const size_t need = norm_workspace(n, tiles);
+  return need == 0 || (ws && aligned(ws, 16) && bytes >= need);
+}
+
+// Norm, and scaling if `clip`, of a list that one workgroup takes.
+ringsim_result_t enqueue_small(int n, const void* const* grads, void* const* outs, const int64_t* counts,
+                               const int* dtypes, const GradFactor& f, bool clip, hipStream_t s) {
+  GradSmallTable t;
+  int next = 0, index[kGradSmallTiles];
+  fill_table(t, n, grads, counts, dtypes, &next, index);
+  set_outs(t, grads, outs, index);
+  return result_of(launch_grad_small(t, f, clip, outs == nullptr, s));
 }
 
 // What a pass over the gradients may leave for the next one in the Infinity
@@ -168,12 +197,6 @@ constexpr int64_t kGradKeepBytes = 192ll << 20;
 
 bool valid_factor(float scale, float max_norm, float eps) {
   return std::isfinite(scale) && std::isfinite(max_norm) && max_norm >= 0.0f && std::isfinite(eps) && eps >= 0.0f;
-}
-
-bool any_elements(int n, const int64_t* counts) {
-  for (int i = 0; i < n; ++i)
-    if (counts[i]) return true;
-  return false;
 }
 
 }  // namespace
@@ -222,10 +245,11 @@ ringsim_result_t ringsim_rms_norm(const ringsim_rms_norm_t* a, ringsim_stream_t 
   return result_of(launch_rms_norm(k, a->dtype, static_cast<hipStream_t>(stream)));
 }
 
-ringsim_result_t ringsim_rms_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes) {
-  if (!bytes || rows < 0 || rows > INT32_MAX || cols < 1 || cols > RINGSIM_NORM_MAX_COLS)
+ringsim_result_t ringsim_rms_norm_backward_workspace(int64_t rows, int64_t cols, int dtype, size_t* bytes) {
+  if (!bytes || !valid_input_type(dtype) || rows < 0 || rows > INT32_MAX || cols < 1 || cols > RINGSIM_NORM_MAX_COLS)
     return RINGSIM_INVALID_ARGUMENT;
-  *bytes = sizeof(float) * (size_t)norm_backward_workgroups(rows, cols) * (size_t)cols;
+  const int g = norm_backward_workgroups(rows, cols, dtype);
+  *bytes = g == 1 ? 0 : sizeof(float) * (size_t)g * (size_t)cols;
   return RINGSIM_SUCCESS;
 }
 
@@ -244,13 +268,14 @@ ringsim_result_t ringsim_rms_norm_backward(const ringsim_rms_norm_backward_t* a,
   if (a->weight && !aligned(a->weight, op_dtype_size(a->weight_dtype))) return RINGSIM_INVALID_ARGUMENT;
   if (a->grad_weight) {
     size_t need = 0;
-    ringsim_rms_norm_backward_workspace(rows, a->cols, &need);
+    ringsim_rms_norm_backward_workspace(rows, a->cols, a->dtype, &need);
     if (!aligned(a->grad_weight, op_dtype_size(a->weight_dtype))) return RINGSIM_INVALID_ARGUMENT;
-    if (rows > 0 && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need))
+    if (need > 0 && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need))
       return RINGSIM_INVALID_ARGUMENT;
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
-  float* const partial = a->grad_weight ? static_cast<float*>(a->workspace) : nullptr;
+  const int g = rows > 0 ? norm_backward_workgroups(rows, a->cols, a->dtype) : 0;
+  float* const partial = a->grad_weight && g > 1 ? static_cast<float*>(a->workspace) : nullptr;
   if (rows > 0) {
     RmsNormBackwardArgs k;
     std::memset(&k, 0, sizeof(k));
@@ -260,6 +285,8 @@ ringsim_result_t ringsim_rms_norm_backward(const ringsim_rms_norm_backward_t* a,
     k.grad_in = rows_out(a->grad_in, a->grad_in_stride);
     k.weight = a->weight;
     k.partial = partial;
+    k.grad_weight = g == 1 ? a->grad_weight : nullptr;
+    k.weight_dtype = a->weight_dtype;
     k.rows = (uint32_t)rows;
     k.inner = (uint32_t)a->inner;
     k.cols = (int)a->cols;
@@ -268,15 +295,16 @@ ringsim_result_t ringsim_rms_norm_backward(const ringsim_rms_norm_backward_t* a,
     k.inv_cols = 1.0f / (float)a->cols;
     if (launch_rms_norm_backward(k, a->dtype, s) != hipSuccess) return RINGSIM_UNHANDLED_DEVICE_ERROR;
   }
-  if (!a->grad_weight) return RINGSIM_SUCCESS;
+  if (!a->grad_weight || g == 1) return RINGSIM_SUCCESS;
   // Without rows the sum runs over no parts and writes zeros.
-  return result_of(launch_rms_norm_weight_sum(partial, rows > 0 ? norm_backward_workgroups(rows, a->cols) : 0,
-                                              (int)a->cols, a->grad_weight, a->weight_dtype, s));
+  return result_of(launch_rms_norm_weight_sum(partial, g, (int)a->cols, a->grad_weight, a->weight_dtype, s));
 }
 
-ringsim_result_t ringsim_grad_norm_workspace(int ntensors, size_t* bytes) {
-  if (!bytes || ntensors < 0) return RINGSIM_INVALID_ARGUMENT;
-  *bytes = norm_workspace(ntensors);
+ringsim_result_t ringsim_grad_norm_workspace(int ntensors, const int64_t* counts, const int* dtypes, size_t* bytes) {
+  if (!bytes || ntensors < 0 || (ntensors > 0 && (!counts || !dtypes))) return RINGSIM_INVALID_ARGUMENT;
+  for (int i = 0; i < ntensors; ++i)
+    if (!valid_input_type(dtypes[i]) || counts[i] < 0 || counts[i] > kMaxElements) return RINGSIM_INVALID_ARGUMENT;
+  *bytes = norm_workspace(ntensors, total_tiles(ntensors, counts, dtypes));
   return RINGSIM_SUCCESS;
 }
 
@@ -286,13 +314,16 @@ ringsim_result_t ringsim_grad_norm(int ntensors, const void* const* grads, const
   const RoctxRange range("ringsim_grad_norm");
   if (!valid_grads(ntensors, grads, nullptr, counts, dtypes) || !std::isfinite(scale) || !norm || !aligned(norm, 4))
     return RINGSIM_INVALID_ARGUMENT;
-  if (any_elements(ntensors, counts) &&
-      (!workspace || !aligned(workspace, 16) || workspace_bytes < norm_workspace(ntensors)))
-    return RINGSIM_INVALID_ARGUMENT;
+  const int64_t tiles = total_tiles(ntensors, counts, dtypes);
+  if (!valid_workspace(workspace, workspace_bytes, ntensors, tiles)) return RINGSIM_INVALID_ARGUMENT;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (is_small(tiles))
+    return enqueue_small(ntensors, grads, nullptr, counts, dtypes, GradFactor{nullptr, 0, norm, scale, 0.0f, 0.0f},
+                         false, s);
   double* const partial = static_cast<double*>(workspace);
   int parts = 0;
-  const ringsim_result_t res = enqueue_squares(ntensors, grads, counts, dtypes, kGradKeepBytes, partial, &parts, s);
+  const ringsim_result_t res =
+      enqueue_squares(ntensors, grads, counts, dtypes, tiles, kGradKeepBytes, partial, &parts, s);
   if (res != RINGSIM_SUCCESS) return res;
   return result_of(launch_grad_norm_join(partial, parts, scale, norm, s));
 }
@@ -316,12 +347,14 @@ ringsim_result_t ringsim_clip_grads(int ntensors, const void* const* grads, void
       !aligned(norm, 4))
     return RINGSIM_INVALID_ARGUMENT;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t tiles = total_tiles(ntensors, counts, dtypes);
+  if (!valid_workspace(workspace, workspace_bytes, ntensors, tiles)) return RINGSIM_INVALID_ARGUMENT;
+  if (is_small(tiles))
+    return enqueue_small(ntensors, grads, outs, counts, dtypes, GradFactor{nullptr, 0, norm, scale, max_norm, eps}, true,
+                         s);
   double* const partial = static_cast<double*>(workspace);
-  if (!any_elements(ntensors, counts)) return result_of(launch_grad_norm_join(partial, 0, scale, norm, s));
-  if (!workspace || !aligned(workspace, 16) || workspace_bytes < norm_workspace(ntensors))
-    return RINGSIM_INVALID_ARGUMENT;
   int parts = 0;
-  ringsim_result_t res = enqueue_squares(ntensors, grads, counts, dtypes, kGradKeepBytes, partial, &parts, s);
+  ringsim_result_t res = enqueue_squares(ntensors, grads, counts, dtypes, tiles, kGradKeepBytes, partial, &parts, s);
   if (res != RINGSIM_SUCCESS) return res;
   const GradFactor f{partial, parts, norm, scale, max_norm, eps};
   return enqueue_scale(ntensors, grads, outs, counts, dtypes, f, s);

@@ -15,90 +15,170 @@
 
 namespace ringsim {
 
+// A row's part of a lane as it lies in memory.
+template <int NP>
+struct BackwardRow {
+  u32x4 dy[NP], h[NP], res[NP];
+};
+
+// Rows on 1024 lanes have 128 registers a lane, too few for the weights and
+// the residual's gradient beside dy, h and the weight's gradient: these two are
+// read where they are used. (Kept in registers they spill: TODO.)
+template <int TPR>
+constexpr bool kReadLate = TPR == 1024;
+
+// Loads of one row. No condition stands around a load, since a wait that some
+// path reaches without it would wait for everything: where the row is not
+// wanted, or there is no residual's gradient, the lanes read the first bytes
+// of a row of h for nothing.
+template <int DT, int TPR, int NP, int LK>
+__device__ __forceinline__ BackwardRow<NP> load_row(const RmsNormBackwardArgs& a, uint32_t row, bool wanted, int t) {
+  constexpr int kPack = OpElem<DT>::kPack;
+  const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
+  const auto* ph = row_ptr<DT>(a.h, o, in);
+  const auto* pdy = wanted ? row_ptr<DT>(a.grad_out, o, in) : ph;
+  const bool res = wanted && a.grad_residual.p;
+  const auto* pr = res ? row_ptr<DT>(a.grad_residual, o, in) : ph;
+  const int least = a.cols < kPack ? a.cols : kPack;
+  const int n = wanted ? a.cols : least, nr = res ? a.cols : least;
+  BackwardRow<NP> r;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c = (k * TPR + t) * kPack;
+    r.dy[k] = load_pack<DT, LK>(pdy, c, n);
+    r.h[k] = load_pack<DT, LK>(ph, c, n);
+    if constexpr (!kReadLate<TPR>) r.res[k] = load_pack<DT, LK>(pr, c, nr);
+  }
+  return r;
+}
+
+// One row in registers: its gradient is written, its part of the weight's
+// gradient added to dw. Everything stays as it lies in memory until it is
+// used, also over the barrier: unpacking again costs an operation an element
+// and saves the registers.
+template <int DT, int TPR, int NP, int LK>
+__device__ __forceinline__ void take_row(const RmsNormBackwardArgs& a, BackwardRow<NP>& r, uint32_t row, int t,
+                                         WeightPack (&w)[NP], float (&dw)[NP][OpElem<DT>::kPack], f32x2 (*lds)[16],
+                                         int& turn) {
+  constexpr int kPack = OpElem<DT>::kPack;
+  float hh = 0.0f, gh = 0.0f;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c = (k * TPR + t) * kPack;
+    float fh[kPack], fdy[kPack], fw[kPack];
+    r.h[k] = fix_pack<DT, LK>(r.h[k], c, a.cols);
+    r.dy[k] = fix_pack<DT, LK>(r.dy[k], c, a.cols);
+    unpack<DT>(r.h[k], fh);
+    unpack<DT>(r.dy[k], fdy);
+    if constexpr (kReadLate<TPR>) {
+      unpack_weight<DT, LK>(load_weight<DT, LK>(a.weight, a.weight_kind, c, a.cols), a.weight_kind, c, a.cols, fw);
+    } else {
+      asm volatile("" : "+v"(w[k].v[0]), "+v"(w[k].v[1]));
+      unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
+    }
+#pragma unroll
+    for (int i = 0; i < kPack; ++i) {
+      hh = __builtin_fmaf(fh[i], fh[i], hh);
+      gh = __builtin_fmaf(fdy[i] * fw[i], fh[i], gh);
+    }
+  }
+  row_reduce2<TPR>(hh, gh, lds, turn);
+  const float rr = rsqrtf(__builtin_fmaf(hh, a.inv_cols, a.eps));
+  const float m = rr * rr * rr * (gh * a.inv_cols);
+  const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
+  auto* pout = row_ptr<typename OpElem<DT>::T>(a.grad_in, o, in);
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    const int c = (k * TPR + t) * kPack;
+    float fh[kPack], fdy[kPack], fw[kPack], g[kPack];
+    asm volatile("" : "+v"(r.h[k]), "+v"(r.dy[k]));
+    unpack<DT>(r.h[k], fh);
+    unpack<DT>(r.dy[k], fdy);
+    if constexpr (kReadLate<TPR>) {
+      if (a.grad_residual.p) r.res[k] = load_pack<DT, LK>(row_ptr<DT>(a.grad_residual, o, in), c, a.cols);
+      unpack_weight<DT, LK>(load_weight<DT, LK>(a.weight, a.weight_kind, c, a.cols), a.weight_kind, c, a.cols, fw);
+    } else {
+      asm volatile("" : "+v"(w[k].v[0]), "+v"(w[k].v[1]));
+      unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
+    }
+#pragma unroll
+    for (int i = 0; i < kPack; ++i) {
+      g[i] = fdy[i] * fw[i] * rr - fh[i] * m;
+      dw[k][i] = __builtin_fmaf(fdy[i], fh[i] * rr, dw[k][i]);
+    }
+    if (a.grad_residual.p) {
+      float fr[kPack];
+      unpack<DT>(fix_pack<DT, LK>(r.res[k], c, a.cols), fr);
+#pragma unroll
+      for (int i = 0; i < kPack; ++i) g[i] += fr[i];
+    }
+    store_pack<DT>(pout, to_pack<DT>(g), c, a.cols);
+  }
+}
+
+// A lane's fp32 sums of a pack's columns, left for the kernel that adds them.
+template <int P>
+__device__ __forceinline__ void store_sums(float* row, const float* f, int c, int cols) {
+#pragma unroll
+  for (int i = 0; i < P / 4; ++i)
+    store16<false>(row, to_pack<RINGSIM_FLOAT32>(f + 4 * i), 4 * (c + 4 * i), 4 * cols);
+}
+
 template <int DT, int TPR, int NP, int LK>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kernel(RmsNormBackwardArgs a) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR;
   constexpr int kRows = kBlock / TPR;
+  constexpr int kPack = OpElem<DT>::kPack;
+  // Whether the next row's loads go out before this row's sums: where two
+  // rows fit into a lane's registers.
+  constexpr bool kAhead = NP * kPack <= 16 && TPR < 1024;
   using T = typename OpElem<DT>::T;
-  __shared__ float sums_hh[2][16];
-  __shared__ float sums_gh[2][16];
+  __shared__ f32x2 lds[2][16];
   __shared__ float dws[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * NP * kPack : 1];
   const int t = threadIdx.x % TPR;
-  int turn_hh = 0, turn_gh = 0;
+  int turn = 0;
   WeightPack w[NP];
   float dw[NP][kPack];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * TPR + t) * kPack, a.cols);
+    if constexpr (!kReadLate<TPR>)
+      w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * TPR + t) * kPack, a.cols);
 #pragma unroll
     for (int i = 0; i < kPack; ++i) dw[k][i] = 0.0f;
   }
-  for (uint32_t row = blockIdx.x * kRows + threadIdx.x / TPR; row < a.rows; row += gridDim.x * kRows) {
-    const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
-    Pack<DT> dy[NP], h[NP], res[NP];
-    const T* pdy = row_ptr<DT>(a.grad_out, o, in);
-    const T* ph = row_ptr<DT>(a.h, o, in);
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int c = (k * TPR + t) * kPack;
-      dy[k] = load_pack<DT, LK>(pdy, c, a.cols);
-      h[k] = load_pack<DT, LK>(ph, c, a.cols);
+  uint32_t row = blockIdx.x * kRows + threadIdx.x / TPR;
+  const uint32_t step = gridDim.x * kRows;
+  if constexpr (!kAhead) {
+    for (; row < a.rows; row += step) {
+      BackwardRow<NP> r = load_row<DT, TPR, NP, LK>(a, row, true, t);
+      take_row<DT, TPR, NP, LK>(a, r, row, t, w, dw, lds, turn);
     }
-    if (a.grad_residual.p) {
-      const T* pr = row_ptr<DT>(a.grad_residual, o, in);
-#pragma unroll
-      for (int k = 0; k < NP; ++k) res[k] = load_pack<DT, LK>(pr, (k * TPR + t) * kPack, a.cols);
-    }
-    float g[NP][kPack], hh = 0.0f, gh = 0.0f;
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int c = (k * TPR + t) * kPack;
-      float fh[kPack], fw[kPack];
-      fix_pack<DT, LK>(h[k], c, a.cols);
-      fix_pack<DT, LK>(dy[k], c, a.cols);
-      unpack<DT>(h[k], fh);
-      unpack<DT>(dy[k], g[k]);
-      unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
-#pragma unroll
-      for (int i = 0; i < kPack; ++i) {
-        g[k][i] *= fw[i];
-        hh = __builtin_fmaf(fh[i], fh[i], hh);
-        gh = __builtin_fmaf(g[k][i], fh[i], gh);
-      }
-    }
-    hh = row_reduce<TPR, AddF32>(hh, sums_hh, turn_hh);
-    gh = row_reduce<TPR, AddF32>(gh, sums_gh, turn_gh);
-    const float r = rsqrtf(__builtin_fmaf(hh, a.inv_cols, a.eps));
-    const float m = r * r * r * (gh * a.inv_cols);
-    T* pout = row_ptr<T>(a.grad_in, o, in);
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      const int c = (k * TPR + t) * kPack;
-      float fh[kPack], fdy[kPack];
-      unpack<DT>(h[k], fh);
-      unpack<DT>(dy[k], fdy);
-#pragma unroll
-      for (int i = 0; i < kPack; ++i) {
-        g[k][i] = g[k][i] * r - fh[i] * m;
-        dw[k][i] = __builtin_fmaf(fdy[i], fh[i] * r, dw[k][i]);
-      }
-      if (a.grad_residual.p) {
-        float fr[kPack];
-        fix_pack<DT, LK>(res[k], c, a.cols);
-        unpack<DT>(res[k], fr);
-#pragma unroll
-        for (int i = 0; i < kPack; ++i) g[k][i] += fr[i];
-      }
-      store_pack<DT>(pout, to_pack<DT>(g[k]), c, a.cols);
+  } else if (row < a.rows) {
+    // Two sets of registers in turn, since moving a loaded vector waits for it.
+    BackwardRow<NP> ra = load_row<DT, TPR, NP, LK>(a, row, true, t), rb;
+    for (;;) {
+      uint32_t next = row + step;  // below 2^31 + 2^14
+      rb = load_row<DT, TPR, NP, LK>(a, next < a.rows ? next : row, next < a.rows, t);
+      take_row<DT, TPR, NP, LK>(a, ra, row, t, w, dw, lds, turn);
+      row = next;
+      if (row >= a.rows) break;
+      next = row + step;
+      ra = load_row<DT, TPR, NP, LK>(a, next < a.rows ? next : row, next < a.rows, t);
+      take_row<DT, TPR, NP, LK>(a, rb, row, t, w, dw, lds, turn);
+      row = next;
+      if (row >= a.rows) break;
     }
   }
-  if (!a.partial) return;
-  float* part = a.partial + (int64_t)blockIdx.x * a.cols;
+  if (!a.partial && !a.grad_weight) return;
+  float* part = a.partial ? a.partial + (int64_t)blockIdx.x * a.cols : nullptr;
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c = (k * TPR + t) * kPack;
-      store_pack<RINGSIM_FLOAT32>(part, to_pack<RINGSIM_FLOAT32>(dw[k]), c, a.cols);
+      if (part || a.weight_dtype == RINGSIM_FLOAT32)
+        store_sums<kPack>(part ? part : static_cast<float*>(a.grad_weight), dw[k], c, a.cols);
+      else
+        store_pack<DT>(a.grad_weight, to_pack<DT>(dw[k]), c, a.cols);
     }
   } else {
     float* mine = dws[threadIdx.x / TPR];
@@ -112,7 +192,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kerne
       float sum = dws[0][c];
 #pragma unroll
       for (int i = 1; i < kRows; ++i) sum += dws[i][c];
-      part[c] = sum;
+      if (part)
+        part[c] = sum;
+      else if (a.weight_dtype == RINGSIM_FLOAT32)
+        static_cast<float*>(a.grad_weight)[c] = sum;
+      else
+        static_cast<T*>(a.grad_weight)[c] = f32_to_elem<DT>(sum);
     }
   }
 }
@@ -121,7 +206,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kerne
 // columns: 16 lanes side by side read a 64-byte line of a row, 64 such groups
 // share the rows out, and their sums are added through LDS in a fixed order.
 constexpr int kSumCols = 16;
-constexpr int kSumSlices = 64;
+template <int kSumSlices>
 __global__ void __launch_bounds__(kSumCols * kSumSlices)
     rms_norm_weight_sum_kernel(const float* partial, int parts, int cols, void* out, int dtype) {
   __shared__ float s[kSumSlices][kSumCols + 1];
@@ -149,30 +234,41 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices)
     static_cast<uint16_t*>(out)[c] = f32_to_elem<RINGSIM_FLOAT16>(sum);
 }
 
-RowShape norm_backward_shape(int64_t rows, int64_t cols) {
-  const int64_t packs = (cols + kPack - 1) / kPack;
+static RowShape norm_backward_shape(int64_t packs) {
   if (packs <= 16) return {16, 1};
   if (packs <= 64) return {64, 1};
   if (packs <= 128) return {64, 2};
   if (packs <= 256) return {256, 1};
   if (packs <= 512) return {256, 2};
   if (packs <= 1024) return {512, 2};
-  if (packs <= 2048) return {1024, 2};
-  return {1024, 4};
+  if (packs <= 2048) return {512, 4};
+  if (packs <= 4096) return {1024, 4};
+  return {1024, 8};
 }
 
-int norm_backward_workgroups(int64_t rows, int64_t cols) {
-  const RowShape sh = norm_backward_shape(rows, cols);
+static int64_t packs_of(int64_t cols, int dtype) {
+  const int per = 16 / op_dtype_size(dtype);
+  return (cols + per - 1) / per;
+}
+
+// So few rows that one workgroup's turns take no longer than a second launch:
+// it writes the weight's gradient itself. (4 rows of 4096 bf16: 7.2 us eager
+// and 6.8 in a graph; 5 rows on 5 workgroups and a second launch 8.8 and 6.1.)
+constexpr int kOneWorkgroupTurns = 3;
+
+int norm_backward_workgroups(int64_t rows, int64_t cols, int dtype) {
+  const RowShape sh = norm_backward_shape(packs_of(cols, dtype));
   const int block = sh.lanes < 256 ? 256 : sh.lanes;
   const int64_t at_once = block / sh.lanes;
+  if (rows <= kOneWorkgroupTurns * at_once) return 1;
   // As many workgroups as fill the waves of two workgroups of 256 a compute unit.
   const int64_t most = (int64_t)kComputeUnits * 512 / block;
-  return (int)std::max<int64_t>(1, std::min(most, (rows + at_once - 1) / at_once));
+  return (int)std::min(most, (rows + at_once - 1) / at_once);
 }
 
 template <int DT, int TPR, int NP, int LK>
 static hipError_t launch_kind(const RmsNormBackwardArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((rms_norm_backward_kernel<DT, TPR, NP, LK>), dim3(norm_backward_workgroups(a.rows, a.cols)),
+  hipLaunchKernelGGL((rms_norm_backward_kernel<DT, TPR, NP, LK>), dim3(norm_backward_workgroups(a.rows, a.cols, DT)),
                      dim3(TPR < 256 ? 256 : TPR), 0, s, a);
   return hipGetLastError();
 }
@@ -187,8 +283,8 @@ static hipError_t launch_shape(const RmsNormBackwardArgs& a, hipStream_t s) {
 
 template <int DT>
 static hipError_t launch_type(const RmsNormBackwardArgs& a, hipStream_t s) {
-  if (a.cols < kPack) return launch_kind<DT, 16, 1, kLoadShort>(a, s);
-  const RowShape sh = norm_backward_shape(a.rows, a.cols);
+  if (a.cols < OpElem<DT>::kPack) return launch_kind<DT, 16, 1, kLoadShort>(a, s);
+  const RowShape sh = norm_backward_shape(packs_of(a.cols, DT));
   switch (sh.lanes * 16 + sh.packs) {
     case 16 * 16 + 1: return launch_shape<DT, 16, 1>(a, s);
     case 64 * 16 + 1: return launch_shape<DT, 64, 1>(a, s);
@@ -196,8 +292,11 @@ static hipError_t launch_type(const RmsNormBackwardArgs& a, hipStream_t s) {
     case 256 * 16 + 1: return launch_shape<DT, 256, 1>(a, s);
     case 256 * 16 + 2: return launch_shape<DT, 256, 2>(a, s);
     case 512 * 16 + 2: return launch_shape<DT, 512, 2>(a, s);
-    case 1024 * 16 + 2: return launch_shape<DT, 1024, 2>(a, s);
+    case 512 * 16 + 4: return launch_shape<DT, 512, 4>(a, s);
     case 1024 * 16 + 4: return launch_shape<DT, 1024, 4>(a, s);
+    case 1024 * 16 + 8:
+      if constexpr (DT == RINGSIM_FLOAT32) return launch_shape<DT, 1024, 8>(a, s);
+      [[fallthrough]];
     default: return hipErrorInvalidValue;
   }
 }
@@ -213,8 +312,13 @@ hipError_t launch_rms_norm_backward(const RmsNormBackwardArgs& a, int dtype, hip
 
 hipError_t launch_rms_norm_weight_sum(const float* partial, int parts, int cols, void* grad_weight, int dtype,
                                       hipStream_t s) {
-  hipLaunchKernelGGL(rms_norm_weight_sum_kernel, dim3((cols + kSumCols - 1) / kSumCols), dim3(kSumCols * kSumSlices),
-                     0, s, partial, parts, cols, grad_weight, dtype);
+  const dim3 grid((cols + kSumCols - 1) / kSumCols);
+  if (parts > 64)
+    hipLaunchKernelGGL(rms_norm_weight_sum_kernel<64>, grid, dim3(kSumCols * 64), 0, s, partial, parts, cols, grad_weight,
+                       dtype);
+  else
+    hipLaunchKernelGGL(rms_norm_weight_sum_kernel<16>, grid, dim3(kSumCols * 16), 0, s, partial, parts, cols, grad_weight,
+                       dtype);
   return hipGetLastError();
 }
 

@@ -57,6 +57,11 @@ LISTS = {
     "a tile": ([8192], [BF16]),
     "a tile and one": ([4097], [F32]),
     "tile borders": ([8191, 8192, 8193, 16384, 16385], [BF16, F16, BF16, F16, BF16]),
+    "16 tiles": ([8192 * 15, 4095], [BF16, F32]),
+    "16 whole tiles": ([4096 * 16], [F32]),
+    "17 tiles": ([8192 * 16 + 1], [F16]),
+    "16 small ones": ([i % 9 for i in range(1, 17)], [F32, BF16, F16, BF16] * 4),
+    "17 small ones": ([i % 8 + 1 for i in range(17)], [F32, BF16, F16] * 5 + [F32, BF16]),
     "empty ones": ([0, 5, 0, 0, 1000, 0], [F32, F32, BF16, F16, BF16, F32]),
     "all empty": ([0, 0], [F32, BF16]),
     "mixed": ([100_003, 17, 65_536, 3, 250_001], [F32, BF16, F16, F32, BF16]),

@@ -245,6 +245,19 @@ def test_backward_many_rows(rows, cols):
         assert torch.equal(again.grad_weight, got.grad_weight) and torch.equal(again.grad_in, got.grad_in)
 
 
+@pytest.mark.parametrize("cols", [5, 100, 128, 500, 1000, 2000, 4096, 8000, 16000, 30000])
+def test_backward_few_rows(cols):
+    """Row counts on both sides of the border below which one workgroup takes
+    all rows (4 turns of 16, 4 or 1 rows)."""
+    for rows in (1, 2, 4, 5, 15, 16, 17, 63, 64, 65):
+        for name, kind in (("bf16", "same"), ("f16", "f32"), ("f32", "same")):
+            say(f"backward {name} {rows}x{cols} weight {kind}")
+            h, hd = make((rows, cols), DTYPES[name], rows)
+            dy, dyd = make((rows, cols), DTYPES[name], rows + 1, 0.1)
+            w, wd = weight_of(kind, cols, DTYPES[name], 3)
+            check_backward(rs.rms_norm_backward(dyd, hd, wd, eps=EPS), dy, h, w, None, EPS, f"{name} {rows}x{cols}")
+
+
 def test_backward_heads_and_in_place():
     h = torch.empty(37, 12, 128).normal_(generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
     dy = torch.empty(37, 8, 128).normal_(generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)

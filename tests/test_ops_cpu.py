@@ -51,9 +51,9 @@ def L():
     for name, args in {
         "ringsim_rms_norm": [vp, vp],
         "ringsim_rms_norm_backward": [vp, vp],
-        "ringsim_rms_norm_backward_workspace": [i64, i64, ctypes.POINTER(sz)],
+        "ringsim_rms_norm_backward_workspace": [i64, i64, i, ctypes.POINTER(sz)],
         "ringsim_grad_norm": [i, vp, vp, vp, f32, vp, vp, sz, vp],
-        "ringsim_grad_norm_workspace": [i, ctypes.POINTER(sz)],
+        "ringsim_grad_norm_workspace": [i, vp, vp, ctypes.POINTER(sz)],
         "ringsim_scale_grads": [i, vp, vp, vp, vp, f32, vp, f32, f32, vp],
         "ringsim_clip_grads": [i, vp, vp, vp, vp, f32, f32, f32, vp, vp, sz, vp],
     }.items():
@@ -118,7 +118,7 @@ def _backward(**over):
     a = RmsNormBackwardArgs()
     v = dict(grad_out=P, h=P, grad_in=P, weight=P, grad_weight=P, workspace=P, workspace_bytes=1 << 30,
              grad_out_stride=(64, 0), h_stride=(64, 0), grad_residual_stride=(64, 0), grad_in_stride=(64, 0),
-             outer=4, inner=1, cols=64, dtype=F32, weight_dtype=F32, eps=1e-5)
+             outer=400, inner=1, cols=64, dtype=F32, weight_dtype=F32, eps=1e-5)
     v.update(over)
     for k, x in v.items():
         setattr(a, k, type(getattr(a, k))(*x) if isinstance(x, tuple) else x)
@@ -138,12 +138,14 @@ def test_backward_refuses(L, over):
 
 def test_backward_workspace(L):
     n = ctypes.c_size_t(0)
-    for rows, cols in ((0, 1), (1, 1), (1, 32768), (777, 1111), (1 << 20, 4096), ((1 << 31) - 1, 64)):
-        assert L.ringsim_rms_norm_backward_workspace(rows, cols, n) == OK
-        assert 4 * cols <= n.value <= 4 * cols * 2048 and n.value % (4 * cols) == 0
-    for rows, cols in ((-1, 64), (4, 0), (4, 32769), (1 << 31, 64)):
-        assert L.ringsim_rms_norm_backward_workspace(rows, cols, n) == BAD
-    assert L.ringsim_rms_norm_backward_workspace(4, 4, None) == BAD
+    for dtype in (F32, BF16, F16):
+        for rows, cols in ((0, 1), (1, 1), (1, 32768), (777, 1111), (1 << 20, 4096), ((1 << 31) - 1, 64)):
+            assert L.ringsim_rms_norm_backward_workspace(rows, cols, dtype, n) == OK
+            # one workgroup (few rows) needs none
+            assert n.value <= 4 * cols * 2048 and n.value % (4 * cols) == 0 and (n.value > 0) == (rows > 64)
+    for rows, cols, dtype in ((-1, 64, F32), (4, 0, F32), (4, 32769, F32), (1 << 31, 64, F32), (4, 64, 0), (4, 64, E4M3)):
+        assert L.ringsim_rms_norm_backward_workspace(rows, cols, dtype, n) == BAD
+    assert L.ringsim_rms_norm_backward_workspace(4, 4, F32, None) == BAD
 
 
 def _list_args(ptrs, counts, types):
@@ -165,14 +167,16 @@ def test_gradient_lists_refused(L, ptrs, counts, types):
 
 
 def test_gradient_calls_refused(L):
-    n, p, c, t = _list_args([P], [8], [F32])
+    n, p, c, t = _list_args([P], [1 << 20], [F32])
     nan, inf, big = float("nan"), float("inf"), 1 << 30
     need = ctypes.c_size_t(0)
-    assert L.ringsim_grad_norm_workspace(1, need) == OK and need.value > 0
-    assert L.ringsim_grad_norm_workspace(-1, need) == BAD
-    assert L.ringsim_grad_norm_workspace(1, None) == BAD
-    assert L.ringsim_grad_norm_workspace(0, need) == OK
-    assert L.ringsim_grad_norm_workspace(1, need) == OK
+    assert L.ringsim_grad_norm_workspace(1, c, t, need) == OK and need.value > 0
+    for args in ((-1, c, t, need), (1, None, t, need), (1, c, None, need), (1, c, t, None),
+                 (1, (ctypes.c_int64 * 1)(-1), t, need), (1, c, (ctypes.c_int * 1)(0), need)):
+        assert L.ringsim_grad_norm_workspace(*args) == BAD
+    few = ctypes.c_size_t(1)
+    assert L.ringsim_grad_norm_workspace(0, None, None, few) == OK and few.value == 0
+    assert L.ringsim_grad_norm_workspace(1, (ctypes.c_int64 * 1)(12 * 4096), t, few) == OK and few.value == 0
     for args in ((-1, p, c, t, 1.0, P, P, big), (1, None, c, t, 1.0, P, P, big), (1, p, None, t, 1.0, P, P, big),
                  (1, p, c, None, 1.0, P, P, big), (1, p, c, t, nan, P, P, big), (1, p, c, t, inf, P, P, big),
                  (1, p, c, t, 1.0, None, P, big), (1, p, c, t, 1.0, P + 2, P, big), (1, p, c, t, 1.0, P, None, big),
