@@ -232,41 +232,64 @@ __device__ __forceinline__ V lanes_reduce(V v) {
 // Rows
 // ---------------------------------------------------------------------------
 
-// Sum (or largest) over the TPR lanes that hold a row. Rows of one wave or
-// less need no barrier. Longer ones join their waves' results through LDS:
-// two buffers in turn, so one barrier a reduction is enough (a wave that
-// writes a buffer again has passed the barrier of the other one, which every
-// wave reached after it had read this one).
+// Lanes that hold a row: TPR of them up to a wave, several rows a workgroup;
+// above, one row a workgroup of whole waves, TPR the most it may have.
+template <int TPR>
+__device__ __forceinline__ int row_lanes() {
+  return TPR <= 64 ? TPR : (int)blockDim.x;
+}
+template <int TPR>
+constexpr int kRowsPerBlock = TPR <= 64 ? 256 / TPR : 1;
+template <int TPR>
+constexpr int kMaxBlock = TPR <= 64 ? 256 : TPR;
+
+// Where the waves of a row leave what they reduced. Two buffers in turn, so
+// one barrier a reduction is enough: a wave that writes a buffer again has
+// passed the barrier of the other one, which every wave reached after it had
+// read this one. Slots of waves that the workgroup does not have stay 0.
+template <int TPR, typename V>
+struct RowBuffers {
+  static constexpr int kWaves = TPR > 64 ? TPR / 64 : 1;
+  V slot[2][kWaves];
+
+  // Before the first reduction; its barrier orders these writes too.
+  __device__ __forceinline__ void clear() {
+    if constexpr (TPR > 64) {
+      const int i = threadIdx.x;
+      if (i < kWaves && i >= (int)(blockDim.x >> 6)) slot[0][i] = slot[1][i] = V{};
+    }
+  }
+};
+
+// Sum (or largest) over the lanes that hold a row, known to each of them.
+// Rows of one wave or less need no barrier.
 template <int TPR, typename OP, typename V>
-__device__ __forceinline__ V row_reduce(V v, V (*buf)[16], int& turn) {
+__device__ __forceinline__ V row_reduce(V v, RowBuffers<TPR, V>& buf, int& turn) {
   v = lanes_reduce<(TPR < 64 ? TPR : 64), OP>(v);
   if constexpr (TPR > 64) {
-    constexpr int kWaves = TPR / 64;
-    if ((threadIdx.x & 63) == 0) buf[turn][threadIdx.x >> 6] = v;
+    if ((threadIdx.x & 63) == 0) buf.slot[turn][threadIdx.x >> 6] = v;
     __syncthreads();
-    v = buf[turn][0];
+    v = buf.slot[turn][0];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) v = OP::of(v, buf[turn][i]);
+    for (int i = 1; i < TPR / 64; ++i) v = OP::of(v, buf.slot[turn][i]);
     turn ^= 1;
   }
   return v;
 }
 
-// Two sums over the lanes that hold a row, with one barrier.
+// Two sums with one barrier.
 template <int TPR>
-__device__ __forceinline__ void row_reduce2(float& a, float& b, f32x2 (*buf)[16], int& turn) {
+__device__ __forceinline__ void row_reduce2(float& a, float& b, RowBuffers<TPR, f32x2>& buf, int& turn) {
   constexpr int kLanes = TPR < 64 ? TPR : 64;
   a = lanes_reduce<kLanes, AddF32>(a);
   b = lanes_reduce<kLanes, AddF32>(b);
   if constexpr (TPR > 64) {
-    if ((threadIdx.x & 63) == 0) buf[turn][threadIdx.x >> 6] = f32x2{a, b};
+    if ((threadIdx.x & 63) == 0) buf.slot[turn][threadIdx.x >> 6] = f32x2{a, b};
     __syncthreads();
-    f32x2 v = buf[turn][0];
-    a = v.x;
-    b = v.y;
+    a = b = 0.0f;
 #pragma unroll
-    for (int i = 1; i < TPR / 64; ++i) {
-      v = buf[turn][i];
+    for (int i = 0; i < TPR / 64; ++i) {
+      const f32x2 v = buf.slot[turn][i];
       a += v.x;
       b += v.y;
     }

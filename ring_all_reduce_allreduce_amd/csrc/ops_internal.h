@@ -60,11 +60,7 @@ struct RmsNormBackwardArgs {
   float eps, inv_cols;
 };
 
-// How a row is laid over lanes: `lanes` lanes of a workgroup hold a row,
-// `packs` packs of 16 bytes each.
-struct RowShape {
-  int lanes, packs;
-};
+// Workgroups, and so rows of partial sums, of the backward pass.
 int norm_backward_workgroups(int64_t rows, int64_t cols, int dtype);
 
 hipError_t launch_rms_norm(const RmsNormArgs& a, int dtype, hipStream_t s);

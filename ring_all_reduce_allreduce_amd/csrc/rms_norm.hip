@@ -19,16 +19,18 @@
 namespace ringsim {
 
 template <int DT, int TPR, int NP, bool Q, int LK>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNormArgs a) {
-  constexpr int kBlock = TPR < 256 ? 256 : TPR;
-  constexpr int kRows = kBlock / TPR;  // rows of a workgroup
+__global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_kernel(RmsNormArgs a) {
+  constexpr int kRows = kRowsPerBlock<TPR>;
   constexpr int kPack = OpElem<DT>::kPack;
   using T = typename OpElem<DT>::T;
-  __shared__ float sums[2][16];
-  __shared__ uint32_t tops[2][16];
+  __shared__ RowBuffers<TPR, float> sums;
+  __shared__ RowBuffers<TPR, uint32_t> tops;
+  sums.clear();
+  if constexpr (Q) tops.clear();
   int turn = 0, qturn = 0;
-  const int t = threadIdx.x % TPR;
-  const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kRows + threadIdx.x / TPR;
+  const int lanes = row_lanes<TPR>(), t = TPR <= 64 ? threadIdx.x % TPR : threadIdx.x;
+  const auto column = [&](int k) { return (k * lanes + t) * kPack; };  // first of pack k
+  const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
   if (row >= a.rows) return;  // the same for all lanes of a row
   const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
   float h[NP][kPack];
@@ -36,21 +38,21 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNorm
   WeightPack w[NP];
   const T* px = row_ptr<DT>(a.x, o, in);
 #pragma unroll
-  for (int k = 0; k < NP; ++k) x[k] = load_pack<DT, LK>(px, (k * TPR + t) * kPack, a.cols);
+  for (int k = 0; k < NP; ++k) x[k] = load_pack<DT, LK>(px, column(k), a.cols);
   if (a.residual.p) {
     const T* pr = row_ptr<DT>(a.residual, o, in);
 #pragma unroll
-    for (int k = 0; k < NP; ++k) res[k] = load_pack<DT, LK>(pr, (k * TPR + t) * kPack, a.cols);
+    for (int k = 0; k < NP; ++k) res[k] = load_pack<DT, LK>(pr, column(k), a.cols);
   }
 #pragma unroll
-  for (int k = 0; k < NP; ++k) w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * TPR + t) * kPack, a.cols);
+  for (int k = 0; k < NP; ++k) w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, column(k), a.cols);
 #pragma unroll
-  for (int k = 0; k < NP; ++k) unpack<DT>(fix_pack<DT, LK>(x[k], (k * TPR + t) * kPack, a.cols), h[k]);
+  for (int k = 0; k < NP; ++k) unpack<DT>(fix_pack<DT, LK>(x[k], column(k), a.cols), h[k]);
   if (a.residual.p) {
     T* ph = row_ptr<T>(a.residual_out, o, in);
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int c = (k * TPR + t) * kPack;
+      const int c = column(k);
       float f[kPack];
       unpack<DT>(fix_pack<DT, LK>(res[k], c, a.cols), f);
 #pragma unroll
@@ -69,21 +71,21 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNorm
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     float fw[kPack];
-    unpack_weight<DT, LK>(w[k], a.weight_kind, (k * TPR + t) * kPack, a.cols, fw);
+    unpack_weight<DT, LK>(w[k], a.weight_kind, column(k), a.cols, fw);
 #pragma unroll
     for (int i = 0; i < kPack; ++i) h[k][i] = h[k][i] * r * fw[i];
   }
   if constexpr (!Q) {
     T* py = row_ptr<T>(a.out, o, in);
 #pragma unroll
-    for (int k = 0; k < NP; ++k) store_pack<DT>(py, to_pack<DT>(h[k]), (k * TPR + t) * kPack, a.cols);
+    for (int k = 0; k < NP; ++k) store_pack<DT>(py, to_pack<DT>(h[k]), column(k), a.cols);
   } else {
     // Largest |y| of the row, or of the lanes that hold a group: groups start
     // at multiples of their width, lanes beyond the row hold 0.
     uint32_t top[NP];
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int c = (k * TPR + t) * kPack;
+      const int c = column(k);
       top[k] = 0;
 #pragma unroll
       for (int i = 0; i < kPack; ++i)
@@ -96,14 +98,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNorm
 #pragma unroll
       for (int k = 1; k < NP; ++k) top[k] = top[0];
     } else {
-      const int lanes = a.group / kPack;  // 4 to 32; a row of 16 lanes is shorter than a group of 32
+      const int wide = a.group / kPack;  // lanes of a group: 4 to 32 (a row of 16 is shorter than a group of 32)
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         top[k] = lanes_reduce<4, MaxBits>(top[k]);
-        if (lanes >= 8) top[k] = MaxBits::of(top[k], dpp<0x141>(top[k]));
-        if (lanes >= 16) top[k] = MaxBits::of(top[k], dpp<0x140>(top[k]));
-        if constexpr (TPR >= 64 && DT == RINGSIM_FLOAT32) {
-          if (lanes >= 32) top[k] = swap16_reduce<MaxBits>(top[k]);
+        if (wide >= 8) top[k] = MaxBits::of(top[k], dpp<0x141>(top[k]));
+        if (wide >= 16) top[k] = MaxBits::of(top[k], dpp<0x140>(top[k]));
+        if constexpr (TPR >= 32 && DT == RINGSIM_FLOAT32) {
+          if (wide >= 32) top[k] = swap16_reduce<MaxBits>(top[k]);
         }
       }
     }
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNorm
     float* ps = a.scales + (int64_t)row * a.groups;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int c = (k * TPR + t) * kPack;
+      const int c = column(k);
       // Not fmaxf, which would drop a NaN.
       float scale = __uint_as_float(top[k]) / 448.0f;
       scale = scale < 0x1p-126f ? 0x1p-126f : scale;
@@ -146,13 +148,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_kernel(RmsNorm
 }
 
 template <int DT, int TPR, int NP, int LK>
-static hipError_t launch_kind(const RmsNormArgs& a, hipStream_t s) {
-  constexpr int kBlock = TPR < 256 ? 256 : TPR;
-  constexpr int kRows = kBlock / TPR;
+static hipError_t launch_kind(const RmsNormArgs& a, int lanes, hipStream_t s) {
+  constexpr int kRows = kRowsPerBlock<TPR>;
   const int64_t need = ((int64_t)a.rows + kRows - 1) / kRows;
   // A dimension of a grid holds below 2^32 threads.
   const unsigned gx = (unsigned)std::min<int64_t>(need, 1 << 20);
-  const dim3 grid(gx, (unsigned)((need + gx - 1) / gx)), block(kBlock);
+  const dim3 grid(gx, (unsigned)((need + gx - 1) / gx)), block(lanes * kRows);
   if (a.scales)
     hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, true, LK>), grid, block, 0, s, a);
   else
@@ -161,43 +162,30 @@ static hipError_t launch_kind(const RmsNormArgs& a, hipStream_t s) {
 }
 
 template <int DT, int TPR, int NP>
-static hipError_t launch_shape(const RmsNormArgs& a, hipStream_t s) {
+static hipError_t launch_shape(const RmsNormArgs& a, int lanes, hipStream_t s) {
   const int64_t bytes = (int64_t)a.rows * a.cols * (int64_t)sizeof(typename OpElem<DT>::T) * (a.residual.p ? 4 : 2);
-  return bytes > kStreamBytes ? launch_kind<DT, TPR, NP, kLoadStream>(a, s)
-                              : launch_kind<DT, TPR, NP, kLoadCached>(a, s);
+  return bytes > kStreamBytes ? launch_kind<DT, TPR, NP, kLoadStream>(a, lanes, s)
+                              : launch_kind<DT, TPR, NP, kLoadCached>(a, lanes, s);
 }
 
-static RowShape norm_shape(int64_t packs) {
-  if (packs <= 16) return {16, 1};
-  if (packs <= 64) return {64, 1};
-  if (packs <= 128) return {64, 2};
-  if (packs <= 256) return {256, 1};
-  if (packs <= 512) return {256, 2};
-  if (packs <= 1024) return {256, 4};
-  if (packs <= 2048) return {1024, 2};
-  if (packs <= 4096) return {1024, 4};
-  return {1024, 8};
-}
-
+// Lanes by the packs of a row: a part of a wave, a wave, or as many whole
+// waves as `np` packs a lane leave. TODO
 template <int DT>
 static hipError_t launch_type(const RmsNormArgs& a, hipStream_t s) {
   constexpr int kPack = OpElem<DT>::kPack;
-  if (a.cols < kPack) return launch_kind<DT, 16, 1, kLoadShort>(a, s);
-  const RowShape sh = norm_shape((a.cols + kPack - 1) / kPack);
-  switch (sh.lanes * 16 + sh.packs) {
-    case 16 * 16 + 1: return launch_shape<DT, 16, 1>(a, s);
-    case 64 * 16 + 1: return launch_shape<DT, 64, 1>(a, s);
-    case 64 * 16 + 2: return launch_shape<DT, 64, 2>(a, s);
-    case 256 * 16 + 1: return launch_shape<DT, 256, 1>(a, s);
-    case 256 * 16 + 2: return launch_shape<DT, 256, 2>(a, s);
-    case 256 * 16 + 4: return launch_shape<DT, 256, 4>(a, s);
-    case 1024 * 16 + 2: return launch_shape<DT, 1024, 2>(a, s);
-    case 1024 * 16 + 4: return launch_shape<DT, 1024, 4>(a, s);
-    case 1024 * 16 + 8:
-      if constexpr (DT == RINGSIM_FLOAT32) return launch_shape<DT, 1024, 8>(a, s);
-      [[fallthrough]];
-    default: return hipErrorInvalidValue;
-  }
+  if (a.cols < kPack) return launch_kind<DT, 16, 1, kLoadShort>(a, 16, s);
+  const int packs = (a.cols + kPack - 1) / kPack;
+  const auto lanes = [&](int np) { return (packs + 64 * np - 1) / (64 * np) * 64; };
+  if (packs <= 16) return launch_shape<DT, 16, 1>(a, 16, s);
+  if (packs <= 32) return launch_shape<DT, 32, 1>(a, 32, s);
+  if (packs <= 64) return launch_shape<DT, 64, 1>(a, 64, s);
+  if (packs <= 128) return launch_shape<DT, 64, 2>(a, 64, s);
+  if (packs <= 256) return launch_shape<DT, 256, 1>(a, lanes(1), s);
+  if (packs <= 1024) return launch_shape<DT, 512, 2>(a, lanes(2), s);
+  if (packs <= 2048) return launch_shape<DT, 1024, 2>(a, lanes(2), s);
+  if (packs <= 4096) return launch_shape<DT, 1024, 4>(a, lanes(4), s);
+  if constexpr (DT == RINGSIM_FLOAT32) return launch_shape<DT, 1024, 8>(a, lanes(8), s);
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_rms_norm(const RmsNormArgs& a, int dtype, hipStream_t s) {

@@ -41,10 +41,11 @@ __device__ __forceinline__ BackwardRow<NP> load_row(const RmsNormBackwardArgs& a
   const auto* pr = res ? row_ptr<DT>(a.grad_residual, o, in) : ph;
   const int least = a.cols < kPack ? a.cols : kPack;
   const int n = wanted ? a.cols : least, nr = res ? a.cols : least;
+  const int lanes = row_lanes<TPR>();
   BackwardRow<NP> r;
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    const int c = (k * TPR + t) * kPack;
+    const int c = (k * lanes + t) * kPack;
     r.dy[k] = load_pack<DT, LK>(pdy, c, n);
     r.h[k] = load_pack<DT, LK>(ph, c, n);
     if constexpr (!kReadLate<TPR>) r.res[k] = load_pack<DT, LK>(pr, c, nr);
@@ -58,13 +59,14 @@ __device__ __forceinline__ BackwardRow<NP> load_row(const RmsNormBackwardArgs& a
 // and saves the registers.
 template <int DT, int TPR, int NP, int LK>
 __device__ __forceinline__ void take_row(const RmsNormBackwardArgs& a, BackwardRow<NP>& r, uint32_t row, int t,
-                                         WeightPack (&w)[NP], float (&dw)[NP][OpElem<DT>::kPack], f32x2 (*lds)[16],
+                                         WeightPack (&w)[NP], float (&dw)[NP][OpElem<DT>::kPack], RowBuffers<TPR, f32x2>& lds,
                                          int& turn) {
   constexpr int kPack = OpElem<DT>::kPack;
+  const int lanes = row_lanes<TPR>();
   float hh = 0.0f, gh = 0.0f;
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    const int c = (k * TPR + t) * kPack;
+    const int c = (k * lanes + t) * kPack;
     float fh[kPack], fdy[kPack], fw[kPack];
     r.h[k] = fix_pack<DT, LK>(r.h[k], c, a.cols);
     r.dy[k] = fix_pack<DT, LK>(r.dy[k], c, a.cols);
@@ -89,7 +91,7 @@ __device__ __forceinline__ void take_row(const RmsNormBackwardArgs& a, BackwardR
   auto* pout = row_ptr<typename OpElem<DT>::T>(a.grad_in, o, in);
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    const int c = (k * TPR + t) * kPack;
+    const int c = (k * lanes + t) * kPack;
     float fh[kPack], fdy[kPack], fw[kPack], g[kPack];
     asm volatile("" : "+v"(r.h[k]), "+v"(r.dy[k]));
     unpack<DT>(r.h[k], fh);
@@ -125,28 +127,28 @@ __device__ __forceinline__ void store_sums(float* row, const float* f, int c, in
 }
 
 template <int DT, int TPR, int NP, int LK>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kernel(RmsNormBackwardArgs a) {
-  constexpr int kBlock = TPR < 256 ? 256 : TPR;
-  constexpr int kRows = kBlock / TPR;
+__global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_backward_kernel(RmsNormBackwardArgs a) {
+  constexpr int kRows = kRowsPerBlock<TPR>;
   constexpr int kPack = OpElem<DT>::kPack;
   // Whether the next row's loads go out before this row's sums: where two
   // rows fit into a lane's registers.
   constexpr bool kAhead = NP * kPack <= 16 && TPR < 1024;
   using T = typename OpElem<DT>::T;
-  __shared__ f32x2 lds[2][16];
+  __shared__ RowBuffers<TPR, f32x2> lds;
   __shared__ float dws[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * NP * kPack : 1];
-  const int t = threadIdx.x % TPR;
+  lds.clear();
+  const int lanes = row_lanes<TPR>(), t = TPR <= 64 ? threadIdx.x % TPR : threadIdx.x;
   int turn = 0;
   WeightPack w[NP];
   float dw[NP][kPack];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     if constexpr (!kReadLate<TPR>)
-      w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * TPR + t) * kPack, a.cols);
+      w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * lanes + t) * kPack, a.cols);
 #pragma unroll
     for (int i = 0; i < kPack; ++i) dw[k][i] = 0.0f;
   }
-  uint32_t row = blockIdx.x * kRows + threadIdx.x / TPR;
+  uint32_t row = blockIdx.x * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
   const uint32_t step = gridDim.x * kRows;
   if constexpr (!kAhead) {
     for (; row < a.rows; row += step) {
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kerne
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-      const int c = (k * TPR + t) * kPack;
+      const int c = (k * lanes + t) * kPack;
       if (part || a.weight_dtype == RINGSIM_FLOAT32)
         store_sums<kPack>(part ? part : static_cast<float*>(a.grad_weight), dw[k], c, a.cols);
       else
@@ -185,10 +187,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) rms_norm_backward_kerne
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
 #pragma unroll
-      for (int i = 0; i < kPack; ++i) mine[(k * TPR + t) * kPack + i] = dw[k][i];
+      for (int i = 0; i < kPack; ++i) mine[(k * lanes + t) * kPack + i] = dw[k][i];
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < a.cols; c += kBlock) {
+    for (int c = threadIdx.x; c < a.cols; c += kMaxBlock<TPR>) {
       float sum = dws[0][c];
 #pragma unroll
       for (int i = 1; i < kRows; ++i) sum += dws[i][c];
@@ -234,68 +236,74 @@ __global__ void __launch_bounds__(kSumCols * kSumSlices)
     static_cast<uint16_t*>(out)[c] = f32_to_elem<RINGSIM_FLOAT16>(sum);
 }
 
-static RowShape norm_backward_shape(int64_t packs) {
-  if (packs <= 16) return {16, 1};
-  if (packs <= 64) return {64, 1};
-  if (packs <= 128) return {64, 2};
-  if (packs <= 256) return {256, 1};
-  if (packs <= 512) return {256, 2};
-  if (packs <= 1024) return {512, 2};
-  if (packs <= 2048) return {512, 4};
-  if (packs <= 4096) return {1024, 4};
-  return {1024, 8};
-}
+// How a row is laid over lanes: a part of a wave, a wave, or as many whole
+// waves as `packs` packs of 16 bytes a lane leave. `most`: the kernel's TPR.
+struct RowShape {
+  int lanes, packs, most;
+};
 
-static int64_t packs_of(int64_t cols, int dtype) {
-  const int per = 16 / op_dtype_size(dtype);
-  return (cols + per - 1) / per;
+static RowShape backward_shape(int64_t cols, int dtype) {
+  const int per = 16 / op_dtype_size(dtype), packs = (int)((cols + per - 1) / per);
+  const auto lanes = [&](int np) { return (packs + 64 * np - 1) / (64 * np) * 64; };
+  if (packs <= 16) return {16, 1, 16};
+  if (packs <= 32) return {32, 1, 32};
+  if (packs <= 64) return {64, 1, 64};
+  if (packs <= 128) return {64, 2, 64};
+  if (packs <= 256) return {lanes(1), 1, 256};
+  if (packs <= 1024) return {lanes(2), 2, 512};
+  if (packs <= 2048) return {lanes(4), 4, 512};
+  if (packs <= 4096) return {lanes(4), 4, 1024};
+  return {lanes(8), 8, 1024};
 }
 
 // So few rows that one workgroup's turns take no longer than a second launch:
 // it writes the weight's gradient itself. (4 rows of 4096 bf16: 7.2 us eager
 // and 6.8 in a graph; 5 rows on 5 workgroups and a second launch 8.8 and 6.1.)
 constexpr int kOneWorkgroupTurns = 3;
+// Waves a compute unit is given. Each workgroup leaves a row of partial sums,
+// so more of them cost more there than they hide: 16384 rows of 4096 bf16 take
+// 96 us with 8 waves and 104 with 12.
+constexpr int kBackwardWaves = 8;
 
 int norm_backward_workgroups(int64_t rows, int64_t cols, int dtype) {
-  const RowShape sh = norm_backward_shape(packs_of(cols, dtype));
-  const int block = sh.lanes < 256 ? 256 : sh.lanes;
-  const int64_t at_once = block / sh.lanes;
+  const RowShape sh = backward_shape(cols, dtype);
+  const int64_t at_once = sh.lanes <= 64 ? 256 / sh.lanes : 1;
   if (rows <= kOneWorkgroupTurns * at_once) return 1;
-  // As many workgroups as fill the waves of two workgroups of 256 a compute unit.
-  const int64_t most = (int64_t)kComputeUnits * 512 / block;
+  const int waves = sh.lanes <= 64 ? 4 : sh.lanes / 64;
+  const int64_t most = (int64_t)kComputeUnits * std::max(1, kBackwardWaves / waves);
   return (int)std::min(most, (rows + at_once - 1) / at_once);
 }
 
 template <int DT, int TPR, int NP, int LK>
-static hipError_t launch_kind(const RmsNormBackwardArgs& a, hipStream_t s) {
+static hipError_t launch_kind(const RmsNormBackwardArgs& a, int lanes, hipStream_t s) {
   hipLaunchKernelGGL((rms_norm_backward_kernel<DT, TPR, NP, LK>), dim3(norm_backward_workgroups(a.rows, a.cols, DT)),
-                     dim3(TPR < 256 ? 256 : TPR), 0, s, a);
+                     dim3(lanes * kRowsPerBlock<TPR>), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DT, int TPR, int NP>
-static hipError_t launch_shape(const RmsNormBackwardArgs& a, hipStream_t s) {
+static hipError_t launch_shape(const RmsNormBackwardArgs& a, int lanes, hipStream_t s) {
   const int64_t bytes =
       (int64_t)a.rows * a.cols * (int64_t)sizeof(typename OpElem<DT>::T) * (a.grad_residual.p ? 4 : 3);
-  return bytes > kStreamBytes ? launch_kind<DT, TPR, NP, kLoadStream>(a, s)
-                              : launch_kind<DT, TPR, NP, kLoadCached>(a, s);
+  return bytes > kStreamBytes ? launch_kind<DT, TPR, NP, kLoadStream>(a, lanes, s)
+                              : launch_kind<DT, TPR, NP, kLoadCached>(a, lanes, s);
 }
 
 template <int DT>
 static hipError_t launch_type(const RmsNormBackwardArgs& a, hipStream_t s) {
-  if (a.cols < OpElem<DT>::kPack) return launch_kind<DT, 16, 1, kLoadShort>(a, s);
-  const RowShape sh = norm_backward_shape(packs_of(a.cols, DT));
-  switch (sh.lanes * 16 + sh.packs) {
-    case 16 * 16 + 1: return launch_shape<DT, 16, 1>(a, s);
-    case 64 * 16 + 1: return launch_shape<DT, 64, 1>(a, s);
-    case 64 * 16 + 2: return launch_shape<DT, 64, 2>(a, s);
-    case 256 * 16 + 1: return launch_shape<DT, 256, 1>(a, s);
-    case 256 * 16 + 2: return launch_shape<DT, 256, 2>(a, s);
-    case 512 * 16 + 2: return launch_shape<DT, 512, 2>(a, s);
-    case 512 * 16 + 4: return launch_shape<DT, 512, 4>(a, s);
-    case 1024 * 16 + 4: return launch_shape<DT, 1024, 4>(a, s);
+  if (a.cols < OpElem<DT>::kPack) return launch_kind<DT, 16, 1, kLoadShort>(a, 16, s);
+  const RowShape sh = backward_shape(a.cols, DT);
+  switch (sh.most * 16 + sh.packs) {
+    case 16 * 16 + 1: return launch_shape<DT, 16, 1>(a, sh.lanes, s);
+    case 32 * 16 + 1: return launch_shape<DT, 32, 1>(a, sh.lanes, s);
+    case 64 * 16 + 1: return launch_shape<DT, 64, 1>(a, sh.lanes, s);
+    case 64 * 16 + 2: return launch_shape<DT, 64, 2>(a, sh.lanes, s);
+    case 256 * 16 + 1: return launch_shape<DT, 256, 1>(a, sh.lanes, s);
+    case 512 * 16 + 2: return launch_shape<DT, 512, 2>(a, sh.lanes, s);
+    case 512 * 16 + 4: return launch_shape<DT, 512, 4>(a, sh.lanes, s);
+    case 1024 * 16 + 4: return launch_shape<DT, 1024, 4>(a, sh.lanes, s);
     case 1024 * 16 + 8:
-      if constexpr (DT == RINGSIM_FLOAT32) return launch_shape<DT, 1024, 8>(a, s);
+      if constexpr (DT == RINGSIM_FLOAT32) return launch_shape<DT, 1024, 8>(a, sh.lanes, s);
       [[fallthrough]];
     default: return hipErrorInvalidValue;
   }

@@ -12,10 +12,10 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 EPS = 1e-5
-# Columns on both sides of every border of a lane's pack (8), a row's lanes
-# (128, 512, 1024, 2048, 4096, 8192, 16384) and the limit.
-COLS = (1, 2, 7, 8, 9, 64, 127, 128, 129, 500, 512, 513, 1024, 1025, 2047, 2048, 2049, 4096, 5119, 8192, 8193, 16384,
-        16385, 32767, 32768)
+# Columns on both sides of every border: of a lane's 16 bytes, of the lanes a
+# row takes (powers of two from 64 on), of whole waves, and the limit.
+COLS = (1, 2, 3, 4, 5, 7, 8, 9, 63, 64, 65, 127, 128, 129, 255, 256, 257, 500, 512, 513, 1024, 1025, 1600, 2047, 2048,
+        2049, 4096, 4097, 5119, 8192, 8193, 12300, 16384, 16385, 24576, 32767, 32768)
 
 
 def make(shape, dtype, seed, std=1.0, pad=0, offset=0):
