@@ -1,0 +1,140 @@
+"""Data-parallel training steps over simulated ranks, with everything between
+the matrix products done by this package.
+
+Every rank holds a copy of a small residual network and its own tokens. A
+block norms the residual stream, with the addition of the previous block's
+output fused into the norm, and runs a two-layer perceptron on it. The
+backward pass is written out with the norm's gradients; each rank's weight
+gradients lie in one bucket, the buckets are summed over the ranks with the
+ring all-reduce, and their mean is clipped by its global norm and taken by a
+plain gradient descent. Afterwards one token goes through the trained norm in
+the form that serving takes: 8 bits with a scale for each group of 128
+columns.
+
+    python examples/train_step.py [--ranks 4] [--steps 10] [--dtype bfloat16]
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import ring_all_reduce_allreduce_amd as rs  # noqa: E402
+
+EPS = 1e-5
+
+
+class Rank:
+    """One rank's copy of the weights, and its gradients in one bucket."""
+
+    def __init__(self, width: int, hidden: int, blocks: int, dtype):
+        gen = torch.Generator().manual_seed(0)  # the same weights on every rank
+
+        def made(*shape, std):
+            return torch.empty(shape).normal_(0.0, std, generator=gen).to("cuda", dtype)
+
+        self.blocks = [(torch.ones(width, device="cuda", dtype=dtype), made(width, hidden, std=width ** -0.5),
+                        made(hidden, width, std=hidden ** -0.5)) for _ in range(blocks)]
+        self.last = torch.ones(width, device="cuda", dtype=dtype)
+        self.weights = [w for b in self.blocks for w in b] + [self.last]
+        self.bucket = torch.zeros(sum(w.numel() for w in self.weights), device="cuda", dtype=dtype)
+        self.reduced = torch.empty_like(self.bucket)
+        self.grads = self._views(self.bucket)
+        self.reduced_grads = self._views(self.reduced)
+
+    def _views(self, flat) -> list:
+        views, at = [], 0
+        for w in self.weights:
+            views.append(flat[at:at + w.numel()].view(w.shape))
+            at += w.numel()
+        return views
+
+    def forward_backward(self, tokens, target) -> torch.Tensor:
+        """Loss of this rank's tokens; leaves the gradients in the bucket."""
+        kept, stream, branch = [], tokens, None
+        for gain, up, down in self.blocks:
+            n = rs.rms_norm(stream if branch is None else branch, gain, residual=None if branch is None else stream,
+                            eps=EPS)
+            stream = stream if branch is None else n.residual
+            a = n.out @ up
+            s = torch.nn.functional.silu(a)
+            kept.append((stream, n.out, a, s))
+            branch = s @ down
+        n = rs.rms_norm(branch, self.last, residual=stream, eps=EPS)
+        off = n.out.float() - target
+        loss = 0.5 * off.square().mean()
+
+        grad_out = (off / off.numel()).to(tokens.dtype)
+        back = rs.rms_norm_backward(grad_out, n.residual, self.last, eps=EPS, grad_weight=self.grads[-1])
+        d_stream = back.grad_in  # of the stream and of the last block's branch alike
+        for i in reversed(range(len(self.blocks))):
+            gain, up, down = self.blocks[i]
+            h, u, a, s = kept[i]
+            g_gain, g_up, g_down = self.grads[3 * i:3 * i + 3]
+            torch.mm(s.t(), d_stream, out=g_down)
+            sig = torch.sigmoid(a.float())
+            da = ((d_stream @ down.t()).float() * (sig * (1 + a.float() * (1 - sig)))).to(a.dtype)
+            torch.mm(u.t(), da, out=g_up)
+            back = rs.rms_norm_backward(da @ up.t(), h, gain, grad_residual=d_stream, eps=EPS, grad_weight=g_gain)
+            d_stream = back.grad_in
+        return loss
+
+
+def train(ranks: int = 4, steps: int = 10, tokens: int = 256, width: int = 512, hidden: int = 1024, blocks: int = 3,
+          dtype=torch.bfloat16, max_norm: float = 0.05, rate: float = 5.0):
+    """(mean loss of every step, gradient norm of every step, the ranks)."""
+    group = [Rank(width, hidden, blocks, dtype) for _ in range(ranks)]
+    gen = torch.Generator().manual_seed(1)
+    data = [torch.empty(tokens, width).normal_(generator=gen).to("cuda", dtype) for _ in range(ranks)]
+    targets = [torch.empty(tokens, width).normal_(generator=gen).to("cuda") for _ in range(ranks)]
+    comm = rs.comm_init(ranks, 4)
+    losses, norms = [], []
+    try:
+        for _ in range(steps):
+            losses.append(torch.stack([r.forward_backward(x, t) for r, x, t in zip(group, data, targets)]).mean())
+            rs.allreduce(comm, [r.bucket for r in group], [r.reduced for r in group], op="sum")
+            # The ranks hold copies of the sum: one norm serves them all.
+            norm = rs.clip_grads(group[0].reduced_grads, max_norm, scale=1.0 / ranks, outs=group[0].grads)
+            for r in group[1:]:
+                rs.scale_grads(r.reduced_grads, norm, max_norm, scale=1.0 / ranks, outs=r.grads)
+            norms.append(norm)
+            for r in group:
+                torch._foreach_add_(r.weights, r.grads, alpha=-rate)
+        torch.cuda.synchronize()
+        if (err := rs.get_async_error(comm)) != rs.SUCCESS:
+            raise rs.RingsimError(err, "ringsim_allreduce")
+    finally:
+        rs.comm_destroy(comm)
+    return [float(v) for v in losses], [float(v) for v in norms], group
+
+
+def serve_one(rank: Rank, token: torch.Tensor) -> tuple:
+    """One token's normed row in 8 bits with its scales, and read back."""
+    n = rs.rms_norm(token, rank.last, eps=EPS, out_dtype="float8_e4m3", group=128)
+    return n.out, n.scales, n.out.float() * n.scales.repeat_interleave(128, -1)[..., :token.shape[-1]]
+
+
+def main() -> None:
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    ap.add_argument("--ranks", type=int, default=4)
+    ap.add_argument("--steps", type=int, default=10)
+    ap.add_argument("--dtype", default="bfloat16", choices=("bfloat16", "float32"))
+    a = ap.parse_args()
+    dtype = getattr(torch, a.dtype)
+    losses, norms, group = train(a.ranks, a.steps, dtype=dtype)
+    for i, (loss, norm) in enumerate(zip(losses, norms)):
+        print(f"step {i}: loss {loss:.4f}, gradient norm {norm:.4f}")
+    same = all(torch.equal(x, y) for r in group[1:] for x, y in zip(group[0].weights, r.weights))
+    print(f"the ranks' weights are {'equal' if same else 'DIFFERENT'}")
+    token = torch.randn(1, group[0].last.numel(), device="cuda").to(dtype)
+    q, scales, read = serve_one(group[0], token)
+    plain = rs.rms_norm(token, group[0].last, eps=EPS).out.float()
+    print(f"one token in 8 bits: {q.numel()} values, {scales.numel()} scales, "
+          f"{float((read - plain).norm() / plain.norm()):.3f} off the unquantised row")
+
+
+if __name__ == "__main__":
+    main()

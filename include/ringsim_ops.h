@@ -54,7 +54,7 @@ typedef enum {
 /* Longest row the norm and its gradients take. */
 #define RINGSIM_NORM_MAX_COLS 32768
 
-/* Arguments of ringsim_rms_norm. Every tensor is a [outer, inner, cols]
+/* Arguments of ringsim_rms_norm. Every tensor of rows is a [outer, inner, cols]
  * array whose last dimension is contiguous; its strides, in elements, are
  * given as {outer, inner} (inner strides are not read where inner == 1).
  * Rows of an output must not overlap. */
@@ -88,10 +88,10 @@ typedef struct {
  * ceil(cols / group), or 1):
  *     scale = max(max|y| / 448, 2^-126),  q = y / scale
  * so that q * scale stands for y; a NaN in a group makes its scale NaN.
- * out and residual_out may be x or residual themselves (same address, same
- * strides), otherwise outputs must not overlap inputs or each other. A row
- * whose sum of squares is beyond fp32's range gives zeros, as 1 / sqrt(inf)
- * does. Nothing to do (no rows) is a success. */
+ * residual_out, and out in the rows' type, may be x or residual themselves
+ * (same address, same strides); otherwise outputs must not overlap inputs or
+ * each other. A row whose sum of squares is beyond fp32's range gives zeros,
+ * as 1 / sqrt(inf) does. Nothing to do (no rows) is a success. */
 ringsim_result_t ringsim_rms_norm(const ringsim_rms_norm_t* args, ringsim_stream_t stream);
 
 /* Arguments of ringsim_rms_norm_backward; tensors as in ringsim_rms_norm_t. */
@@ -154,8 +154,10 @@ ringsim_result_t ringsim_grad_norm_workspace(int ntensors, const int64_t* counts
 /* Scales gradients by what a norm known to the device leaves of them,
  *     outs[i] = grads[i] * scale * min(1, max_norm / (*norm + eps))
  * where a NaN norm makes every element NaN and an infinite one makes finite
- * elements 0. outs[i] is grads[i] itself or does not overlap any gradient;
- * outs == NULL means in place, where a factor of exactly 1 writes nothing.
+ * elements 0. outs[i] is grads[i] itself or does not overlap any gradient, and
+ * no two outputs overlap (a gradient that two parameters share is listed
+ * once); outs == NULL means in place, where a factor of exactly 1 writes
+ * nothing.
  * max_norm and eps are finite and >= 0. For ranks that hold copies of the
  * same gradients: the norm of one copy serves them all. */
 ringsim_result_t ringsim_scale_grads(int ntensors, const void* const* grads, void* const* outs, const int64_t* counts,

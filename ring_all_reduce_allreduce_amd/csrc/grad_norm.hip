@@ -275,7 +275,10 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(GradScaleTable tab
 
 // Norm and scaling of a list of at most kGradSmallTiles tiles by one
 // workgroup: every tile is read once and stays in registers until it is
-// scaled, and there is one launch instead of two. TODO
+// scaled, and there is one launch instead of two. A call takes 4.4 us for one
+// tensor of 4 KiB and 5.0 (norm) or 6.8 (clip) for 192 KiB, the 12 tiles that
+// are the limit; two launches take 8.8 and 9.7. In a graph, where a launch
+// costs less, 12 tiles are even (4.5 and 6.6 against 4.8 and 6.1), 16 lose.
 __global__ void __launch_bounds__(kGradSmallThreads)
     grad_small_kernel(GradSmallTable tab, GradFactor fac, int clip, int in_place) {
   constexpr int kGroups = kGradSmallThreads / kThreads, kRounds = kGradSmallTiles / kGroups;

@@ -19,7 +19,7 @@ typedef uint32_t u32_e1 __attribute__((aligned(1)));
 
 // A lane holds 16 bytes side by side, whatever the type, so that a wave's
 // access covers 1024 bytes without gaps. (With 32 bytes a lane for fp32, each
-// non-temporal store left half-written lines: 236 us against TODO for the
+// non-temporal store left half-written lines: 236 us against 173 for the
 // gradients of 16384 rows of 4096.)
 template <int DT>
 struct OpElem {

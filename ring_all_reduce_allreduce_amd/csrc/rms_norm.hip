@@ -18,43 +18,54 @@
 
 namespace ringsim {
 
+// A row's part of a lane as it lies in memory.
+template <int NP>
+struct NormRow {
+  u32x4 x[NP], res[NP];
+};
+
+template <int TPR>
+struct NormShared {
+  RowBuffers<TPR, float> sums;
+  RowBuffers<TPR, uint32_t> tops;
+};
+
+template <int DT, int TPR, int NP, int LK>
+__device__ __forceinline__ NormRow<NP> load_row(const RmsNormArgs& a, uint32_t row, int t) {
+  constexpr int kPack = OpElem<DT>::kPack;
+  const int lanes = row_lanes<TPR>();
+  const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
+  NormRow<NP> r;
+  const auto* px = row_ptr<DT>(a.x, o, in);
+#pragma unroll
+  for (int k = 0; k < NP; ++k) r.x[k] = load_pack<DT, LK>(px, (k * lanes + t) * kPack, a.cols);
+  if (a.residual.p) {
+    const auto* pr = row_ptr<DT>(a.residual, o, in);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) r.res[k] = load_pack<DT, LK>(pr, (k * lanes + t) * kPack, a.cols);
+  }
+  return r;
+}
+
 template <int DT, int TPR, int NP, bool Q, int LK>
-__global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_kernel(RmsNormArgs a) {
-  constexpr int kRows = kRowsPerBlock<TPR>;
+__device__ __forceinline__ void take_row(const RmsNormArgs& a, const NormRow<NP>& in_row, const WeightPack (&w)[NP],
+                                         uint32_t row, int t, NormShared<TPR>& lds) {
   constexpr int kPack = OpElem<DT>::kPack;
   using T = typename OpElem<DT>::T;
-  __shared__ RowBuffers<TPR, float> sums;
-  __shared__ RowBuffers<TPR, uint32_t> tops;
-  sums.clear();
-  if constexpr (Q) tops.clear();
-  int turn = 0, qturn = 0;
-  const int lanes = row_lanes<TPR>(), t = TPR <= 64 ? threadIdx.x % TPR : threadIdx.x;
+  int turn = 0, qturn = 0;  // one reduction of each a row and workgroup above a wave
+  const int lanes = row_lanes<TPR>();
   const auto column = [&](int k) { return (k * lanes + t) * kPack; };  // first of pack k
-  const uint32_t row = (blockIdx.y * gridDim.x + blockIdx.x) * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
-  if (row >= a.rows) return;  // the same for all lanes of a row
   const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
   float h[NP][kPack];
-  u32x4 x[NP], res[NP];
-  WeightPack w[NP];
-  const T* px = row_ptr<DT>(a.x, o, in);
 #pragma unroll
-  for (int k = 0; k < NP; ++k) x[k] = load_pack<DT, LK>(px, column(k), a.cols);
-  if (a.residual.p) {
-    const T* pr = row_ptr<DT>(a.residual, o, in);
-#pragma unroll
-    for (int k = 0; k < NP; ++k) res[k] = load_pack<DT, LK>(pr, column(k), a.cols);
-  }
-#pragma unroll
-  for (int k = 0; k < NP; ++k) w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, column(k), a.cols);
-#pragma unroll
-  for (int k = 0; k < NP; ++k) unpack<DT>(fix_pack<DT, LK>(x[k], column(k), a.cols), h[k]);
+  for (int k = 0; k < NP; ++k) unpack<DT>(fix_pack<DT, LK>(in_row.x[k], column(k), a.cols), h[k]);
   if (a.residual.p) {
     T* ph = row_ptr<T>(a.residual_out, o, in);
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c = column(k);
       float f[kPack];
-      unpack<DT>(fix_pack<DT, LK>(res[k], c, a.cols), f);
+      unpack<DT>(fix_pack<DT, LK>(in_row.res[k], c, a.cols), f);
 #pragma unroll
       for (int i = 0; i < kPack; ++i) h[k][i] += f[i];
       store_pack<DT>(ph, to_pack<DT>(h[k]), c, a.cols);
@@ -66,7 +77,7 @@ __global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_kernel(RmsNormArgs a)
 #pragma unroll
     for (int i = 0; i < kPack; ++i) ss = __builtin_fmaf(h[k][i], h[k][i], ss);
   }
-  ss = row_reduce<TPR, AddF32>(ss, sums, turn);
+  ss = row_reduce<TPR, AddF32>(ss, lds.sums, turn);
   const float r = rsqrtf(__builtin_fmaf(ss, a.inv_cols, a.eps));
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
@@ -94,7 +105,7 @@ __global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_kernel(RmsNormArgs a)
     if (a.group == 0) {
 #pragma unroll
       for (int k = 1; k < NP; ++k) top[0] = MaxBits::of(top[0], top[k]);
-      top[0] = row_reduce<TPR, MaxBits>(top[0], tops, qturn);
+      top[0] = row_reduce<TPR, MaxBits>(top[0], lds.tops, qturn);
 #pragma unroll
       for (int k = 1; k < NP; ++k) top[k] = top[0];
     } else {
@@ -147,18 +158,63 @@ __global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_kernel(RmsNormArgs a)
   }
 }
 
-template <int DT, int TPR, int NP, int LK>
-static hipError_t launch_kind(const RmsNormArgs& a, int lanes, hipStream_t s) {
+// NR rows for each of the workgroup's groups of lanes, their loads all at once.
+template <int DT, int TPR, int NP, bool Q, int LK, int NR>
+__global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_kernel(RmsNormArgs a) {
+  static_assert(NR == 1 || TPR <= 64, "several rows only where no barrier is needed");
   constexpr int kRows = kRowsPerBlock<TPR>;
-  const int64_t need = ((int64_t)a.rows + kRows - 1) / kRows;
+  constexpr int kPack = OpElem<DT>::kPack;
+  __shared__ NormShared<TPR> lds;
+  lds.sums.clear();
+  if constexpr (Q) lds.tops.clear();
+  const int lanes = row_lanes<TPR>(), t = TPR <= 64 ? threadIdx.x % TPR : threadIdx.x;
+  const uint32_t first = (blockIdx.y * gridDim.x + blockIdx.x) * (kRows * NR) + (TPR <= 64 ? threadIdx.x / TPR : 0);
+  if (first >= a.rows) return;  // the same for all lanes of a row
+  NormRow<NP> r[NR];
+  WeightPack w[NP];
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const uint32_t row = first + j * kRows;
+    r[j] = load_row<DT, TPR, NP, LK>(a, row < a.rows ? row : first, t);
+  }
+#pragma unroll
+  for (int k = 0; k < NP; ++k) w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * lanes + t) * kPack, a.cols);
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const uint32_t row = first + j * kRows;
+    if (row < a.rows) take_row<DT, TPR, NP, Q, LK>(a, r[j], w, row, t, lds);
+  }
+}
+
+template <int DT, int TPR, int NP, int LK, int NR>
+static hipError_t launch_rows(const RmsNormArgs& a, int lanes, hipStream_t s) {
+  constexpr int kRows = kRowsPerBlock<TPR>;
+  const int64_t need = ((int64_t)a.rows + kRows * NR - 1) / (kRows * NR);
   // A dimension of a grid holds below 2^32 threads.
   const unsigned gx = (unsigned)std::min<int64_t>(need, 1 << 20);
   const dim3 grid(gx, (unsigned)((need + gx - 1) / gx)), block(lanes * kRows);
   if (a.scales)
-    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, true, LK>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, true, LK, NR>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, false, LK>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((rms_norm_kernel<DT, TPR, NP, false, LK, NR>), grid, block, 0, s, a);
   return hipGetLastError();
+}
+
+// Rows of a wave's lanes or fewer are a few hundred bytes: two of them a group
+// of lanes halve the workgroups, whose start is what such calls wait for, once
+// there are four workgroups a compute unit all the same. 65536 rows of 128
+// bf16: 7.0 us, one row 7.7, four 7.2; 10^6 rows of 64: 57.6, 67.5, 52.0; but
+// with a residual four rows of 128 lose what two keep (into 8 bits 14.0 us,
+// two 13.3, one 12.3).
+constexpr int kShortRows = 2;
+
+template <int DT, int TPR, int NP, int LK>
+static hipError_t launch_kind(const RmsNormArgs& a, int lanes, hipStream_t s) {
+  if constexpr (TPR <= 64 && NP == 1) {
+    if (a.rows >= (uint32_t)(kComputeUnits * 4 * kShortRows * kRowsPerBlock<TPR>))
+      return launch_rows<DT, TPR, NP, LK, kShortRows>(a, lanes, s);
+  }
+  return launch_rows<DT, TPR, NP, LK, 1>(a, lanes, s);
 }
 
 template <int DT, int TPR, int NP>
@@ -169,7 +225,12 @@ static hipError_t launch_shape(const RmsNormArgs& a, int lanes, hipStream_t s) {
 }
 
 // Lanes by the packs of a row: a part of a wave, a wave, or as many whole
-// waves as `np` packs a lane leave. TODO
+// waves as `np` packs a lane leave. Few packs a lane keep short rows spread
+// out; more of them, up to what 1024 lanes need, keep the waves that meet at
+// the barrier few. 1021 rows of 5119 fp16 (640 packs) take 8.3 us on five
+// waves and 9.8 on four of four packs, half of the last one empty; 4096 rows
+// of 12288 bf16 into 8 bits (1536 packs) 59 us on 12 waves of two packs and
+// 71 on six of four, whose registers leave fewer workgroups on a compute unit.
 template <int DT>
 static hipError_t launch_type(const RmsNormArgs& a, hipStream_t s) {
   constexpr int kPack = OpElem<DT>::kPack;

@@ -11,7 +11,11 @@ import pytest
 import torch
 
 import ring_all_reduce_allreduce_amd as rs
-from ring_all_reduce_allreduce_amd import operators as ops
+from ring_all_reduce_allreduce_amd import build
+
+if not (os.path.exists(build.LIB) and os.path.exists(build.BINDING)):
+    build.build()
+from ring_all_reduce_allreduce_amd import operators as ops  # noqa: E402
 
 OK, BAD = 0, 4
 F32, BF16, F16, E4M3 = 2, 3, 16, 17
@@ -42,10 +46,6 @@ RmsNormBackwardArgs = _struct("ringsim_rms_norm_backward_t")
 
 @pytest.fixture(scope="module")
 def L():
-    if not os.path.exists(rs.LIB_PATH):
-        from ring_all_reduce_allreduce_amd import build
-
-        build.build()
     lib = ctypes.CDLL(rs.lib()._name)
     vp, i, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     for name, args in {
