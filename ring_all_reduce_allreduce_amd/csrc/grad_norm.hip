@@ -17,6 +17,7 @@ namespace ringsim {
 
 
 struct GradTile {
+  const void* in;
   int tensor;
   int type;
   int bytes;      // of the tile
@@ -48,39 +49,46 @@ struct TileFinder {
     const int type = (int)(meta >> kGradLastBits);
     const uint32_t from = tab.tile0[k], to = tab.tile0[k + 1];
     const int last = (int)(meta & ((1u << kGradLastBits) - 1)) * (type == kGradF32 ? 4 : 2);
-    return GradTile{k, type, t + 1 == to ? last : kGradTileBytes, to - from == 1 && last < 16,
+    return GradTile{tab.in[k], k, type, t + 1 == to ? last : kGradTileBytes, to - from == 1 && last < 16,
                     (int64_t)(t - from) * kGradTileBytes};
   }
 };
 
-// A tile in registers: four 16-byte vectors a thread of 256, whatever the type.
-constexpr int kTileVecs = kGradTileBytes / 16 / kThreads;
+// A tile in registers: V 16-byte vectors for each of THREADS threads, whatever
+// the type.
+template <int THREADS, int V>
 struct TileData {
-  u32x4 v[kTileVecs];
+  u32x4 v[V];
+  static __device__ __forceinline__ int thread() { return (int)(threadIdx.x % THREADS); }
+  static __device__ __forceinline__ int at(int i) { return (i * THREADS + thread()) * 16; }
+
+  template <int LK>
+  __device__ __forceinline__ void load(const char* tile, int bytes) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = load16<LK>(tile, at(i), bytes);
+  }
+  // Waits for the loads of a tile that is not used, so that no path leaves
+  // them pending (its registers' next loads would wait for all others).
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) asm volatile("" ::"v"(v[i]));
+  }
+  __device__ __forceinline__ void fix(int bytes) {
+    if (bytes == THREADS * V * 16) return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = fix16<kLoadCached>(v[i], at(i), bytes);
+  }
 };
+using BigTile = TileData<kThreads, kGradTileBytes / 16 / kThreads>;
+using SmallTile = TileData<64, kGradShortTileBytes / 16 / 64>;
 
 constexpr int kWaves = kThreads / 64;
-__device__ __forceinline__ int tile_thread() { return (int)(threadIdx.x % kThreads); }
-__device__ __forceinline__ int vec_at(int i) { return (i * kThreads + tile_thread()) * 16; }
 
-template <int LK>
-__device__ __forceinline__ TileData load_tile(const char* tile, int bytes) {
-  TileData d;
-#pragma unroll
-  for (int i = 0; i < kTileVecs; ++i) d.v[i] = load16<LK>(tile, vec_at(i), bytes);
-  return d;
-}
-
-__device__ __forceinline__ void fix_tile(TileData& d, int bytes) {
-#pragma unroll
-  for (int i = 0; i < kTileVecs; ++i) d.v[i] = fix16<kLoadCached>(d.v[i], vec_at(i), bytes);
-}
-
-template <int DT>
-__device__ __forceinline__ double tile_squares(const TileData& d) {
+template <int DT, int THREADS, int V>
+__device__ __forceinline__ double tile_squares(const TileData<THREADS, V>& d) {
   double s = 0.0;
 #pragma unroll
-  for (int i = 0; i < kTileVecs; ++i) {
+  for (int i = 0; i < V; ++i) {
     float f[OpElem<DT>::kPack];
     unpack<DT>(d.v[i], f);
 #pragma unroll
@@ -89,7 +97,8 @@ __device__ __forceinline__ double tile_squares(const TileData& d) {
   return s;
 }
 
-__device__ __forceinline__ double squares_of(const TileData& d, int type) {
+template <typename TILE>
+__device__ __forceinline__ double squares_of(const TILE& d, int type) {
   switch (type) {
     case kGradF32: return tile_squares<RINGSIM_FLOAT32>(d);
     case kGradBF16: return tile_squares<RINGSIM_BFLOAT16>(d);
@@ -97,46 +106,64 @@ __device__ __forceinline__ double squares_of(const TileData& d, int type) {
   }
 }
 
-// Element i of a tensor of any type.
-__device__ __forceinline__ float grad_elem(const void* p, int type, int i) {
-  if (type == kGradF32) return static_cast<const float*>(p)[i];
-  const uint16_t e = static_cast<const uint16_t*>(p)[i];
-  return type == kGradBF16 ? elem_to_f32<RINGSIM_BFLOAT16>(e) : elem_to_f32<RINGSIM_FLOAT16>(e);
+typedef __attribute__((address_space(1))) uint16_t GlobalHalf;
+
+// Element i of a tensor shorter than a vector (thread i has it): its two
+// halves as they lie in memory (the same half twice for a 16-bit type), and
+// its value, 0 beyond the tensor.
+struct Halves {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Halves small_load(const void* in, int size, int n, int i) {
+  const GlobalHalf* p = (const GlobalHalf*)(static_cast<const char*>(in) + (i < n ? i : n - 1) * size);
+  return Halves{p[0], p[size / 2 - 1]};
+}
+__device__ __forceinline__ float small_value(Halves h, int type, int n, int i) {
+  const float e = type == kGradF32    ? __uint_as_float(h.lo | h.hi << 16)
+                  : type == kGradBF16 ? elem_to_f32<RINGSIM_BFLOAT16>((uint16_t)h.lo)
+                                      : elem_to_f32<RINGSIM_FLOAT16>((uint16_t)h.lo);
+  return i < n ? e : 0.0f;
+}
+__device__ __forceinline__ float small_elem(const GradTile& g, int i) {
+  const int size = g.type == kGradF32 ? 4 : 2, n = g.bytes / size;
+  return small_value(small_load(g.in, size, n, i), g.type, n, i);
 }
 
-// The squares of a tensor shorter than a vector, one element a thread.
-__device__ __forceinline__ double small_squares(const void* in, const GradTile& g) {
-  const int i = tile_thread(), n = g.bytes / (g.type == kGradF32 ? 4 : 2);
-  const double e = i < n ? (double)grad_elem(in, g.type, i) : 0.0;
-  return e * e;
-}
+// 16 bytes that can be read: where a thread's load is not wanted, but stands
+// under no condition since a wait that some path reaches without it would
+// wait for everything, it reads these.
+__device__ const u32x4 g_spare = {0, 0, 0, 0};
+__device__ __forceinline__ const char* spare_bytes() { return reinterpret_cast<const char*>(&g_spare); }
 
 // The squares of tiles t, t + step, ... below `end`; t is left at the first
 // one at or past it. One tile ahead: the next one's loads are under way
 // while this one's squares are added (40 buckets of 25 MiB: 160 us, without
 // 166). The two tiles take turns in two sets of registers, since moving a
-// loaded vector waits for it, and the loads stand under no condition, since a
-// wait that some path reaches without them waits for everything: where there
-// is no next tile, and for a tensor shorter than a vector, the lanes read 16
-// bytes of `spare` for nothing. Such a tensor's elements are read when its
+// loaded vector waits for it. A tensor shorter than a vector is read when its
 // turn comes.
 template <int LK>
 __device__ __forceinline__ double walk_squares(const GradSquareTable& tab, const TileFinder<GradSquareTable>& finder,
-                                               uint32_t& t, uint32_t end, uint32_t step, const void* spare) {
+                                               uint32_t& t, uint32_t end, uint32_t step) {
   if (t >= end) return 0.0;
   const auto load = [&](const GradTile& g, bool wanted) {
     const bool real = wanted && !g.small;
-    const char* p = static_cast<const char*>(real ? tab.in[g.tensor] : spare) + (real ? g.first : 0);
-    return load_tile<LK>(p, real ? g.bytes : 16);
+    const char* p = real ? static_cast<const char*>(g.in) + g.first : spare_bytes();
+    BigTile d;
+    d.load<LK>(p, real ? g.bytes : 16);
+    return d;
   };
-  const auto squares = [&](TileData& d, const GradTile& g) {
-    if (g.small) return small_squares(tab.in[g.tensor], g);
-    if (g.bytes != kGradTileBytes) fix_tile(d, g.bytes);
+  const auto squares = [&](BigTile& d, const GradTile& g) {
+    if (g.small) {
+      d.settle();
+      const double e = (double)small_elem(g, BigTile::thread());
+      return e * e;
+    }
+    d.fix(g.bytes);
     return squares_of(d, g.type);
   };
   double s = 0.0;
   GradTile ga = finder.find(tab, t), gb;
-  TileData da = load(ga, true), db;
+  BigTile da = load(ga, true), db;
   for (;;) {
     t += step;
     gb = finder.find(tab, t < end ? t : end - 1);
@@ -171,8 +198,8 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t tiles = tab.tile0[tab.ntensors];
   const TileFinder<GradSquareTable> finder(tab);
   uint32_t t = blockIdx.x;
-  double s = walk_squares<kLoadStream>(tab, finder, t, tiles - keep, gridDim.x, partial);
-  s += walk_squares<kLoadCached>(tab, finder, t, tiles, gridDim.x, partial);
+  double s = walk_squares<kLoadStream>(tab, finder, t, tiles - keep, gridDim.x);
+  s += walk_squares<kLoadCached>(tab, finder, t, tiles, gridDim.x);
   s = block_sum<kWaves>(s, lds);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
@@ -205,36 +232,37 @@ __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* 
   if (threadIdx.x == 0) *norm = v;
 }
 
-template <int DT>
-__device__ __forceinline__ void tile_scale(const TileData& d, int bytes, char* out, float factor) {
+template <int DT, int THREADS, int V>
+__device__ __forceinline__ void scale_vecs(const TileData<THREADS, V>& d, int bytes, char* out, float factor) {
 #pragma unroll
-  for (int i = 0; i < kTileVecs; ++i) {
+  for (int i = 0; i < V; ++i) {
     float f[OpElem<DT>::kPack];
     unpack<DT>(d.v[i], f);
 #pragma unroll
     for (int j = 0; j < OpElem<DT>::kPack; ++j) f[j] *= factor;
-    store16<true>(out, to_pack<DT>(f), vec_at(i), bytes);
+    store16<true>(out, to_pack<DT>(f), d.at(i), bytes);
   }
 }
 
-// Writes a tile in registers, scaled.
-__device__ __forceinline__ void scale_tile(const TileData& d, const GradTile& g, const void* in, void* out, float f) {
+// Writes a tile in registers, scaled; `e` is the thread's element of a tensor
+// shorter than a vector.
+template <typename TILE>
+__device__ __forceinline__ void scale_tile(const TILE& d, const GradTile& g, float e, void* out, float f) {
+  char* to = static_cast<char*>(out) + g.first;
   if (g.small) {
-    const int i = tile_thread();
+    const int i = TILE::thread();
     if (i >= g.bytes / (g.type == kGradF32 ? 4 : 2)) return;
-    const float e = grad_elem(in, g.type, i) * f;
     if (g.type == kGradF32)
-      static_cast<float*>(out)[i] = e;
+      reinterpret_cast<float*>(to)[i] = e * f;
     else
-      static_cast<uint16_t*>(out)[i] =
-          g.type == kGradBF16 ? f32_to_elem<RINGSIM_BFLOAT16>(e) : f32_to_elem<RINGSIM_FLOAT16>(e);
+      reinterpret_cast<uint16_t*>(to)[i] =
+          g.type == kGradBF16 ? f32_to_elem<RINGSIM_BFLOAT16>(e * f) : f32_to_elem<RINGSIM_FLOAT16>(e * f);
     return;
   }
-  char* to = static_cast<char*>(out) + g.first;
   switch (g.type) {
-    case kGradF32: tile_scale<RINGSIM_FLOAT32>(d, g.bytes, to, f); break;
-    case kGradBF16: tile_scale<RINGSIM_BFLOAT16>(d, g.bytes, to, f); break;
-    default: tile_scale<RINGSIM_FLOAT16>(d, g.bytes, to, f); break;
+    case kGradF32: scale_vecs<RINGSIM_FLOAT32>(d, g.bytes, to, f); break;
+    case kGradBF16: scale_vecs<RINGSIM_BFLOAT16>(d, g.bytes, to, f); break;
+    default: scale_vecs<RINGSIM_FLOAT16>(d, g.bytes, to, f); break;
   }
 }
 
@@ -263,60 +291,97 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(GradScaleTable tab
   const uint32_t tiles = tab.tile0[tab.ntensors];
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const GradTile g = finder.find(tab, tiles - 1 - t);
-    const void* in = tab.in[g.tensor];
-    TileData d;
-    if (!g.small) {
-      d = load_tile<kLoadStream>(static_cast<const char*>(in) + g.first, g.bytes);
-      if (g.bytes != kGradTileBytes) fix_tile(d, g.bytes);
+    BigTile d;
+    float e = 0.0f;
+    if (g.small) {
+      e = small_elem(g, BigTile::thread());
+    } else {
+      d.load<kLoadStream>(static_cast<const char*>(g.in) + g.first, g.bytes);
+      d.fix(g.bytes);
     }
-    scale_tile(d, g, in, tab.out[g.tensor], f);
+    scale_tile(d, g, e, tab.out[g.tensor], f);
   }
 }
 
-// Norm and scaling of a list of at most kGradSmallTiles tiles by one
-// workgroup: every tile is read once and stays in registers until it is
-// scaled, and there is one launch instead of two. A call takes 4.4 us for one
-// tensor of 4 KiB and 5.0 (norm) or 6.8 (clip) for 192 KiB, the 12 tiles that
-// are the limit; two launches take 8.8 and 9.7. In a graph, where a launch
-// costs less, 12 tiles are even (4.5 and 6.6 against 4.8 and 6.1), 16 lose.
-__global__ void __launch_bounds__(kGradSmallThreads)
-    grad_small_kernel(GradSmallTable tab, GradFactor fac, int clip, int in_place) {
-  constexpr int kGroups = kGradSmallThreads / kThreads, kRounds = kGradSmallTiles / kGroups;
-  __shared__ double lds[kGradSmallThreads / 64];
-  const uint32_t tiles = tab.tile0[tab.ntensors];
-  const TileFinder<GradSmallTable> finder(tab);
-  const uint32_t group = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
-  TileData d[kRounds];
-  GradTile g[kRounds];
+// A value of lane k, the same for the whole wave afterwards.
+template <typename P>
+__device__ __forceinline__ P* lane_ptr(P* p, int k) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, k), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), k);
+  return reinterpret_cast<P*>((uint64_t)hi << 32 | lo);
+}
+
+// Norm and scaling of a short list by one workgroup: every tile is read once
+// and stays in registers until it is scaled, and there is one launch instead
+// of two. A call takes 4.3 us for the norm and 4.6 for the clipping of one
+// tensor of 4 KiB, 4.9 and 5.3 for 34 tensors of 600 bytes, 5.4 and 8.6 for
+// one of 192 KiB, the most it holds; two launches take 8.8 and 9.7. In a
+// graph, where a launch costs less, 192 KiB take 5.0 and 8.3 against 4.8 and
+// 6.1, 64 KiB 3.1 and 4.4.
+// Lane k of a wave reads the table for the wave's round k, and all loads of
+// tiles are under way before the first is used: what a call waits for is the
+// table, the tiles and the barrier.
+template <int ROUNDS>
+__global__ void __launch_bounds__(kGradShortWaves * 64)
+    grad_short_kernel(GradShortTable tab, GradFactor fac, int clip, int in_place) {
+  __shared__ double lds[kGradShortWaves];
+  const int lane = SmallTile::thread();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const auto wanted = [&](int k) { return wave + k * kGradShortWaves < tab.tiles; };
+  const void* in = spare_bytes();
+  void* out = nullptr;
+  uint32_t meta = kGradBF16 << 12 | 16;
+  if (lane < ROUNDS && wanted(lane)) {
+    in = tab.in[wave + lane * kGradShortWaves];
+    out = tab.out[wave + lane * kGradShortWaves];
+    meta = tab.meta[wave + lane * kGradShortWaves];
+  }
+  GradTile g[ROUNDS];
+  SmallTile d[ROUNDS];
+  float e[ROUNDS];
+  bool small = false;
 #pragma unroll
-  for (int k = 0; k < kRounds; ++k) {
-    const uint32_t t = group + k * kGroups;
-    if (t >= tiles) continue;
-    g[k] = finder.find(tab, t);
-    if (!g[k].small) d[k] = load_tile<kLoadCached>(static_cast<const char*>(tab.in[g[k].tensor]) + g[k].first, g[k].bytes);
+  for (int k = 0; k < ROUNDS; ++k) {
+    const uint32_t m = __builtin_amdgcn_readlane(meta, k);
+    g[k] = GradTile{lane_ptr(in, k), k, (int)(m >> 12), (int)(m & 2047), (m >> 11 & 1) != 0, 0};
+    d[k].template load<kLoadCached>(g[k].small ? spare_bytes() : static_cast<const char*>(g[k].in),
+                                    g[k].small ? 16 : g[k].bytes);
+    small = small || g[k].small;
+    e[k] = 0.0f;
+  }
+  if (small) {
+    Halves h[ROUNDS];
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+      const int size = g[k].type == kGradF32 ? 4 : 2;
+      h[k] = small_load(g[k].small ? g[k].in : spare_bytes(), size, g[k].small ? g[k].bytes / size : 1, lane);
+    }
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) asm volatile("" : "+v"(h[k].lo), "+v"(h[k].hi));
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k)
+      e[k] = small_value(h[k], g[k].type, g[k].bytes / (g[k].type == kGradF32 ? 4 : 2), lane);
   }
   double s = 0.0;
 #pragma unroll
-  for (int k = 0; k < kRounds; ++k) {
-    if (group + k * kGroups >= tiles) continue;
+  for (int k = 0; k < ROUNDS; ++k) {
+    if (!wanted(k)) continue;
     if (g[k].small) {
-      s += small_squares(tab.in[g[k].tensor], g[k]);
-      continue;
+      s += (double)e[k] * (double)e[k];
+    } else {
+      d[k].fix(g[k].bytes);
+      s += squares_of(d[k], g[k].type);
     }
-    if (g[k].bytes != kGradTileBytes) fix_tile(d[k], g[k].bytes);
-    s += squares_of(d[k], g[k].type);
   }
-  s = block_sum<kGradSmallThreads / 64>(s, lds);
+  s = block_sum<kGradShortWaves>(s, lds);
   const float norm = norm_of(s, fac.scale);
   if (threadIdx.x == 0) *fac.norm = norm;
   if (!clip) return;
   const float f = factor_of(norm, fac);
   if (in_place && f == 1.0f) return;
 #pragma unroll
-  for (int k = 0; k < kRounds; ++k) {
-    if (group + k * kGroups >= tiles) continue;
-    scale_tile(d[k], g[k], tab.in[g[k].tensor], tab.out[g[k].tensor], f);
-  }
+  for (int k = 0; k < ROUNDS; ++k)
+    if (wanted(k)) scale_tile(d[k], g[k], e[k], lane_ptr(out, k), f);
 }
 
 hipError_t launch_grad_squares(const GradSquareTable& t, uint32_t keep, double* partial, int workgroups,
@@ -330,8 +395,14 @@ hipError_t launch_grad_norm_join(const double* partial, int parts, float scale, 
   return hipGetLastError();
 }
 
-hipError_t launch_grad_small(const GradSmallTable& t, const GradFactor& f, int clip, int in_place, hipStream_t s) {
-  hipLaunchKernelGGL(grad_small_kernel, dim3(1), dim3(kGradSmallThreads), 0, s, t, f, clip, in_place);
+hipError_t launch_grad_short(const GradShortTable& t, const GradFactor& f, int clip, int in_place, hipStream_t s) {
+  const dim3 grid(1), block(kGradShortWaves * 64);
+  if (t.tiles <= kGradShortWaves)
+    hipLaunchKernelGGL(grad_short_kernel<1>, grid, block, 0, s, t, f, clip, in_place);
+  else if (t.tiles <= 4 * kGradShortWaves)
+    hipLaunchKernelGGL(grad_short_kernel<4>, grid, block, 0, s, t, f, clip, in_place);
+  else
+    hipLaunchKernelGGL(grad_short_kernel<kGradShortRounds>, grid, block, 0, s, t, f, clip, in_place);
   return hipGetLastError();
 }
 

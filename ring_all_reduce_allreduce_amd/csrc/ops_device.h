@@ -54,6 +54,10 @@ __device__ __forceinline__ typename OpElem<DT>::T f32_to_elem(float f) {
   }
 }
 
+// A vector in device memory: said so, the load needs no test for LDS addresses
+// where the compiler cannot tell where a pointer comes from.
+typedef __attribute__((address_space(1))) u32x4_e2 GlobalVec;
+
 // How a kernel reads its rows: through the caches, past them (data that the
 // Infinity Cache will not hold until it is needed again), or element by
 // element, for rows shorter than a vector.
@@ -78,7 +82,7 @@ __device__ __forceinline__ u32x4 load16(const void* p, int at, int bytes) {
     return u32x4{w[0], w[1], w[2], w[3]};
   } else {
     const int start = at < bytes - 16 ? at : bytes - 16;
-    const u32x4_e2* q = reinterpret_cast<const u32x4_e2*>(c + start);
+    const GlobalVec* q = (const GlobalVec*)(c + start);
     return LK == kLoadStream ? __builtin_nontemporal_load(q) : *q;
   }
 }

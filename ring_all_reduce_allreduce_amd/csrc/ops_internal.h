@@ -93,10 +93,24 @@ struct GradTable {
   uint32_t meta[N / 2];  // two tensors a word: GradType << kGradLastBits | elements of the last tile
   int ntensors;
 };
-// A list of at most this many tiles is one workgroup's: it keeps them in
-// registers, three for each 256 of its 1024 threads.
-constexpr int kGradSmallTiles = 12;
-constexpr int kGradSmallThreads = 1024;
+// A short list is one workgroup's, which keeps it in registers: tiles of 1
+// KiB, one for each wave and round. Its table says for every tile where it
+// lies, so there is nothing to look up.
+constexpr int kGradShortTileBytes = 1024;
+constexpr int kGradShortWaves = 16;
+constexpr int kGradShortRounds = 12;
+constexpr int kGradShortTiles = kGradShortWaves * kGradShortRounds;
+struct GradShortTable {
+  const void* in[kGradShortTiles];
+  void* out[kGradShortTiles];
+  // GradType << 12 | tensor shorter than a vector << 11 | bytes of the tile. 32
+  // bits though 14 would do: a scalar load drops the two lowest bits of its
+  // base and of its offset each, and an index that a 16-bit array shares with
+  // the pointers is split by the compiler into parts that have them.
+  uint32_t meta[kGradShortTiles];
+  int tiles;
+};
+static_assert(sizeof(GradShortTable) <= 4000, "kernel arguments");
 
 using GradSquareTable = GradTable<kGradSquareTensors>;
 template <int N>
@@ -104,7 +118,6 @@ struct GradOutTable : GradTable<N> {
   void* out[N];
 };
 using GradScaleTable = GradOutTable<kGradScaleTensors>;
-using GradSmallTable = GradOutTable<kGradSmallTiles>;
 static_assert(sizeof(GradSquareTable) <= 4000 && sizeof(GradScaleTable) <= 4000, "kernel arguments");
 
 // The last `keep` tiles are read so that they stay in the Infinity Cache.
@@ -116,8 +129,8 @@ struct GradFactor {
   float* norm;            // partial null: read the norm here; else workgroup 0 writes it here, if not null
   float scale, max_norm, eps;
 };
-// Norm and, if `clip`, scaling of a small list in one launch; f.partial is not read.
-hipError_t launch_grad_small(const GradSmallTable& t, const GradFactor& f, int clip, int in_place, hipStream_t s);
+// Norm and, if `clip`, scaling of a short list in one launch; f.partial is not read.
+hipError_t launch_grad_short(const GradShortTable& t, const GradFactor& f, int clip, int in_place, hipStream_t s);
 hipError_t launch_grad_scale(const GradScaleTable& t, const GradFactor& f, int in_place, int workgroups, hipStream_t s);
 
 }  // namespace ringsim

@@ -57,7 +57,14 @@ LISTS = {
     "a tile": ([8192], [BF16]),
     "a tile and one": ([4097], [F32]),
     "tile borders": ([8191, 8192, 8193, 16384, 16385], [BF16, F16, BF16, F16, BF16]),
-    "16 tiles": ([8192 * 15, 4095], [BF16, F32]),
+    "16 short tiles": ([512 * 15, 255], [BF16, F32]),
+    "17 short tiles": ([512 * 16 + 1], [F16]),
+    "64 short tiles": ([512 * 30 + 7, 256 * 20, 100, 512 * 11 + 1], [F16, F32, F32, BF16]),
+    "65 short tiles": ([1] * 65, [BF16] * 65),
+    "192 short tiles": ([512] * 100 + [256] * 91 + [3], [F16] * 100 + [F32] * 92),
+    "192 KiB": ([49152], [F32]),
+    "192 KiB and one": ([98305], [BF16]),
+    "193 short tiles": ([512] * 193, [BF16] * 193),
     "16 whole tiles": ([4096 * 16], [F32]),
     "17 tiles": ([8192 * 16 + 1], [F16]),
     "16 small ones": ([i % 9 for i in range(1, 17)], [F32, BF16, F16, BF16] * 4),
