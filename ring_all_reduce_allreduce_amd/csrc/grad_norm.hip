@@ -169,12 +169,18 @@ __device__ __forceinline__ double walk_squares(const GradSquareTable& tab, const
     gb = finder.find(tab, t < end ? t : end - 1);
     db = load(gb, t < end);
     s += squares(da, ga);
-    if (t >= end) return s;
+    if (t >= end) {
+      db.settle();
+      return s;
+    }
     t += step;
     ga = finder.find(tab, t < end ? t : end - 1);
     da = load(ga, t < end);
     s += squares(db, gb);
-    if (t >= end) return s;
+    if (t >= end) {
+      da.settle();
+      return s;
+    }
   }
 }
 

@@ -74,7 +74,11 @@ hipError_t launch_rms_norm_weight_sum(const float* partial, int parts, int cols,
 // Tables travel as kernel arguments (below 4 KiB), which a graph's capture
 // keeps by itself.
 constexpr int kGradTileBytes = 16384;
-constexpr int kGradWorkgroups = 1024;  // most of a launch
+constexpr int kGradWorkgroups = 1024;  // most of a launch that leaves a sum each
+// Scaling takes a workgroup a tile: the hardware starts the next one while
+// this one's stores drain. 40 buckets of 25 MiB take 332 us so, with 1024
+// workgroups that walk the tiles 365, although each joins the sums for itself.
+constexpr uint32_t kGradScaleWorkgroups = 1u << 22;
 constexpr int kGradSquareTensors = 280;
 constexpr int kGradScaleTensors = 180;
 

@@ -126,6 +126,7 @@ void set_outs(TABLE& t, const void* const* grads, void* const* outs, const int* 
 }
 
 int grad_workgroups(uint32_t tiles) { return (int)std::min<uint32_t>(tiles, kGradWorkgroups); }
+int grad_scale_workgroups(uint32_t tiles) { return (int)std::min<uint32_t>(tiles, kGradScaleWorkgroups); }
 
 // Sums of squares of every launch's workgroups into the workspace. `left`:
 // tiles still to come. `keep` bytes at the end are read so that they stay in
@@ -155,7 +156,7 @@ ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* out
     const uint32_t tiles = fill_table(t, n, grads, counts, dtypes, &next, index);
     if (tiles == 0) continue;
     set_outs(t, grads, outs, index);
-    if (launch_grad_scale(t, f, outs == nullptr, grad_workgroups(tiles), s) != hipSuccess)
+    if (launch_grad_scale(t, f, outs == nullptr, grad_scale_workgroups(tiles), s) != hipSuccess)
       return RINGSIM_UNHANDLED_DEVICE_ERROR;
     if (f.partial) f.norm = nullptr;  // the first launch writes it
   }
