@@ -45,12 +45,13 @@ struct TileFinder {
     int k = -1;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) k += __builtin_popcountll(__builtin_amdgcn_ballot_w64(first[i] <= t));
-    const uint32_t meta = tab.meta[k / 2] >> (16 * (k % 2)) & 0xffffu;
+    const uint64_t in = tab.in[k];
+    const uint32_t meta = (uint32_t)(in >> kGradAddressBits);
     const int type = (int)(meta >> kGradLastBits);
     const uint32_t from = tab.tile0[k], to = tab.tile0[k + 1];
     const int last = (int)(meta & ((1u << kGradLastBits) - 1)) * (type == kGradF32 ? 4 : 2);
-    return GradTile{tab.in[k], k, type, t + 1 == to ? last : kGradTileBytes, to - from == 1 && last < 16,
-                    (int64_t)(t - from) * kGradTileBytes};
+    return GradTile{reinterpret_cast<const void*>(in & ((1ull << kGradAddressBits) - 1)), k, type,
+                    t + 1 == to ? last : kGradTileBytes, to - from == 1 && last < 16, (int64_t)(t - from) * kGradTileBytes};
   }
 };
 
@@ -142,7 +143,7 @@ __device__ __forceinline__ const char* spare_bytes() { return reinterpret_cast<c
 // loaded vector waits for it. A tensor shorter than a vector is read when its
 // turn comes.
 template <int LK>
-__device__ __forceinline__ double walk_squares(const GradSquareTable& tab, const TileFinder<GradSquareTable>& finder,
+__device__ __forceinline__ double walk_squares(const GradTable& tab, const TileFinder<GradTable>& finder,
                                                uint32_t& t, uint32_t end, uint32_t step) {
   if (t >= end) return 0.0;
   const auto load = [&](const GradTile& g, bool wanted) {
@@ -199,10 +200,10 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 }
 
 __global__ void __launch_bounds__(kThreads)
-    grad_squares_kernel(GradSquareTable tab, uint32_t keep, double* partial) {
+    grad_squares_kernel(GradTable tab, uint32_t keep, double* partial) {
   __shared__ double lds[kWaves];
   const uint32_t tiles = tab.tile0[tab.ntensors];
-  const TileFinder<GradSquareTable> finder(tab);
+  const TileFinder<GradTable> finder(tab);
   uint32_t t = blockIdx.x;
   double s = walk_squares<kLoadStream>(tab, finder, t, tiles - keep, gridDim.x);
   s += walk_squares<kLoadCached>(tab, finder, t, tiles, gridDim.x);
@@ -280,11 +281,13 @@ __device__ __forceinline__ float factor_of(float norm, const GradFactor& fac) {
   return (float)(c * (double)fac.scale);
 }
 
-// Walks the tiles from the last to the first: what the norm's pass read last
+// Takes the tiles from the last to the first: what the norm's pass read last
 // is still in the Infinity Cache.
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(GradScaleTable tab, GradFactor fac, int in_place) {
+template <typename TABLE>
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(TABLE tab, GradFactor fac) {
+  constexpr bool kInPlace = std::is_same_v<TABLE, GradTable>;
   __shared__ double lds[kWaves];
-  const TileFinder<GradScaleTable> finder(tab);
+  const TileFinder<TABLE> finder(tab);
   float norm;
   if (fac.partial) {
     norm = join_norm(fac.partial, fac.parts, fac.scale, lds);
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(GradScaleTable tab
     norm = *fac.norm;
   }
   const float f = factor_of(norm, fac);
-  if (in_place && f == 1.0f) return;
+  if (kInPlace && f == 1.0f) return;
   const uint32_t tiles = tab.tile0[tab.ntensors];
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const GradTile g = finder.find(tab, tiles - 1 - t);
@@ -305,7 +308,10 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(GradScaleTable tab
       d.load<kLoadStream>(static_cast<const char*>(g.in) + g.first, g.bytes);
       d.fix(g.bytes);
     }
-    scale_tile(d, g, e, tab.out[g.tensor], f);
+    if constexpr (kInPlace)
+      scale_tile(d, g, e, const_cast<void*>(g.in), f);
+    else
+      scale_tile(d, g, e, tab.out[g.tensor], f);
   }
 }
 
@@ -390,7 +396,7 @@ __global__ void __launch_bounds__(kGradShortWaves * 64)
     if (wanted(k)) scale_tile(d[k], g[k], e[k], lane_ptr(out, k), f);
 }
 
-hipError_t launch_grad_squares(const GradSquareTable& t, uint32_t keep, double* partial, int workgroups,
+hipError_t launch_grad_squares(const GradTable& t, uint32_t keep, double* partial, int workgroups,
                                hipStream_t s) {
   hipLaunchKernelGGL(grad_squares_kernel, dim3(workgroups), dim3(kThreads), 0, s, t, keep, partial);
   return hipGetLastError();
@@ -412,10 +418,16 @@ hipError_t launch_grad_short(const GradShortTable& t, const GradFactor& f, int c
   return hipGetLastError();
 }
 
-hipError_t launch_grad_scale(const GradScaleTable& t, const GradFactor& f, int in_place, int workgroups,
-                             hipStream_t s) {
-  hipLaunchKernelGGL(grad_scale_kernel, dim3(workgroups), dim3(kThreads), 0, s, t, f, in_place);
+template <typename TABLE>
+static hipError_t launch_scale(const TABLE& t, const GradFactor& f, int workgroups, hipStream_t s) {
+  hipLaunchKernelGGL(grad_scale_kernel<TABLE>, dim3(workgroups), dim3(kThreads), 0, s, t, f);
   return hipGetLastError();
+}
+hipError_t launch_grad_scale(const GradScaleTable& t, const GradFactor& f, int workgroups, hipStream_t s) {
+  return launch_scale(t, f, workgroups, s);
+}
+hipError_t launch_grad_scale(const GradTable& t, const GradFactor& f, int workgroups, hipStream_t s) {
+  return launch_scale(t, f, workgroups, s);
 }
 
 }  // namespace ringsim

@@ -79,8 +79,8 @@ constexpr int kGradWorkgroups = 1024;  // most of a launch that leaves a sum eac
 // this one's stores drain. 40 buckets of 25 MiB take 332 us so, with 1024
 // workgroups that walk the tiles 365, although each joins the sums for itself.
 constexpr uint32_t kGradScaleWorkgroups = 1u << 22;
-constexpr int kGradSquareTensors = 280;
-constexpr int kGradScaleTensors = 180;
+constexpr int kGradTensors = 330;     // of a launch that reads, or writes in place
+constexpr int kGradOutTensors = 196;  // of one that writes elsewhere
 
 // Type and last tile of a tensor in 16 bits.
 enum GradType : int { kGradF32 = 0, kGradBF16 = 1, kGradF16 = 2 };
@@ -89,14 +89,25 @@ constexpr int grad_type(int dtype) {
 }
 constexpr int kGradLastBits = 14;  // elements of a tensor's last tile: up to 8192
 
+// An address has 48 bits (the host refuses others); the 16 above them hold
+// GradType << kGradLastBits | elements of the last tile.
+constexpr int kGradAddressBits = 48;
+
 template <int N>
-struct GradTable {
+struct GradInTable {
   static constexpr int kTensors = N;
-  const void* in[N];
+  uint64_t in[N];
   uint32_t tile0[N + 1];
-  uint32_t meta[N / 2];  // two tensors a word: GradType << kGradLastBits | elements of the last tile
   int ntensors;
 };
+template <int N>
+struct GradOutTable : GradInTable<N> {
+  void* out[N];
+};
+using GradTable = GradInTable<kGradTensors>;
+using GradScaleTable = GradOutTable<kGradOutTensors>;
+static_assert(sizeof(GradTable) <= 4000 && sizeof(GradScaleTable) <= 4000, "kernel arguments");
+
 // A short list is one workgroup's, which keeps it in registers: tiles of 1
 // KiB, one for each wave and round. Its table says for every tile where it
 // lies, so there is nothing to look up.
@@ -116,16 +127,8 @@ struct GradShortTable {
 };
 static_assert(sizeof(GradShortTable) <= 4000, "kernel arguments");
 
-using GradSquareTable = GradTable<kGradSquareTensors>;
-template <int N>
-struct GradOutTable : GradTable<N> {
-  void* out[N];
-};
-using GradScaleTable = GradOutTable<kGradScaleTensors>;
-static_assert(sizeof(GradSquareTable) <= 4000 && sizeof(GradScaleTable) <= 4000, "kernel arguments");
-
 // The last `keep` tiles are read so that they stay in the Infinity Cache.
-hipError_t launch_grad_squares(const GradSquareTable& t, uint32_t keep, double* partial, int workgroups, hipStream_t s);
+hipError_t launch_grad_squares(const GradTable& t, uint32_t keep, double* partial, int workgroups, hipStream_t s);
 hipError_t launch_grad_norm_join(const double* partial, int parts, float scale, float* norm, hipStream_t s);
 struct GradFactor {
   const double* partial;  // join these into the norm, or
@@ -135,6 +138,8 @@ struct GradFactor {
 };
 // Norm and, if `clip`, scaling of a short list in one launch; f.partial is not read.
 hipError_t launch_grad_short(const GradShortTable& t, const GradFactor& f, int clip, int in_place, hipStream_t s);
-hipError_t launch_grad_scale(const GradScaleTable& t, const GradFactor& f, int in_place, int workgroups, hipStream_t s);
+hipError_t launch_grad_scale(const GradScaleTable& t, const GradFactor& f, int workgroups, hipStream_t s);
+// The same in place.
+hipError_t launch_grad_scale(const GradTable& t, const GradFactor& f, int workgroups, hipStream_t s);
 
 }  // namespace ringsim

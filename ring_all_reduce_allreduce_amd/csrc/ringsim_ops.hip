@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "ops_internal.h"
 #include "ringsim_host.h"
@@ -90,7 +91,7 @@ bool valid_grads(int n, const void* const* grads, void* const* outs, const int64
     const int e = op_dtype_size(dtypes[i]);
     tiles += tiles_of(counts[i], dtypes[i]);
     if (tiles > INT32_MAX) return false;
-    if (!grads[i] || !aligned(grads[i], e)) return false;
+    if (!grads[i] || !aligned(grads[i], e) || reinterpret_cast<uintptr_t>(grads[i]) >> kGradAddressBits) return false;
     if (outs && (!outs[i] || !aligned(outs[i], e))) return false;
   }
   return true;
@@ -110,19 +111,13 @@ uint32_t fill_table(TABLE& t, int n, const void* const* grads, const int64_t* co
     const int64_t k = tiles_of(counts[i], dtypes[i]);
     const int64_t last = counts[i] - (k - 1) * (kGradTileBytes / op_dtype_size(dtypes[i]));
     const int j = t.ntensors++;
-    t.in[j] = grads[i];
-    const uint32_t meta = (uint32_t)grad_type(dtypes[i]) << kGradLastBits | (uint32_t)last;
-    t.meta[j / 2] = j % 2 ? t.meta[j / 2] | meta << 16 : meta;
+    const uint64_t meta = (uint64_t)grad_type(dtypes[i]) << kGradLastBits | (uint64_t)last;
+    t.in[j] = (uint64_t)reinterpret_cast<uintptr_t>(grads[i]) | meta << kGradAddressBits;
     tiles += (uint32_t)k;
     t.tile0[j + 1] = tiles;
     if (index) index[j] = i;
   }
   return tiles;
-}
-
-template <typename TABLE>
-void set_outs(TABLE& t, const void* const* grads, void* const* outs, const int* index) {
-  for (int j = 0; j < t.ntensors; ++j) t.out[j] = outs ? outs[index[j]] : const_cast<void*>(grads[index[j]]);
 }
 
 int grad_workgroups(uint32_t tiles) { return (int)std::min<uint32_t>(tiles, kGradWorkgroups); }
@@ -136,7 +131,7 @@ ringsim_result_t enqueue_squares(int n, const void* const* grads, const int64_t*
   *parts = 0;
   keep /= kGradTileBytes;
   for (int next = 0; next < n;) {
-    GradSquareTable t;
+    GradTable t;
     const uint32_t tiles = fill_table(t, n, grads, counts, dtypes, &next, nullptr);
     if (tiles == 0) continue;  // the rest of the list was empty
     left -= tiles;
@@ -148,19 +143,26 @@ ringsim_result_t enqueue_squares(int n, const void* const* grads, const int64_t*
   return RINGSIM_SUCCESS;
 }
 
+template <typename TABLE>
 ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* outs, const int64_t* counts,
                                const int* dtypes, GradFactor f, hipStream_t s) {
   for (int next = 0; next < n;) {
-    GradScaleTable t;
-    int index[kGradScaleTensors];
+    TABLE t;
+    int index[TABLE::kTensors];
     const uint32_t tiles = fill_table(t, n, grads, counts, dtypes, &next, index);
     if (tiles == 0) continue;
-    set_outs(t, grads, outs, index);
-    if (launch_grad_scale(t, f, outs == nullptr, grad_scale_workgroups(tiles), s) != hipSuccess)
-      return RINGSIM_UNHANDLED_DEVICE_ERROR;
+    if constexpr (std::is_same_v<TABLE, GradScaleTable>)
+      for (int j = 0; j < t.ntensors; ++j) t.out[j] = outs[index[j]];
+    if (launch_grad_scale(t, f, grad_scale_workgroups(tiles), s) != hipSuccess) return RINGSIM_UNHANDLED_DEVICE_ERROR;
     if (f.partial) f.norm = nullptr;  // the first launch writes it
   }
   return RINGSIM_SUCCESS;
+}
+
+ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* outs, const int64_t* counts,
+                               const int* dtypes, const GradFactor& f, hipStream_t s) {
+  return outs ? enqueue_scale<GradScaleTable>(n, grads, outs, counts, dtypes, f, s)
+              : enqueue_scale<GradTable>(n, grads, outs, counts, dtypes, f, s);
 }
 
 // Tiles of the whole list.
@@ -178,7 +180,7 @@ bool is_short(int n, const int64_t* counts, const int* dtypes) {
 }
 
 size_t norm_workspace(int n) {
-  return sizeof(double) * kGradWorkgroups * (size_t)((n + kGradSquareTensors - 1) / kGradSquareTensors);
+  return sizeof(double) * kGradWorkgroups * (size_t)((n + kGradTensors - 1) / kGradTensors);
 }
 
 bool valid_workspace(const void* ws, size_t bytes, int n) {

@@ -258,8 +258,10 @@ static RowShape backward_shape(int64_t cols, int dtype) {
 }
 
 // So few rows that one workgroup's turns take no longer than a second launch:
-// it writes the weight's gradient itself. (4 rows of 4096 bf16: 7.2 us eager
-// and 6.8 in a graph; 5 rows on 5 workgroups and a second launch 8.8 and 6.1.)
+// it writes the weight's gradient itself. A turn takes 0.6 us (1024 columns
+// fp32) to 1.5 us (4096 bf16), a second launch 3.4 us of a call and 1.5 us in
+// a graph: three rows of 4096 bf16 take 6.8 us a call and 6.4 in a graph, with
+// workgroups of their own 8.9 and 5.8; four would take 8.2 and 7.8.
 constexpr int kOneWorkgroupTurns = 3;
 // Waves a compute unit is given. Each workgroup leaves a row of partial sums,
 // so more of them cost more there than they hide: 16384 rows of 4096 bf16 take

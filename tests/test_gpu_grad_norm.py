@@ -72,6 +72,10 @@ LISTS = {
     "empty ones": ([0, 5, 0, 0, 1000, 0], [F32, F32, BF16, F16, BF16, F32]),
     "all empty": ([0, 0], [F32, BF16]),
     "mixed": ([100_003, 17, 65_536, 3, 250_001], [F32, BF16, F16, F32, BF16]),
+    "196 tensors": ([600 + i for i in range(196)], [F32, BF16] * 98),
+    "197 tensors": ([600 + i for i in range(197)], [F16] * 197),
+    "330 tensors": ([5 * i + 1 for i in range(330)], [BF16, F32] * 165),
+    "331 tensors": ([9000 - 20 * i for i in range(331)], [F32] * 331),
     "128 tensors": ([i * 7 + 1 for i in range(128)], [F32, BF16] * 64),
     "129 tensors": ([i * 7 for i in range(129)], [BF16] * 129),
     "600 tensors": ([(i * 37) % 900 for i in range(600)], [F32, F16, BF16] * 200),

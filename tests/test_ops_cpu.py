@@ -156,7 +156,7 @@ def _list_args(ptrs, counts, types):
 @pytest.mark.parametrize("ptrs, counts, types", [
     ([None], [1], [F32]), ([P + 2], [1], [F32]), ([P + 1], [1], [BF16]), ([P], [-1], [F32]), ([P], [1], [0]),
     ([P], [1], [E4M3]), ([P], [1 << 60], [F32]), ([P], [1 << 50], [BF16]), ([P, None], [1, 5], [F32, F32]),
-    ([P] * 4, [1 << 43] * 4, [F32] * 4),
+    ([P] * 4, [1 << 43] * 4, [F32] * 4), ([1 << 48], [1], [F32]), ([P, 1 << 63], [9, 9], [BF16, F32]),
 ], ids=str)
 def test_gradient_lists_refused(L, ptrs, counts, types):
     n, p, c, t = _list_args(ptrs, counts, types)
