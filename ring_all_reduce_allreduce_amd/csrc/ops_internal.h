@@ -21,7 +21,10 @@ inline int op_dtype_size(int dtype) {
 }
 
 // A call that moves more than the 256 MiB of the Infinity Cache reads its
-// inputs non-temporally: nothing of them will be found there again.
+// inputs non-temporally: nothing of them will be found there again. Norm of
+// 16384 x 8192 fp32 355 us so, 385 through the caches; backward of 16384 x
+// 4096 bf16 96 and 102; norm of 4096 x 4096 bf16 (128 MiB) 24.0 and 20.5, of
+// 4096 x 6144 35.3 and 34.4.
 constexpr int64_t kStreamBytes = 256ll << 20;
 
 // A [outer, inner, cols] tensor: row r is at p + (r / inner) * s0 + (r % inner) * s1 elements.

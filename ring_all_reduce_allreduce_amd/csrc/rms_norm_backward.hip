@@ -208,6 +208,9 @@ __global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_backward_kernel(RmsNo
 // grad_weight[c] = sum over `parts` rows of partial. A workgroup takes 16
 // columns: 16 lanes side by side read a 64-byte line of a row, 64 such groups
 // share the rows out, and their sums are added through LDS in a fixed order.
+// 512 rows of 4096 take 4.3 us and 512 of 1111 2.7: mostly the start of a
+// launch and one trip to sums that other dies wrote (128-byte segments with
+// sums inside the waves first: 4.2 and 3.1).
 constexpr int kSumCols = 16;
 template <int kSumSlices>
 __global__ void __launch_bounds__(kSumCols * kSumSlices)
