@@ -110,7 +110,7 @@ def build(verbose: bool = False) -> str:
         os.replace(tmp_lib, LIB)
         # Loaded by Python, so Python's symbols stay open; libringsim.so is found beside it.
         cmd = [cc, "-shared", "-fPIC", "-o", BINDING + ".tmp", binding_obj, f"-L{torch_lib_dir()}", "-lc10",
-               "-lc10_hip", "-ltorch_cpu", "-ltorch_python", f"-L{PKG}", "-l:libringsim.so", "-Wl,-rpath,$ORIGIN"]
+               "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", f"-L{PKG}", "-l:libringsim.so", "-Wl,-rpath,$ORIGIN"]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)

@@ -2,19 +2,19 @@
 // it.
 //
 //   norm = |scale| sqrt(sum g^2),  out = g * scale * min(1, max_norm / (norm + eps))
-// A launch walks all tensors of its table: each is cut into tiles of 16 KiB,
-// and the workgroups walk the tiles of all tensors with one stride. Squares
-// are summed in fp64: the product of two fp32 values is exact there and
-// cannot leave its range, and the vector unit's fp64 rate is several times
-// what the memory delivers. Workgroups leave one sum each; whoever needs the
-// norm adds these in a fixed order, so no atomics and the same bits every
-// time. Both kernels are bound by memory.
-#include <algorithm>
+// A launch takes all tensors of its table: each is cut into tiles of 16 KiB,
+// which the workgroups share out, walking them with one stride where each
+// leaves a sum (40 buckets of 25 MiB bf16: 6.3-6.6 TB/s), one tile a workgroup
+// where it only writes (6.3 TB/s). Squares are summed in fp64: the product of
+// two fp32 values is exact there and cannot leave its range, and the vector
+// unit's fp64 rate is several times what the memory delivers. Workgroups leave
+// one sum each; whoever needs the norm adds these in a fixed order, so no
+// atomics and the same bits every time. Both kernels are bound by memory.
+#include <type_traits>
 
 #include "ops_device.h"
 
 namespace ringsim {
-
 
 struct GradTile {
   const void* in;

@@ -8,7 +8,6 @@
 
 namespace ringsim {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 // The same vectors at an address that is only aligned to an element: gfx950
 // reads and writes them with one 128-bit access all the same.
 typedef u32x4 u32x4_e2 __attribute__((aligned(2)));
