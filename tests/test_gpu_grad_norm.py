@@ -146,6 +146,22 @@ def test_values_whose_squares_leave_fp32():
     assert abs(float(big.double().square().sum().sqrt()) - 1.0) < 1e-5
 
 
+def test_more_than_2_to_the_31_elements():
+    """One tensor of 2^31 + 9 elements: its norm, and what is written at its
+    start, at its end and where 32 bits wrap."""
+    n = (1 << 31) + 9
+    t = torch.full((n,), 0.5, dtype=BF16, device=DEV)
+    t[-1] = 256.0
+    want = math.sqrt(0.25 * (n - 1) + 65536.0)
+    assert abs(float(rs.grad_norm([t])) - want) <= want * 2 * ref.U
+    norm = rs.clip_grads([t], want / 2, eps=0.0)
+    assert abs(float(norm) - want) <= want * 2 * ref.U
+    assert float(t[-1]) == 128.0
+    for lo in (0, (1 << 30) - 50, (1 << 31) - 50, n - 101):
+        assert bool((t[lo:min(lo + 100, n - 1)] == 0.25).all()), lo
+    assert abs(float(rs.grad_norm([t])) - want / 2) <= want * 2 * ref.U
+
+
 def test_special_values():
     """An infinite norm leaves 0 in finite places and NaN in infinite ones; a
     NaN norm makes everything NaN."""

@@ -317,6 +317,50 @@ def test_backward_against_differences():
         assert abs(float(prod.sum()) - dw) <= slack + 1e-6 * float(prod.abs().sum())
 
 
+def test_backward_special_values_stay_in_their_rows():
+    """What a NaN or an infinity does to its row's gradient and to the columns
+    of the weight's is the formula's; other rows are untouched."""
+    for name, dtype in DTYPES.items():
+        for cols in (300, 2000):
+            h, hd = make((6, cols), dtype, 11)
+            dy, dyd = make((6, cols), dtype, 12)
+            w, wd = weight_of("same", cols, dtype, 1)
+            for t in (h, hd):
+                t[1, 17] = float("nan")
+                t[2, cols - 1] = float("inf")
+            for t in (dy, dyd):
+                t[4, 3] = float("-inf")
+            got = rs.rms_norm_backward(dyd, hd, wd, eps=EPS)
+            dx, _, bound, _ = ref.backward(dy, h, w, None, EPS)
+            keep = [0, 3, 5]
+            ref.within(got.grad_in[keep], dx[keep], bound[keep] + ref.half_step(dx[keep], dtype), f"{name} other rows")
+            for row in (1, 2, 4):
+                assert not bool(torch.isfinite(got.grad_in[row]).any()), (name, row)
+            assert bool(torch.isnan(got.grad_weight).all())  # row 1's root is NaN in every column
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Rows more than 2^31 elements into their memory."""
+    far = 1_200_000_000
+    for name, kind in (("bf16", "same"),):
+        dtype = DTYPES[name]
+        flat = torch.zeros(2 * far + 4096, dtype=dtype, device=DEV)
+        x, xd = make((3, 1000), dtype, 1)
+        r, rd = make((3, 1000), dtype, 2)
+        view = flat.as_strided((3, 1000), (far, 1))
+        view.copy_(xd)
+        w, wd = weight_of(kind, 1000, dtype, 3)
+        got = rs.rms_norm(view, wd, residual=rd, eps=EPS, residual_out=view)
+        check_norm(got, x, r, w, EPS, "far rows")
+        view.copy_(xd)
+        back = rs.rms_norm_backward(rd, view, wd, eps=EPS, grad_in=view)
+        check_backward(back, r, x, w, None, EPS, "far rows")
+        heads = flat.as_strided((3, 5, 128), (far, 200, 1))
+        y, yd = make((3, 5, 128), dtype, 4)
+        heads.copy_(yd)
+        check_norm(rs.rms_norm(heads, None, eps=EPS, out=heads), y, None, None, EPS, "far heads")
+
+
 # ---------------------------------------------------------------------------
 # Streams and graphs
 # ---------------------------------------------------------------------------
