@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(TABLE tab, GradFac
   float norm;
   if (fac.partial) {
     norm = join_norm(fac.partial, fac.parts, fac.scale, lds);
-    if (fac.norm && blockIdx.x == 0 && threadIdx.x == 0) *fac.norm = norm;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *fac.norm = norm;
   } else {
     norm = *fac.norm;
   }

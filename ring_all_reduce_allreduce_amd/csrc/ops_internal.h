@@ -136,7 +136,7 @@ hipError_t launch_grad_norm_join(const double* partial, int parts, float scale, 
 struct GradFactor {
   const double* partial;  // join these into the norm, or
   int parts;
-  float* norm;            // partial null: read the norm here; else workgroup 0 writes it here, if not null
+  float* norm;            // partial null: read the norm here; else workgroup 0 writes it here
   float scale, max_norm, eps;
 };
 // Norm and, if `clip`, scaling of a short list in one launch; f.partial is not read.

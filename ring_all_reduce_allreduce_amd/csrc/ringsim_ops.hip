@@ -154,7 +154,7 @@ ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* out
     if constexpr (std::is_same_v<TABLE, GradScaleTable>)
       for (int j = 0; j < t.ntensors; ++j) t.out[j] = outs[index[j]];
     if (launch_grad_scale(t, f, grad_scale_workgroups(tiles), s) != hipSuccess) return RINGSIM_UNHANDLED_DEVICE_ERROR;
-    if (f.partial) f.norm = nullptr;  // the first launch writes it
+    f.partial = nullptr;  // the first launch has written the norm
   }
   return RINGSIM_SUCCESS;
 }
