@@ -279,7 +279,14 @@ int norm_backward_workgroups(int64_t rows, int64_t cols, int dtype) {
   if (rows <= kOneWorkgroupTurns * at_once) return 1;
   const int waves = sh.lanes <= 64 ? 4 : sh.lanes / 64;
   const int64_t most = (int64_t)kComputeUnits * std::max(1, kBackwardWaves / waves);
-  return (int)std::min(most, (rows + at_once - 1) / at_once);
+  const int64_t units = (rows + at_once - 1) / at_once;
+  // Rows above a wave that most workgroups would take one of and some two: as
+  // many as take two each, which leaves fewer sums (777 rows of 4096 bf16 14.0
+  // against 15.4 us, 600 of them 12.7 against 14.9; from three turns on, and
+  // for short rows, the workgroups that start early win by as much: 1984 rows
+  // of 4224 22.1 against 21.7, 12186 of 80 7.3 against 6.6 in a graph).
+  if (at_once == 1 && units > most && units < 2 * most) return (int)((units + 1) / 2);
+  return (int)std::min(most, units);
 }
 
 template <int DT, int TPR, int NP, int LK>
