@@ -102,7 +102,8 @@ def train(ranks: int = 4, steps: int = 10, tokens: int = 256, width: int = 512, 
                 rs.scale_grads(r.reduced_grads, norm, max_norm, scale=1.0 / ranks, outs=r.grads)
             norms.append(norm)
             for r in group:
-                torch._foreach_add_(r.weights, r.grads, alpha=-rate)
+                for w, g in zip(r.weights, r.grads):
+                    w.add_(g, alpha=-rate)
         torch.cuda.synchronize()
         if (err := rs.get_async_error(comm)) != rs.SUCCESS:
             raise rs.RingsimError(err, "ringsim_allreduce")

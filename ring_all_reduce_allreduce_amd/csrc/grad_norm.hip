@@ -37,7 +37,7 @@ struct TileFinder {
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
       const int j = (int)(threadIdx.x & 63) + 64 * i;
-      first[i] = j < tab.ntensors ? tab.tile0[j] : ~0u;
+      first[i] = j < TABLE::kTensors ? tab.tile0[j] : ~0u;
     }
   }
 
@@ -45,10 +45,11 @@ struct TileFinder {
     int k = -1;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) k += __builtin_popcountll(__builtin_amdgcn_ballot_w64(first[i] <= t));
-    const uint64_t in = tab.in[k];
+    uint64_t in = tab.in[k];
+    uint32_t from = tab.tile0[k], to = tab.tile0[k + 1];
+    asm volatile("" : "+s"(in), "+s"(from), "+s"(to));  // all three on their way before one is waited for
     const uint32_t meta = (uint32_t)(in >> kGradAddressBits);
     const int type = (int)(meta >> kGradLastBits);
-    const uint32_t from = tab.tile0[k], to = tab.tile0[k + 1];
     const int last = (int)(meta & ((1u << kGradLastBits) - 1)) * (type == kGradF32 ? 4 : 2);
     return GradTile{reinterpret_cast<const void*>(in & ((1ull << kGradAddressBits) - 1)), k, type,
                     t + 1 == to ? last : kGradTileBytes, to - from == 1 && last < 16, (int64_t)(t - from) * kGradTileBytes};
@@ -202,7 +203,7 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
 __global__ void __launch_bounds__(kThreads)
     grad_squares_kernel(GradTable tab, uint32_t keep, double* partial) {
   __shared__ double lds[kWaves];
-  const uint32_t tiles = tab.tile0[tab.ntensors];
+  const uint32_t tiles = tab.tiles;
   const TileFinder<GradTable> finder(tab);
   uint32_t t = blockIdx.x;
   double s = walk_squares<kLoadStream>(tab, finder, t, tiles - keep, gridDim.x);
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(TABLE tab, GradFac
   }
   const float f = factor_of(norm, fac);
   if (kInPlace && f == 1.0f) return;
-  const uint32_t tiles = tab.tile0[tab.ntensors];
+  const uint32_t tiles = tab.tiles;
   for (uint32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const GradTile g = finder.find(tab, tiles - 1 - t);
     BigTile d;

@@ -100,8 +100,8 @@ template <int N>
 struct GradInTable {
   static constexpr int kTensors = N;
   uint64_t in[N];
-  uint32_t tile0[N + 1];
-  int ntensors;
+  uint32_t tile0[N + 1];  // tile0[tensors] == tiles, ~0 above
+  uint32_t tiles;
 };
 template <int N>
 struct GradOutTable : GradInTable<N> {

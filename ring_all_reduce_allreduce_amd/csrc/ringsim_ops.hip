@@ -98,26 +98,25 @@ bool valid_grads(int n, const void* const* grads, void* const* outs, const int64
 }
 
 // Fills a table with the next tensors of the list that hold elements,
-// beginning with *next; advances *next. Returns the tiles in it.
+// beginning with *next; advances *next. No tiles: the rest was empty.
 template <typename TABLE>
-uint32_t fill_table(TABLE& t, int n, const void* const* grads, const int64_t* counts, const int* dtypes, int* next,
-                    int* index) {
-  uint32_t tiles = 0;
-  t.ntensors = 0;
+void fill_table(TABLE& t, int n, const void* const* grads, void* const* outs, const int64_t* counts,
+                const int* dtypes, int* next) {
+  int tensors = 0;
+  t.tiles = 0;
   t.tile0[0] = 0;
-  for (; *next < n && t.ntensors < TABLE::kTensors; ++*next) {
+  for (; *next < n && tensors < TABLE::kTensors; ++*next) {
     const int i = *next;
     if (counts[i] == 0) continue;
     const int64_t k = tiles_of(counts[i], dtypes[i]);
     const int64_t last = counts[i] - (k - 1) * (kGradTileBytes / op_dtype_size(dtypes[i]));
-    const int j = t.ntensors++;
     const uint64_t meta = (uint64_t)grad_type(dtypes[i]) << kGradLastBits | (uint64_t)last;
-    t.in[j] = (uint64_t)reinterpret_cast<uintptr_t>(grads[i]) | meta << kGradAddressBits;
-    tiles += (uint32_t)k;
-    t.tile0[j + 1] = tiles;
-    if (index) index[j] = i;
+    t.in[tensors] = (uint64_t)reinterpret_cast<uintptr_t>(grads[i]) | meta << kGradAddressBits;
+    if constexpr (std::is_same_v<TABLE, GradScaleTable>) t.out[tensors] = outs[i];
+    t.tiles += (uint32_t)k;
+    t.tile0[++tensors] = t.tiles;
   }
-  return tiles;
+  for (int j = tensors + 1; j <= TABLE::kTensors; ++j) t.tile0[j] = ~0u;
 }
 
 int grad_workgroups(uint32_t tiles) { return (int)std::min<uint32_t>(tiles, kGradWorkgroups); }
@@ -132,11 +131,11 @@ ringsim_result_t enqueue_squares(int n, const void* const* grads, const int64_t*
   keep /= kGradTileBytes;
   for (int next = 0; next < n;) {
     GradTable t;
-    const uint32_t tiles = fill_table(t, n, grads, counts, dtypes, &next, nullptr);
-    if (tiles == 0) continue;  // the rest of the list was empty
-    left -= tiles;
-    const int g = grad_workgroups(tiles);
-    const uint32_t here = (uint32_t)std::min<int64_t>(tiles, std::max<int64_t>(0, keep - left));
+    fill_table(t, n, grads, nullptr, counts, dtypes, &next);
+    if (t.tiles == 0) break;
+    left -= t.tiles;
+    const int g = grad_workgroups(t.tiles);
+    const uint32_t here = (uint32_t)std::min<int64_t>(t.tiles, std::max<int64_t>(0, keep - left));
     if (launch_grad_squares(t, here, partial + *parts, g, s) != hipSuccess) return RINGSIM_UNHANDLED_DEVICE_ERROR;
     *parts += g;
   }
@@ -148,12 +147,9 @@ ringsim_result_t enqueue_scale(int n, const void* const* grads, void* const* out
                                const int* dtypes, GradFactor f, hipStream_t s) {
   for (int next = 0; next < n;) {
     TABLE t;
-    int index[TABLE::kTensors];
-    const uint32_t tiles = fill_table(t, n, grads, counts, dtypes, &next, index);
-    if (tiles == 0) continue;
-    if constexpr (std::is_same_v<TABLE, GradScaleTable>)
-      for (int j = 0; j < t.ntensors; ++j) t.out[j] = outs[index[j]];
-    if (launch_grad_scale(t, f, grad_scale_workgroups(tiles), s) != hipSuccess) return RINGSIM_UNHANDLED_DEVICE_ERROR;
+    fill_table(t, n, grads, outs, counts, dtypes, &next);
+    if (t.tiles == 0) break;
+    if (launch_grad_scale(t, f, grad_scale_workgroups(t.tiles), s) != hipSuccess) return RINGSIM_UNHANDLED_DEVICE_ERROR;
     f.partial = nullptr;  // the first launch has written the norm
   }
   return RINGSIM_SUCCESS;
