@@ -23,64 +23,141 @@ struct BackwardRow {
   u32x4 dy[NP], h[NP], res[NP];
 };
 
-// Rows on 1024 lanes have 128 registers a lane, too few for the weights and
-// the residual's gradient beside dy, h and the weight's gradient: these two are
-// read where they are used (2048 rows of 32768 bf16 take 217 us so, 310 with
-// them in registers that spill).
-template <int TPR>
-constexpr bool kReadLate = TPR == 1024;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// Loads of one row. No condition stands around a load, since a wait that some
-// path reaches without it would wait for everything: where the row is not
-// wanted, or there is no residual's gradient, the lanes read the first bytes
-// of a row of h for nothing.
+// A workgroup of 1024 lanes has a compute unit for itself, with 128 registers
+// a lane: too few for a row, the next row and 16 or 32 sums of the weight's
+// gradient. Such wide rows keep the sums in LDS, which nothing else needs, and
+// load the next row a pack at a time, each into the registers of the pack just
+// written. 2048 rows of 32768 bf16 with a residual's gradient take 123 us so
+// and 215 with sums in registers that spill, of 16384 51 us on 1024 lanes and
+// 61 on 512 lanes that have the registers but load a row after another.
+template <int TPR>
+constexpr bool kWide = TPR == 1024;
+
+// With 32 elements a lane the weights and the residual's gradient do not fit
+// beside dy and h either: they are read where they are used.
+template <int DT, int TPR, int NP>
+constexpr bool kReadLate = kWide<TPR> && NP * OpElem<DT>::kPack > 16;
+
+// Makes a wide row's offsets unknown from here on, and those of its later
+// packs unknown until `after` is: the compiler would compute and load what
+// eight packs need at once, and spill it. Two packs at a time hide the loads
+// (one at a time takes up to 4% longer).
+template <int TPR>
+__device__ __forceinline__ void offsets_after(int k, int& t, float& after) {
+  if (kWide<TPR> && k % 2 == 0) asm volatile("" : "+v"(t), "+v"(after));
+}
+
+// Where a row is read from. No condition stands around a load, since a wait
+// that some path reaches without it would wait for everything: where the row
+// is not wanted, or there is no residual's gradient, the lanes read the first
+// bytes of a row of h for nothing.
+template <int DT>
+struct RowSource {
+  const typename OpElem<DT>::T *dy, *h, *res;
+  int n, n_res;
+};
+
+template <int DT>
+__device__ __forceinline__ RowSource<DT> row_source(const RmsNormBackwardArgs& a, uint32_t row, bool wanted) {
+  const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
+  const int least = a.cols < OpElem<DT>::kPack ? a.cols : OpElem<DT>::kPack;
+  const bool res = wanted && a.grad_residual.p;
+  RowSource<DT> s;
+  s.h = row_ptr<DT>(a.h, o, in);
+  s.dy = wanted ? row_ptr<DT>(a.grad_out, o, in) : s.h;
+  s.res = res ? row_ptr<DT>(a.grad_residual, o, in) : s.h;
+  s.n = wanted ? a.cols : least;
+  s.n_res = res ? a.cols : least;
+  return s;
+}
+
+template <int DT, int TPR, int NP, int LK>
+__device__ __forceinline__ void load_part(BackwardRow<NP>& r, const RowSource<DT>& s, int k, int c) {
+  r.dy[k] = load_pack<DT, LK>(s.dy, c, s.n);
+  r.h[k] = load_pack<DT, LK>(s.h, c, s.n);
+  if constexpr (!kReadLate<DT, TPR, NP>) r.res[k] = load_pack<DT, LK>(s.res, c, s.n_res);
+}
+
 template <int DT, int TPR, int NP, int LK>
 __device__ __forceinline__ BackwardRow<NP> load_row(const RmsNormBackwardArgs& a, uint32_t row, bool wanted, int t) {
-  constexpr int kPack = OpElem<DT>::kPack;
-  const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
-  const auto* ph = row_ptr<DT>(a.h, o, in);
-  const auto* pdy = wanted ? row_ptr<DT>(a.grad_out, o, in) : ph;
-  const bool res = wanted && a.grad_residual.p;
-  const auto* pr = res ? row_ptr<DT>(a.grad_residual, o, in) : ph;
-  const int least = a.cols < kPack ? a.cols : kPack;
-  const int n = wanted ? a.cols : least, nr = res ? a.cols : least;
-  const int lanes = row_lanes<TPR>();
+  const RowSource<DT> s = row_source<DT>(a, row, wanted);
   BackwardRow<NP> r;
 #pragma unroll
-  for (int k = 0; k < NP; ++k) {
-    const int c = (k * lanes + t) * kPack;
-    r.dy[k] = load_pack<DT, LK>(pdy, c, n);
-    r.h[k] = load_pack<DT, LK>(ph, c, n);
-    if constexpr (!kReadLate<TPR>) r.res[k] = load_pack<DT, LK>(pr, c, nr);
-  }
+  for (int k = 0; k < NP; ++k) load_part<DT, TPR, NP, LK>(r, s, k, (k * row_lanes<TPR>() + t) * OpElem<DT>::kPack);
   return r;
 }
 
+// A lane's sums for its columns of the weight's gradient: in registers, or
+// for wide rows in LDS, where lanes side by side have vectors side by side and
+// only the lane itself reads and writes them.
+template <int TPR, int NP, int P>
+struct WeightSums {
+  float f[NP][P];
+  __device__ __forceinline__ void get(int k, int, float* d) const {
+#pragma unroll
+    for (int i = 0; i < P; ++i) d[i] = f[k][i];
+  }
+  __device__ __forceinline__ void put(int k, int, const float* d) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) f[k][i] = d[i];
+  }
+};
+template <int NP, int P>
+struct WeightSums<1024, NP, P> {
+  f32x4* lds;  // [NP * P / 4][1024]
+  __device__ __forceinline__ void get(int k, int t, float* d) const {
+#pragma unroll
+    for (int j = 0; j < P / 4; ++j) {
+      const f32x4 v = lds[(k * (P / 4) + j) * 1024 + t];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[4 * j + i] = v[i];
+    }
+  }
+  __device__ __forceinline__ void put(int k, int t, const float* d) {
+#pragma unroll
+    for (int j = 0; j < P / 4; ++j)
+      lds[(k * (P / 4) + j) * 1024 + t] = f32x4{d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]};
+  }
+};
+
 // One row in registers: its gradient is written, its part of the weight's
-// gradient added to dw. Everything stays as it lies in memory until it is
-// used, also over the barrier: unpacking again costs an operation an element
-// and saves the registers.
+// gradient added to dw, and a wide row's registers filled from `next`.
+// Everything stays as it lies in memory until it is used, also over the
+// barrier: unpacking again costs an operation an element and saves the
+// registers.
 template <int DT, int TPR, int NP, int LK>
 __device__ __forceinline__ void take_row(const RmsNormBackwardArgs& a, BackwardRow<NP>& r, uint32_t row, int t,
-                                         WeightPack (&w)[NP], float (&dw)[NP][OpElem<DT>::kPack], RowBuffers<TPR, f32x2>& lds,
-                                         int& turn) {
+                                         WeightPack (&w)[NP], WeightSums<TPR, NP, OpElem<DT>::kPack>& dw,
+                                         RowBuffers<TPR, f32x2>& lds, int& turn, const RowSource<DT>& next) {
   constexpr int kPack = OpElem<DT>::kPack;
+  constexpr bool kLate = kReadLate<DT, TPR, NP>;
+  // Eight packs have no registers for branches around late loads either (2048
+  // rows of 20480 fp32 with a residual's gradient: 144 us, 168 with branches;
+  // of fewer packs, the loads for nothing cost more): without a weight, or a
+  // residual's gradient, they read h.
+  constexpr bool kPlain = kLate && NP == 8;
   const int lanes = row_lanes<TPR>();
+  const RowSource<DT> here = row_source<DT>(a, row, true);
+  const void* weight = kPlain && a.weight_kind == kWeightNone ? (const void*)here.h : a.weight;
+  const int kind = kPlain ? (int)kWeightF32 : a.weight_kind;
+  static_assert(!kPlain || DT == RINGSIM_FLOAT32, "eight packs");
   float hh = 0.0f, gh = 0.0f;
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
+    offsets_after<TPR>(k, t, gh);
     const int c = (k * lanes + t) * kPack;
     float fh[kPack], fdy[kPack], fw[kPack];
     r.h[k] = fix_pack<DT, LK>(r.h[k], c, a.cols);
     r.dy[k] = fix_pack<DT, LK>(r.dy[k], c, a.cols);
     unpack<DT>(r.h[k], fh);
     unpack<DT>(r.dy[k], fdy);
-    if constexpr (kReadLate<TPR>) {
-      unpack_weight<DT, LK>(load_weight<DT, LK>(a.weight, a.weight_kind, c, a.cols), a.weight_kind, c, a.cols, fw);
-    } else {
+    if constexpr (kLate)
+      w[k] = load_weight<DT, LK>(weight, kind, c, a.cols);
+    else
       asm volatile("" : "+v"(w[k].v[0]), "+v"(w[k].v[1]));
-      unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
-    }
+    unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
 #pragma unroll
     for (int i = 0; i < kPack; ++i) {
       hh = __builtin_fmaf(fh[i], fh[i], hh);
@@ -92,25 +169,30 @@ __device__ __forceinline__ void take_row(const RmsNormBackwardArgs& a, BackwardR
   const float m = rr * rr * rr * (gh * a.inv_cols);
   const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
   auto* pout = row_ptr<typename OpElem<DT>::T>(a.grad_in, o, in);
+  float last = m;  // of the pack before
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
+    offsets_after<TPR>(k, t, last);
     const int c = (k * lanes + t) * kPack;
-    float fh[kPack], fdy[kPack], fw[kPack], g[kPack];
+    float fh[kPack], fdy[kPack], fw[kPack], g[kPack], d[kPack];
     asm volatile("" : "+v"(r.h[k]), "+v"(r.dy[k]));
     unpack<DT>(r.h[k], fh);
     unpack<DT>(r.dy[k], fdy);
-    if constexpr (kReadLate<TPR>) {
-      if (a.grad_residual.p) r.res[k] = load_pack<DT, LK>(row_ptr<DT>(a.grad_residual, o, in), c, a.cols);
-      unpack_weight<DT, LK>(load_weight<DT, LK>(a.weight, a.weight_kind, c, a.cols), a.weight_kind, c, a.cols, fw);
+    dw.get(k, t, d);
+    if constexpr (kLate) {
+      if (kPlain || a.grad_residual.p) r.res[k] = load_pack<DT, LK>(here.res, c, here.n_res);
+      w[k] = load_weight<DT, LK>(weight, kind, c, a.cols);
     } else {
       asm volatile("" : "+v"(w[k].v[0]), "+v"(w[k].v[1]));
-      unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
     }
+    unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
 #pragma unroll
     for (int i = 0; i < kPack; ++i) {
       g[i] = fdy[i] * fw[i] * rr - fh[i] * m;
-      dw[k][i] = __builtin_fmaf(fdy[i], fh[i] * rr, dw[k][i]);
+      d[i] = __builtin_fmaf(fdy[i], fh[i] * rr, d[i]);
     }
+    dw.put(k, t, d);
+    last = g[0] + g[kPack - 1];
     if (a.grad_residual.p) {
       float fr[kPack];
       unpack<DT>(fix_pack<DT, LK>(r.res[k], c, a.cols), fr);
@@ -118,6 +200,7 @@ __device__ __forceinline__ void take_row(const RmsNormBackwardArgs& a, BackwardR
       for (int i = 0; i < kPack; ++i) g[i] += fr[i];
     }
     store_pack<DT>(pout, to_pack<DT>(g), c, a.cols);
+    if constexpr (kWide<TPR>) load_part<DT, TPR, NP, LK>(r, next, k, c);
   }
 }
 
@@ -133,9 +216,6 @@ template <int DT, int TPR, int NP, int LK>
 __global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_backward_kernel(RmsNormBackwardArgs a) {
   constexpr int kRows = kRowsPerBlock<TPR>;
   constexpr int kPack = OpElem<DT>::kPack;
-  // Whether the next row's loads go out before this row's sums: where two
-  // rows fit into a lane's registers.
-  constexpr bool kAhead = NP * kPack <= 16 && TPR < 1024;
   using T = typename OpElem<DT>::T;
   __shared__ RowBuffers<TPR, f32x2> lds;
   __shared__ float dws[kRows > 1 ? kRows : 1][kRows > 1 ? TPR * NP * kPack : 1];
@@ -143,20 +223,29 @@ __global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_backward_kernel(RmsNo
   const int lanes = row_lanes<TPR>(), t = TPR <= 64 ? threadIdx.x % TPR : threadIdx.x;
   int turn = 0;
   WeightPack w[NP];
-  float dw[NP][kPack];
+  WeightSums<TPR, NP, kPack> dw;
+  if constexpr (kWide<TPR>) {
+    __shared__ f32x4 sums[NP * (kPack / 4) * 1024];
+    dw.lds = sums;
+  }
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    if constexpr (!kReadLate<TPR>)
+    if constexpr (!kReadLate<DT, TPR, NP>)
       w[k] = load_weight<DT, LK>(a.weight, a.weight_kind, (k * lanes + t) * kPack, a.cols);
-#pragma unroll
-    for (int i = 0; i < kPack; ++i) dw[k][i] = 0.0f;
+    const float zeros[kPack] = {};
+    dw.put(k, t, zeros);
   }
   uint32_t row = blockIdx.x * kRows + (TPR <= 64 ? threadIdx.x / TPR : 0);
   const uint32_t step = gridDim.x * kRows;
-  if constexpr (!kAhead) {
-    for (; row < a.rows; row += step) {
+  if constexpr (kWide<TPR>) {
+    if (row < a.rows) {
       BackwardRow<NP> r = load_row<DT, TPR, NP, LK>(a, row, true, t);
-      take_row<DT, TPR, NP, LK>(a, r, row, t, w, dw, lds, turn);
+      do {
+        const uint32_t next = row + step;
+        take_row<DT, TPR, NP, LK>(a, r, row, t, w, dw, lds, turn,
+                                  row_source<DT>(a, next < a.rows ? next : row, next < a.rows));
+        row = next;
+      } while (row < a.rows);
     }
   } else if (row < a.rows) {
     // Two sets of registers in turn, since moving a loaded vector waits for it.
@@ -164,12 +253,12 @@ __global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_backward_kernel(RmsNo
     for (;;) {
       uint32_t next = row + step;  // below 2^31 + 2^14
       rb = load_row<DT, TPR, NP, LK>(a, next < a.rows ? next : row, next < a.rows, t);
-      take_row<DT, TPR, NP, LK>(a, ra, row, t, w, dw, lds, turn);
+      take_row<DT, TPR, NP, LK>(a, ra, row, t, w, dw, lds, turn, {});
       row = next;
       if (row >= a.rows) break;
       next = row + step;
       ra = load_row<DT, TPR, NP, LK>(a, next < a.rows ? next : row, next < a.rows, t);
-      take_row<DT, TPR, NP, LK>(a, rb, row, t, w, dw, lds, turn);
+      take_row<DT, TPR, NP, LK>(a, rb, row, t, w, dw, lds, turn, {});
       row = next;
       if (row >= a.rows) break;
     }
@@ -180,17 +269,18 @@ __global__ void __launch_bounds__(kMaxBlock<TPR>) rms_norm_backward_kernel(RmsNo
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
       const int c = (k * lanes + t) * kPack;
+      float d[kPack];
+      dw.get(k, t, d);
       if (part || a.weight_dtype == RINGSIM_FLOAT32)
-        store_sums<kPack>(part ? part : static_cast<float*>(a.grad_weight), dw[k], c, a.cols);
+        store_sums<kPack>(part ? part : static_cast<float*>(a.grad_weight), d, c, a.cols);
       else
-        store_pack<DT>(a.grad_weight, to_pack<DT>(dw[k]), c, a.cols);
+        store_pack<DT>(a.grad_weight, to_pack<DT>(d), c, a.cols);
     }
   } else {
     float* mine = dws[threadIdx.x / TPR];
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
-#pragma unroll
-      for (int i = 0; i < kPack; ++i) mine[(k * lanes + t) * kPack + i] = dw[k][i];
+      dw.get(k, t, mine + (k * lanes + t) * kPack);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.cols; c += kMaxBlock<TPR>) {
@@ -257,7 +347,9 @@ static RowShape backward_shape(int64_t cols, int dtype) {
   if (packs <= 128) return {64, 2, 64};
   if (packs <= 256) return {lanes(1), 1, 256};
   if (packs <= 1024) return {lanes(2), 2, 512};
-  if (packs <= 2048) return {lanes(4), 4, 512};
+  // 4 packs a lane are 16 elements of fp32, so that 512 lanes have room for two
+  // rows (4096 rows of 8192: 74 us, 77 as wide rows), and 32 of the others.
+  if (packs <= 2048) return dtype == RINGSIM_FLOAT32 ? RowShape{lanes(4), 4, 512} : RowShape{lanes(2), 2, 1024};
   if (packs <= 4096) return {lanes(4), 4, 1024};
   return {lanes(8), 8, 1024};
 }
@@ -315,13 +407,12 @@ static hipError_t launch_type(const RmsNormBackwardArgs& a, hipStream_t s) {
     case 64 * 16 + 2: return launch_shape<DT, 64, 2>(a, sh.lanes, s);
     case 256 * 16 + 1: return launch_shape<DT, 256, 1>(a, sh.lanes, s);
     case 512 * 16 + 2: return launch_shape<DT, 512, 2>(a, sh.lanes, s);
-    case 512 * 16 + 4: return launch_shape<DT, 512, 4>(a, sh.lanes, s);
     case 1024 * 16 + 4: return launch_shape<DT, 1024, 4>(a, sh.lanes, s);
-    case 1024 * 16 + 8:
-      if constexpr (DT == RINGSIM_FLOAT32) return launch_shape<DT, 1024, 8>(a, sh.lanes, s);
-      [[fallthrough]];
-    default: return hipErrorInvalidValue;
   }
+  if constexpr (DT == RINGSIM_FLOAT32)
+    return sh.packs == 4 ? launch_shape<DT, 512, 4>(a, sh.lanes, s) : launch_shape<DT, 1024, 8>(a, sh.lanes, s);
+  else
+    return launch_shape<DT, 1024, 2>(a, sh.lanes, s);
 }
 
 hipError_t launch_rms_norm_backward(const RmsNormBackwardArgs& a, int dtype, hipStream_t s) {

@@ -258,6 +258,25 @@ def test_backward_few_rows(cols):
             check_backward(rs.rms_norm_backward(dyd, hd, wd, eps=EPS), dy, h, w, None, EPS, f"{name} {rows}x{cols}")
 
 
+@pytest.mark.parametrize("cols", [8193, 12296, 16384, 16385, 20003, 32768])
+def test_backward_wide_rows(cols):
+    """Rows on 1024 lanes, which load the next row while they write one: one to
+    three turns a workgroup, with and without the weight and the residual's
+    gradient, results in place of each input."""
+    for rows in (4, 257, 600):
+        for name, kind, target in (("bf16", "same", "grad_residual"), ("f16", "f32", "h"), ("f32", "none", "grad_out"),
+                                   ("f32", "same", "grad_residual"), ("bf16", "none", None), ("f32", "same", None)):
+            what = f"backward {name} {rows}x{cols} weight {kind} into {target}"
+            say(what)
+            h, hd = make((rows, cols), DTYPES[name], rows)
+            dy, dyd = make((rows, cols), DTYPES[name], rows + 1, 0.1)
+            r, rd = make((rows, cols), DTYPES[name], rows + 2, 0.1) if target else (None, None)
+            w, wd = weight_of(kind, cols, DTYPES[name], 3)
+            into = {"grad_out": dyd, "h": hd, "grad_residual": rd, None: None}[target]
+            got = rs.rms_norm_backward(dyd, hd, wd, grad_residual=rd, eps=EPS, grad_in=into)
+            check_backward(got, dy, h, w, r, EPS, what)
+
+
 def test_backward_heads_and_in_place():
     h = torch.empty(37, 12, 128).normal_(generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
     dy = torch.empty(37, 8, 128).normal_(generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
