@@ -6,11 +6,11 @@
 // One pass reads each row once: both sums over the row (h^2 and g h) are taken
 // together, r is recomputed from h rather than stored by the forward call
 // (the row is here anyway), and every lane adds its columns' part of
-// grad_weight into registers over all rows its workgroup walks. Workgroups
-// leave these sums in a workspace, and a second small kernel adds them in a
-// fixed order: no atomics, the same bits every time. Bound by memory: 16384
-// rows of 4096 take 91 us in bf16 (5.9 TB/s) and 168 us in fp32, the sum
-// another 4.4 us.
+// grad_weight over all rows its workgroup walks, in registers or, for the
+// widest rows, in LDS. Workgroups leave these sums in a workspace, and a second
+// small kernel adds them in a fixed order: no atomics, the same bits every
+// time. Bound by memory: 16384 rows of 4096 take 91 us in bf16 (5.9 TB/s) and
+// 168 us in fp32, the sum another 4.4 us.
 #include <algorithm>
 
 #include "ops_device.h"
