@@ -277,6 +277,19 @@ def test_backward_wide_rows(cols):
             check_backward(got, dy, h, w, r, EPS, what)
 
 
+@pytest.mark.parametrize("rows, cols", [(2048, 4100), (2049, 4104), (2049, 4097), (2100, 5121), (2600, 6144), (2100, 6145)])
+def test_backward_three_packs(rows, cols):
+    """Both sides of the borders of rows on three or four waves."""
+    for name, kind, with_residual in (("bf16", "same", True), ("f16", "f32", False)):
+        what = f"backward {name} {rows}x{cols} weight {kind} residual {with_residual}"
+        say(what)
+        h, hd = make((rows, cols), DTYPES[name], rows, pad=1)
+        dy, dyd = make((rows, cols), DTYPES[name], rows + 1, 0.1)
+        r, rd = make((rows, cols), DTYPES[name], rows + 2, 0.1) if with_residual else (None, None)
+        w, wd = weight_of(kind, cols, DTYPES[name], 3)
+        check_backward(rs.rms_norm_backward(dyd, hd, wd, grad_residual=rd, eps=EPS), dy, h, w, r, EPS, what)
+
+
 def test_backward_heads_and_in_place():
     h = torch.empty(37, 12, 128).normal_(generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
     dy = torch.empty(37, 8, 128).normal_(generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
