@@ -114,10 +114,13 @@ int type_code(at::ScalarType t) {
   }
 }
 
+void check_strided(const at::Tensor& t, const char* name) {
+  if (t.layout() != at::kStrided) throw WrongValue(std::string(name) + " must be a strided tensor");
+}
 void check_device(const at::Tensor& t, int device, const char* name) {
+  check_strided(t, name);
   if (!t.is_cuda() || t.get_device() != device)
     throw WrongValue(std::string(name) + " must be a tensor on the current device");
-  if (t.layout() != at::kStrided) throw WrongValue(std::string(name) + " must be a strided tensor");
 }
 
 // The allocation at::empty ends in, without its way through the dispatcher
@@ -132,38 +135,58 @@ ringsim_stream_t current_stream(int device) {
   return c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
 }
 
+// The leading dimensions of a shape that count: those of size 1 take no part
+// in where a row lies, and their strides may be anything. The last of them is
+// the inner one; those before it are taken together as the outer one.
+struct Leading {
+  c10::SmallVector<int, 8> dims;  // from the inner one outwards
+  bool no_rows = false;
+
+  explicit Leading(at::IntArrayRef shape) {
+    for (int i = (int)shape.size() - 2; i >= 0; --i) {
+      if (shape[i] != 1) dims.push_back(i);
+      no_rows = no_rows || shape[i] == 0;
+    }
+  }
+};
+
 // {outer, inner} strides of a tensor whose rows are its last dimension: up to
-// two leading dimensions of any strides, or more that follow one another in
-// memory without gaps.
+// two leading dimensions of any strides, or more whose outer ones follow one
+// another in memory without gaps.
 void rows(const at::Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type, int device,
           int64_t stride[2]) {
   if (t.scalar_type() != type)
     throw WrongType(std::string(name) + " must have dtype " + c10::toString(type) + ", not " +
                     c10::toString(t.scalar_type()));
-  check_device(t, device, name);
+  check_strided(t, name);
   if (t.sizes() != shape)
     throw WrongValue(std::string(name) + " must have shape " + shape_text(shape) + ", not " + shape_text(t.sizes()));
   const auto st = t.strides();
-  const int n = (int)shape.size();
-  if (shape[n - 1] > 1 && st[n - 1] != 1)
+  if (shape.back() > 1 && st.back() != 1)
     throw WrongValue(std::string("the last dimension of ") + name + " must be contiguous");
+  const Leading lead(shape);
+  const auto& d = lead.dims;
   stride[0] = stride[1] = 0;
-  if (n == 2) stride[0] = st[0];
-  if (n < 3) return;
-  for (int i = 0; i < n - 3; ++i)
-    if (shape[i] != 1 && st[i] != st[i + 1] * shape[i + 1])
-      throw WrongValue(std::string("the leading dimensions of ") + name + " must be contiguous among themselves");
-  stride[0] = st[n - 3];
-  stride[1] = st[n - 2];
+  if (!lead.no_rows) {
+    for (size_t k = 2; k < d.size(); ++k)
+      if (st[d[k]] != st[d[k - 1]] * shape[d[k - 1]])
+        throw WrongValue(std::string("the leading dimensions of ") + name + " must be contiguous among themselves");
+    if (d.size() == 1) stride[0] = st[d[0]];
+    if (d.size() > 1) {
+      stride[0] = st[d[1]];
+      stride[1] = st[d[0]];
+    }
+  }
+  check_device(t, device, name);
 }
 
-// [outer, inner, cols] of a shape.
+// [outer, inner, cols] of a shape, as rows() takes its strides.
 void row_counts(at::IntArrayRef shape, int64_t* outer, int64_t* inner, int64_t* cols) {
-  const int n = (int)shape.size();
-  *cols = shape[n - 1];
-  *inner = n >= 3 ? shape[n - 2] : 1;
-  *outer = n == 2 ? shape[0] : 1;
-  for (int i = 0; i + 2 < n; ++i) *outer *= shape[i];
+  const Leading lead(shape);
+  *cols = shape.back();
+  *outer = *inner = 1;
+  for (size_t k = 0; k < lead.dims.size(); ++k)
+    *(k == 0 && lead.dims.size() > 1 ? inner : outer) *= shape[lead.dims[k]];
 }
 
 // Types of the normed tensor and of the weight, and the weight's shape.

@@ -71,7 +71,9 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, out_dtype=None
     in front of it:  h = x + residual,  out = h / sqrt(mean(h^2) + eps) * weight.
 
     float32, bfloat16 or float16; the weight of x's dtype or float32. Rows may
-    be apart in memory: up to two leading dimensions of any strides.
+    be apart in memory: up to two leading dimensions of any strides, or more
+    of which all but the last follow one another without gaps (dimensions of
+    size 1 do not count).
     ``out_dtype="float8_e4m3"`` (or torch.float8_e4m3fn) gives 8-bit values
     and fp32 ``scales`` of shape ``x.shape[:-1] + (groups,)``: one for every
     ``group`` columns (32, 64 or 128), or one a row (group 0).
