@@ -117,10 +117,12 @@ typedef struct {
 } ringsim_rms_norm_backward_t;
 
 /* Gradients of the norm. With r = 1 / sqrt(mean(h^2) + eps), recomputed from
- * h, and g = grad_out * weight, for every row
- *     grad_in = grad_residual + r * g - h * r^3 * mean(g * h)
+ * h, n = h * r and g = grad_out * weight, for every row
+ *     grad_in = grad_residual + r * (g - n * mean(g * n))
  * and over all rows
- *     grad_weight = sum of grad_out * h * r
+ *     grad_weight = sum of grad_out * n
+ * where mean(g * n) is formed as r * mean(g * h): a row's sums of h^2 and of
+ * g * h have to lie in fp32's range. Beyond it, r is 0 as in the forward call.
  * grad_weight is overwritten (with zeros if there are no rows). grad_in may
  * be grad_out, h or grad_residual itself (same address, same strides). The
  * gradient of an output in 8 bits passes its rounding unchanged: grad_out is

@@ -1,8 +1,11 @@
 // rms_norm_backward.hip -- gradients of the root-mean-square norm.
 //
-// With r = 1 / sqrt(mean(h^2) + eps) and g = grad_out * w, for every row
-//   grad_in = grad_residual + r g - h r^3 mean(g h)
-// and over all rows  grad_weight = sum of grad_out h r.
+// With r = 1 / sqrt(mean(h^2) + eps), n = h r and g = grad_out * w, for every row
+//   grad_in = grad_residual + r (g - n mean(g n))
+// and over all rows  grad_weight = sum of grad_out n.
+// mean(g n) is taken as r mean(g h), so that both sums need the row but once.
+// r itself is never raised to a power: r^3 leaves fp32's range for rows above
+// 1e13 and below 1e-13, where every factor of this form is as large as g or n.
 // One pass reads each row once: both sums over the row (h^2 and g h) are taken
 // together, r is recomputed from h rather than stored by the forward call
 // (the row is here anyway), and every lane adds its columns' part of
@@ -166,7 +169,7 @@ __device__ __forceinline__ void take_row(const RmsNormBackwardArgs& a, BackwardR
   }
   row_reduce2<TPR>(hh, gh, lds, turn);
   const float rr = rsqrtf(__builtin_fmaf(hh, a.inv_cols, a.eps));
-  const float m = rr * rr * rr * (gh * a.inv_cols);
+  const float m = rr * (gh * a.inv_cols);
   const uint32_t o = a.inner == 1 ? row : row / a.inner, in = a.inner == 1 ? 0 : row - o * a.inner;
   auto* pout = row_ptr<typename OpElem<DT>::T>(a.grad_in, o, in);
   float last = m;  // of the pack before
@@ -188,8 +191,9 @@ __device__ __forceinline__ void take_row(const RmsNormBackwardArgs& a, BackwardR
     unpack_weight<DT, LK>(w[k], a.weight_kind, c, a.cols, fw);
 #pragma unroll
     for (int i = 0; i < kPack; ++i) {
-      g[i] = fdy[i] * fw[i] * rr - fh[i] * m;
-      d[i] = __builtin_fmaf(fdy[i], fh[i] * rr, d[i]);
+      const float n = fh[i] * rr;
+      g[i] = __builtin_fmaf(-n, m, fdy[i] * fw[i]) * rr;
+      d[i] = __builtin_fmaf(fdy[i], n, d[i]);
     }
     dw.put(k, t, d);
     last = g[0] + g[kPack - 1];
