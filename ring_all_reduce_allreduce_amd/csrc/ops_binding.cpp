@@ -244,6 +244,14 @@ void want_args(Py_ssize_t n, Py_ssize_t want) {
 
 void* data(const at::Tensor& t) { return t.data_ptr(); }
 
+// Says that the memory of an argument has been written, so that autograd
+// notices where it had been saved. Tensors of inference mode have no version.
+void written(PyObject* given) {
+  if (given == Py_None) return;
+  const at::Tensor& t = THPVariable_Unpack(given);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // rms_norm(x, weight, residual, eps, quant, group, out, residual_out, scales)
 PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return guarded([&] {
@@ -302,6 +310,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     a.residual_out = res ? data(*res_out) : nullptr;
     a.group = (int)group;
     check(ringsim_rms_norm(&a, current_stream(device)), "ringsim_rms_norm");
+    for (int i = 6; i < 9; ++i) written(args[i]);
     return pack({result(args[6], made_out), result(args[7], made_res), result(args[8], made_scales)});
   });
 }
@@ -358,6 +367,7 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) 
     a.grad_residual = res ? data(*res) : nullptr;
     a.grad_in = data(*dx);
     check(ringsim_rms_norm_backward(&a, current_stream(device)), "ringsim_rms_norm_backward");
+    for (int i = 5; i < 7; ++i) written(args[i]);
     return pack({result(args[5], made_dx), result(args[6], made_dw)});
   });
 }
@@ -399,6 +409,9 @@ struct GradList {
   GradList(const GradList&) = delete;
   GradList& operator=(const GradList&) = delete;
   int size() const { return (int)ptrs.size(); }
+  void all_written() const {
+    for (int i = 0; i < size(); ++i) written(PySequence_Fast_GET_ITEM(seq, i));
+  }
 };
 
 // The outputs' addresses, which have to match the gradients.
@@ -441,6 +454,7 @@ PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     check(ringsim_grad_norm(g.size(), g.ptrs.data(), g.counts.data(), g.types.data(), scale, norm, address(ws), bytes,
                             current_stream(device)),
           "ringsim_grad_norm");
+    written(args[2]);
     return result(args[2], made);
   });
 }
@@ -461,6 +475,7 @@ PyObject* scale_grads(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
                               (float)number(args[4]), norm, (float)number(args[2]), (float)number(args[5]),
                               current_stream(device)),
           "ringsim_scale_grads");
+    (o ? o : &g)->all_written();
     return none();
   });
 }
@@ -482,6 +497,8 @@ PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
                              (float)number(args[3]), (float)number(args[1]), (float)number(args[4]), norm, address(ws),
                              bytes, current_stream(device)),
           "ringsim_clip_grads");
+    (o ? o : &g)->all_written();
+    written(args[5]);
     return result(args[5], made);
   });
 }

@@ -16,7 +16,9 @@ Arguments are device tensors of the current device. Calls are asynchronous on
 stream); results and workspaces that a call allocates come from that stream's
 memory, so they are safe to use and to drop there. A tensor the caller brings
 must be ready on that stream and stay alive until the work is done, as for
-every call of this package. None of them records anything for autograd. Wrong
+every call of this package. None of them records anything for autograd;
+tensors they write advance their version, so that autograd notices a saved
+tensor that was overwritten. Wrong
 arguments raise TypeError or ValueError before anything is enqueued; codes of
 the library raise RingsimError.
 
