@@ -15,6 +15,7 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <optional>
 #include <sstream>
 #include <stdexcept>
 #include <string>
@@ -244,6 +245,21 @@ void want_args(Py_ssize_t n, Py_ssize_t want) {
 
 void* data(const at::Tensor& t) { return t.data_ptr(); }
 
+// Lets other Python threads run while a call allocates and launches, both of
+// which can wait for the driver. What stands in its scope must not touch
+// Python objects, and what was read from them must be held: by the caller's
+// arguments, or by a list's own references.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* const state_;
+};
+
 // Says that the memory of an argument has been written, so that autograd
 // notices where it had been saved. Tensors of inference mode have no version.
 void written(PyObject* given) {
@@ -276,40 +292,43 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     const auto type = x.scalar_type(), out_type = quant ? at::kFloat8_e4m3fn : type;
     rows(x, "x", shape, type, device, a.x_stride);
     if (res) rows(*res, "residual", shape, type, device, a.residual_stride);
-    at::Tensor made_out, made_res, made_scales;
-    if (!out) {
-      made_out = empty(shape, out_type, device);
-      out = &made_out;
-    }
-    rows(*out, "out", shape, out_type, device, a.out_stride);
-    if (res) {
-      if (!res_out) {
-        made_res = empty(shape, type, device);
-        res_out = &made_res;
-      }
-      rows(*res_out, "residual_out", shape, type, device, a.residual_out_stride);
-    }
-    if (quant) {
-      std::vector<int64_t> want(shape.begin(), shape.end());
-      want.back() = group ? (want.back() + group - 1) / group : 1;
-      if (!scales) {
-        made_scales = empty(want, at::kFloat, device);
-        scales = &made_scales;
-      } else if (scales->scalar_type() != at::kFloat || scales->sizes() != at::IntArrayRef(want) ||
-                 !scales->is_contiguous()) {
-        throw WrongValue("scales must be contiguous float32 of shape " + shape_text(want));
-      }
+    if (out) rows(*out, "out", shape, out_type, device, a.out_stride);
+    if (res_out) rows(*res_out, "residual_out", shape, type, device, a.residual_out_stride);
+    c10::SmallVector<int64_t, 5> scale_shape(shape.begin(), shape.end());
+    scale_shape.back() = group ? (shape.back() + group - 1) / group : 1;
+    if (scales) {
+      if (scales->scalar_type() != at::kFloat || scales->sizes() != at::IntArrayRef(scale_shape) ||
+          !scales->is_contiguous())
+        throw WrongValue("scales must be contiguous float32 of shape " + shape_text(scale_shape));
       check_device(*scales, device, "scales");
-      a.scales = static_cast<float*>(data(*scales));
     }
     row_counts(shape, &a.outer, &a.inner, &a.cols);
-    a.x = data(x);
-    a.residual = res ? data(*res) : nullptr;
-    a.weight = w ? data(*w) : nullptr;
-    a.out = data(*out);
-    a.residual_out = res ? data(*res_out) : nullptr;
     a.group = (int)group;
-    check(ringsim_rms_norm(&a, current_stream(device)), "ringsim_rms_norm");
+    at::Tensor made_out, made_res, made_scales;
+    {
+      const Unlocked unlocked;
+      if (!out) {
+        made_out = empty(shape, out_type, device);
+        rows(made_out, "out", shape, out_type, device, a.out_stride);
+        out = &made_out;
+      }
+      if (res && !res_out) {
+        made_res = empty(shape, type, device);
+        rows(made_res, "residual_out", shape, type, device, a.residual_out_stride);
+        res_out = &made_res;
+      }
+      if (quant && !scales) {
+        made_scales = empty(scale_shape, at::kFloat, device);
+        scales = &made_scales;
+      }
+      a.x = data(x);
+      a.residual = res ? data(*res) : nullptr;
+      a.weight = w ? data(*w) : nullptr;
+      a.out = data(*out);
+      a.residual_out = res ? data(*res_out) : nullptr;
+      a.scales = quant ? static_cast<float*>(data(*scales)) : nullptr;
+      check(ringsim_rms_norm(&a, current_stream(device)), "ringsim_rms_norm");
+    }
     for (int i = 6; i < 9; ++i) written(args[i]);
     return pack({result(args[6], made_out), result(args[7], made_res), result(args[8], made_scales)});
   });
@@ -325,6 +344,8 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) 
     const int device = current_device();
     ringsim_rms_norm_backward_t a{};
     a.eps = (float)number(args[4]);
+    const int need = PyObject_IsTrue(args[7]);
+    if (need < 0) throw PythonError{};
     norm_types(h, w, "h", device, &a.dtype, &a.weight_dtype);
     if (!w && dw) throw WrongValue("grad_weight needs a weight");
     const auto shape = h.sizes();
@@ -337,43 +358,43 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) 
         throw WrongValue("grad_weight must be contiguous, of the weight's shape and dtype");
       check_device(*dw, device, "grad_weight");
     }
-    at::Tensor made_dx, made_dw, workspace;
-    if (!dx) {
-      made_dx = empty(shape, type, device);
-      dx = &made_dx;
-    }
-    rows(*dx, "grad_in", shape, type, device, a.grad_in_stride);
+    if (dx) rows(*dx, "grad_in", shape, type, device, a.grad_in_stride);
     row_counts(shape, &a.outer, &a.inner, &a.cols);
-    const int need = PyObject_IsTrue(args[7]);
-    if (need < 0) throw PythonError{};
-    if (w && (need || dw)) {
-      if (!dw) {
-        made_dw = empty(w->sizes(), w->scalar_type(), device);
-        dw = &made_dw;
+    at::Tensor made_dx, made_dw, workspace;
+    {
+      const Unlocked unlocked;
+      if (!dx) {
+        made_dx = empty(shape, type, device);
+        rows(made_dx, "grad_in", shape, type, device, a.grad_in_stride);
+        dx = &made_dx;
       }
-      size_t bytes = 0;
-      check(ringsim_rms_norm_backward_workspace(a.outer * a.inner, a.cols, a.dtype, &bytes),
-            "ringsim_rms_norm_backward_workspace");
-      if (bytes) {
-        workspace = empty({(int64_t)bytes}, at::kByte, device);
-        a.workspace = data(workspace);
+      if (w && (need || dw)) {
+        if (!dw) {
+          made_dw = empty(w->sizes(), w->scalar_type(), device);
+          dw = &made_dw;
+        }
+        check(ringsim_rms_norm_backward_workspace(a.outer * a.inner, a.cols, a.dtype, &a.workspace_bytes),
+              "ringsim_rms_norm_backward_workspace");
+        if (a.workspace_bytes) {
+          workspace = empty({(int64_t)a.workspace_bytes}, at::kByte, device);
+          a.workspace = data(workspace);
+        }
+        a.grad_weight = data(*dw);
       }
-      a.grad_weight = data(*dw);
-      a.workspace_bytes = bytes;
+      a.grad_out = data(dy);
+      a.h = data(h);
+      a.weight = w ? data(*w) : nullptr;
+      a.grad_residual = res ? data(*res) : nullptr;
+      a.grad_in = data(*dx);
+      check(ringsim_rms_norm_backward(&a, current_stream(device)), "ringsim_rms_norm_backward");
     }
-    a.grad_out = data(dy);
-    a.h = data(h);
-    a.weight = w ? data(*w) : nullptr;
-    a.grad_residual = res ? data(*res) : nullptr;
-    a.grad_in = data(*dx);
-    check(ringsim_rms_norm_backward(&a, current_stream(device)), "ringsim_rms_norm_backward");
     for (int i = 5; i < 7; ++i) written(args[i]);
     return pack({result(args[5], made_dx), result(args[6], made_dw)});
   });
 }
 
-// A list of gradients as the C ABI takes it. The sequence is held while its
-// tensors are in use.
+// A list of gradients as the C ABI takes it. Its tensors are held by a tuple of
+// its own, since other threads may change the caller's list during the call.
 struct GradList {
   PyObject* seq = nullptr;
   std::vector<void*> ptrs;
@@ -381,16 +402,15 @@ struct GradList {
   std::vector<int> types;
 
   GradList(PyObject* o, const char* name, int device) {
-    seq = PySequence_Fast(o, "expected a sequence of tensors");
+    seq = PySequence_Tuple(o);
     if (!seq) throw PythonError{};
     try {
-      const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq);
-      PyObject** items = PySequence_Fast_ITEMS(seq);
+      const Py_ssize_t n = PyTuple_GET_SIZE(seq);
       ptrs.reserve(n);
       counts.reserve(n);
       types.reserve(n);
       for (Py_ssize_t i = 0; i < n; ++i) {
-        const at::Tensor& t = required(items[i], name);
+        const at::Tensor& t = required(PyTuple_GET_ITEM(seq, i), name);
         const int code = type_code(t.scalar_type());
         if (code < 0) throw WrongType(std::string("unsupported dtype ") + c10::toString(t.scalar_type()) + " in " + name);
         check_device(t, device, name);
@@ -410,7 +430,7 @@ struct GradList {
   GradList& operator=(const GradList&) = delete;
   int size() const { return (int)ptrs.size(); }
   void all_written() const {
-    for (int i = 0; i < size(); ++i) written(PySequence_Fast_GET_ITEM(seq, i));
+    for (int i = 0; i < size(); ++i) written(PyTuple_GET_ITEM(seq, i));
   }
 };
 
@@ -421,41 +441,49 @@ const GradList* match(const GradList* outs, const GradList& grads) {
   return outs;
 }
 
-float* norm_ptr(PyObject* o, at::Tensor& made, int device) {
+// The norm an argument holds; null for None.
+const at::Tensor* norm_arg(PyObject* o, int device) {
   const at::Tensor* t = tensor(o, "norm");
-  if (!t) {
-    made = empty({}, at::kFloat, device);
-    t = &made;
-  } else {
-    if (t->scalar_type() != at::kFloat || t->numel() != 1) throw WrongValue("norm must be one float32");
-    check_device(*t, device, "norm");
-  }
-  return static_cast<float*>(data(*t));
+  if (!t) return nullptr;
+  if (t->scalar_type() != at::kFloat || t->numel() != 1) throw WrongValue("norm must be one float32");
+  check_device(*t, device, "norm");
+  return t;
 }
 
-// The workspace of a list, if it needs one; `bytes` are its size.
-at::Tensor norm_workspace(const GradList& g, size_t* bytes, int device) {
-  check(ringsim_grad_norm_workspace(g.size(), g.counts.data(), g.types.data(), bytes), "ringsim_grad_norm_workspace");
-  return *bytes ? empty({(int64_t)*bytes}, at::kByte, device) : at::Tensor();
-}
-void* address(const at::Tensor& t) { return t.defined() ? data(t) : nullptr; }
+// What a call that forms a norm writes: the norm, and a workspace if its list
+// needs one.
+struct NormMemory {
+  at::Tensor made, workspace;
+  float* norm;
+  size_t bytes = 0;
+
+  NormMemory(const GradList& g, const at::Tensor* given, int device) {
+    if (!given) made = empty({}, at::kFloat, device);
+    norm = static_cast<float*>(data(given ? *given : made));
+    check(ringsim_grad_norm_workspace(g.size(), g.counts.data(), g.types.data(), &bytes), "ringsim_grad_norm_workspace");
+    if (bytes) workspace = empty({(int64_t)bytes}, at::kByte, device);
+  }
+  void* space() const { return workspace.defined() ? data(workspace) : nullptr; }
+};
 
 // grad_norm(grads, scale, norm)
 PyObject* grad_norm(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return guarded([&] {
     want_args(nargs, 3);
     const int device = current_device();
-    const GradList g(args[0], "grads", device);
     const float scale = (float)number(args[1]);
-    at::Tensor made;
-    float* norm = norm_ptr(args[2], made, device);
-    size_t bytes = 0;
-    const at::Tensor ws = norm_workspace(g, &bytes, device);
-    check(ringsim_grad_norm(g.size(), g.ptrs.data(), g.counts.data(), g.types.data(), scale, norm, address(ws), bytes,
-                            current_stream(device)),
-          "ringsim_grad_norm");
+    const GradList g(args[0], "grads", device);
+    const at::Tensor* norm = norm_arg(args[2], device);
+    std::optional<NormMemory> m;
+    {
+      const Unlocked unlocked;
+      m.emplace(g, norm, device);
+      check(ringsim_grad_norm(g.size(), g.ptrs.data(), g.counts.data(), g.types.data(), scale, m->norm, m->space(),
+                              m->bytes, current_stream(device)),
+            "ringsim_grad_norm");
+    }
     written(args[2]);
-    return result(args[2], made);
+    return result(args[2], m->made);
   });
 }
 
@@ -464,17 +492,19 @@ PyObject* scale_grads(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return guarded([&] {
     want_args(nargs, 6);
     const int device = current_device();
+    const float max_norm = (float)number(args[2]), scale = (float)number(args[4]), eps = (float)number(args[5]);
     const GradList g(args[0], "grads", device);
     required(args[1], "norm");
-    at::Tensor unused;
-    const float* norm = norm_ptr(args[1], unused, device);
-    c10::optional<GradList> outs;
+    const at::Tensor* norm = norm_arg(args[1], device);
+    std::optional<GradList> outs;
     if (args[3] != Py_None) outs.emplace(args[3], "outs", device);
     const GradList* o = match(outs ? &*outs : nullptr, g);
-    check(ringsim_scale_grads(g.size(), g.ptrs.data(), o ? o->ptrs.data() : nullptr, g.counts.data(), g.types.data(),
-                              (float)number(args[4]), norm, (float)number(args[2]), (float)number(args[5]),
-                              current_stream(device)),
-          "ringsim_scale_grads");
+    {
+      const Unlocked unlocked;
+      check(ringsim_scale_grads(g.size(), g.ptrs.data(), o ? o->ptrs.data() : nullptr, g.counts.data(), g.types.data(),
+                                scale, static_cast<const float*>(data(*norm)), max_norm, eps, current_stream(device)),
+            "ringsim_scale_grads");
+    }
     (o ? o : &g)->all_written();
     return none();
   });
@@ -485,21 +515,23 @@ PyObject* clip_grads(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   return guarded([&] {
     want_args(nargs, 6);
     const int device = current_device();
+    const float max_norm = (float)number(args[1]), scale = (float)number(args[3]), eps = (float)number(args[4]);
     const GradList g(args[0], "grads", device);
-    c10::optional<GradList> outs;
+    std::optional<GradList> outs;
     if (args[2] != Py_None) outs.emplace(args[2], "outs", device);
     const GradList* o = match(outs ? &*outs : nullptr, g);
-    at::Tensor made;
-    float* norm = norm_ptr(args[5], made, device);
-    size_t bytes = 0;
-    const at::Tensor ws = norm_workspace(g, &bytes, device);
-    check(ringsim_clip_grads(g.size(), g.ptrs.data(), o ? o->ptrs.data() : nullptr, g.counts.data(), g.types.data(),
-                             (float)number(args[3]), (float)number(args[1]), (float)number(args[4]), norm, address(ws),
-                             bytes, current_stream(device)),
-          "ringsim_clip_grads");
+    const at::Tensor* norm = norm_arg(args[5], device);
+    std::optional<NormMemory> m;
+    {
+      const Unlocked unlocked;
+      m.emplace(g, norm, device);
+      check(ringsim_clip_grads(g.size(), g.ptrs.data(), o ? o->ptrs.data() : nullptr, g.counts.data(), g.types.data(),
+                               scale, max_norm, eps, m->norm, m->space(), m->bytes, current_stream(device)),
+            "ringsim_clip_grads");
+    }
     (o ? o : &g)->all_written();
     written(args[5]);
-    return result(args[5], made);
+    return result(args[5], m->made);
   });
 }
 
