@@ -28,7 +28,7 @@
  *   - Results do not depend on timing: the same call on the same values gives
  *     the same bits (no floating-point atomics).
  *   - Arithmetic is in fp32 (sums of squares of gradients in fp64), each
- *     output rounded once to its type, round to nearest even. Infinities and
+ *     result rounded once to its output's type, round to nearest even. Infinities and
  *     NaN take the course the formulas give them.
  */
 #ifndef RINGSIM_OPS_H
@@ -86,8 +86,11 @@ typedef struct {
  * before it is rounded. With out_dtype FLOAT8_E4M3, out and scales receive,
  * for every group of `group` columns (the last one may be shorter; groups =
  * ceil(cols / group), or 1):
- *     scale = max(max|y| / 448, 2^-126),  q = y / scale
- * so that q * scale stands for y; a NaN in a group makes its scale NaN.
+ *     scale = max(max|y| / 448, 2^-126),  q = y * (1 / scale)
+ * so that q * scale stands for y; a NaN in a group makes its scale NaN. The
+ * reciprocal and the product are fp32 values: q is y / scale rounded to
+ * nearest, but where y / scale lies within 2^-22 of itself from the middle of
+ * two 8-bit values it may be either of them.
  * residual_out, and out in the rows' type, may be x or residual themselves
  * (same address, same strides); otherwise outputs must not overlap inputs or
  * each other. A row whose sum of squares is beyond fp32's range gives zeros,

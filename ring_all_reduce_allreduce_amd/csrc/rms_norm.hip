@@ -145,8 +145,10 @@ __device__ __forceinline__ void take_row(const RmsNormArgs& a, const NormRow<NP>
       } else if (c < a.cols && c % a.group == 0) {
         ps[c / a.group] = scale;
       }
-      // |y| * inv is at most 448 (1 + 2^-22), which rounds to 448, the
-      // largest e4m3 value: nothing to clamp.
+      // One division a scale, one product an element, whose two roundings of
+      // 2^-24 decide only which side a value next to a tie falls on (8 of 16
+      // million). |y| * inv is at most 448 (1 + 2^-22), which rounds to 448,
+      // the largest e4m3 value: nothing to clamp.
       const float inv = 1.0f / scale;
       uint32_t b[kPack / 4];
 #pragma unroll
