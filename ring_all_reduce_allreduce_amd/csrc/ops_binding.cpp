@@ -4,8 +4,8 @@
 //
 // Compiled, not ctypes like the collectives' binding, because it is the host
 // that bounds small calls: marshalling in Python took 12-18 us a call and
-// 0.4 us for every tensor of a list, where the kernels of one token take about
-// 4 us. operators.py holds the functions users call; arguments arrive here by
+// 0.4 us for every tensor of a list (here 12 to 16 ns), where the kernels of
+// one token take about 4 us. operators.py holds the functions users call; arguments arrive here by
 // position.
 #include <Python.h>
 

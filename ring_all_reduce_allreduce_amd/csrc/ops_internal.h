@@ -80,7 +80,9 @@ constexpr int kGradTileBytes = 16384;
 constexpr int kGradWorkgroups = 1024;  // most of a launch that leaves a sum each
 // Scaling takes a workgroup a tile: the hardware starts the next one while
 // this one's stores drain. 40 buckets of 25 MiB take 332 us so, with 1024
-// workgroups that walk the tiles 365, although each joins the sums for itself.
+// workgroups that walk the tiles 365, although each joins the 1024 sums of one
+// launch of squares for itself (a list of several launches has as many times
+// the sums to join in the first launch that scales).
 constexpr uint32_t kGradScaleWorkgroups = 1u << 22;
 constexpr int kGradTensors = 330;     // of a launch that reads, or writes in place
 constexpr int kGradOutTensors = 196;  // of one that writes elsewhere

@@ -201,8 +201,8 @@ ringsim_result_t enqueue_short(int n, const void* const* grads, void* const* out
 }
 
 // What a pass over the gradients may leave for the next one in the Infinity
-// Cache of 256 MiB. (Clipping 40 buckets of 25 MiB: 519 us, with nothing read
-// to stay 529, with everything 535.)
+// Cache of 256 MiB. (Clipping 40 buckets of 25 MiB: 485 us, with nothing read
+// to stay 491, with everything 492.)
 constexpr int64_t kGradKeepBytes = 192ll << 20;
 
 bool valid_factor(float scale, float max_norm, float eps) {

@@ -12,7 +12,8 @@
 // hardware starts the next workgroup while this one waits at its barrier.
 // Workgroups that walked rows with the weights kept in registers took 94
 // against 78 us for 8192 rows of 8192 into 8 bits, 13.5 against 10.2 us for
-// 1021 rows of 5119, and one more memory latency for a single row.
+// 1021 rows of 5119 (on four waves each; on the five they have now 8.4), and
+// one more memory latency for a single row.
 #include <algorithm>
 
 #include "ops_device.h"
@@ -243,7 +244,7 @@ static hipError_t launch_shape(const RmsNormArgs& a, int lanes, hipStream_t s) {
 // Lanes by the packs of a row: a part of a wave, a wave, or as many whole
 // waves as `np` packs a lane leave. Few packs a lane keep short rows spread
 // out; more of them, up to what 1024 lanes need, keep the waves that meet at
-// the barrier few. 1021 rows of 5119 fp16 (640 packs) take 8.3 us on five
+// the barrier few. 1021 rows of 5119 fp16 (640 packs) take 8.4 us on five
 // waves and 9.8 on four of four packs, half of the last one empty; 4096 rows
 // of 12288 bf16 into 8 bits (1536 packs) 59 us on 12 waves of two packs and
 // 71 on six of four, whose registers leave fewer workgroups on a compute unit.
