@@ -43,6 +43,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libringsim.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "ringsim.h")
 OPS_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "ringsim_ops.h")
+ATTENTION_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "ringsim_attention.h")
 
 SUCCESS = 0
 RESULT_NAMES = {
@@ -419,13 +420,18 @@ def header_exports() -> list[str]:
 
 # The step operators need torch's types, so they load with their first use
 # (the collectives' host-only calls work before torch is imported).
-_OPERATORS = ("rms_norm", "rms_norm_backward", "grad_norm", "scale_grads", "clip_grads")
+_OPERATORS = {
+    "operators": ("rms_norm", "rms_norm_backward", "grad_norm", "scale_grads", "clip_grads"),
+    "attention": ("rotary", "rotary_backward", "rotary_frequencies", "KvCache", "kv_cache", "kv_append", "kv_read",
+                  "paged_attention"),
+}
 
 
 def __getattr__(name: str):
-    if name in _OPERATORS:
-        from . import operators
+    for module, names in _OPERATORS.items():
+        if name in names:
+            import importlib
 
-        globals()[name] = getattr(operators, name)
-        return globals()[name]
+            globals()[name] = getattr(importlib.import_module(f".{module}", __name__), name)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

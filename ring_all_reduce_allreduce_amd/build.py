@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libringsim.so")
 BINDING = os.path.join(PKG, "_ops_binding.so")
 # (source, object name, extra defines): the line kernel's instantiation unit
-# is compiled once per line mode.
+# is compiled once per line mode, the attention's once per head size.
 SOURCES = [
     ("ringsim_api.hip", "ringsim_api", []),
     ("ring_bulk.hip", "ring_bulk", []),
@@ -30,7 +30,14 @@ SOURCES = [
     ("rms_norm.hip", "rms_norm", []),
     ("rms_norm_backward.hip", "rms_norm_backward", []),
     ("grad_norm.hip", "grad_norm", []),
+    ("ringsim_attention.hip", "ringsim_attention", []),
+    ("rotary.hip", "rotary", []),
+    ("kv_cache.hip", "kv_cache", []),
+    ("attention.hip", "attention", []),
+    *(("attention_inst.hip", f"attention_{d}", [f"-DRINGSIM_HEAD_DIM={d}"]) for d in (64, 96, 128, 192, 256)),
 ]
+# The Python extension's sources: host code only.
+BINDING_SOURCES = ["ops_binding", "attention_binding"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from forming packed fp32 instructions.
@@ -79,20 +86,18 @@ def build(verbose: bool = False) -> str:
     operators' Python extension, returns the library's path."""
     cc = hipcc()
     with tempfile.TemporaryDirectory(prefix="ringsim_build_") as tmp:
-        binding_obj = os.path.join(tmp, "ops_binding.o")
-        objs = []
+        objs, binding_objs = [], []
         procs = []
         jobs = [(name, [cc, *HIP_FLAGS, *defines, "-c", os.path.join(CSRC, src), "-o", os.path.join(tmp, name + ".o")])
                 for src, name, defines in SOURCES]
-        jobs.append(("ops_binding", [cc, *binding_flags(), "-c", os.path.join(CSRC, "ops_binding.cpp"), "-o",
-                                     binding_obj]))
+        jobs += [(name, [cc, *binding_flags(), "-c", os.path.join(CSRC, name + ".cpp"), "-o",
+                         os.path.join(tmp, name + ".o")]) for name in BINDING_SOURCES]
         for name, cmd in jobs:
             obj = cmd[-1]
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((name, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-            if obj != binding_obj:
-                objs.append(obj)
+            (binding_objs if name in BINDING_SOURCES else objs).append(obj)
         failed = []
         for src, p in procs:
             out, _ = p.communicate()
@@ -109,7 +114,7 @@ def build(verbose: bool = False) -> str:
         subprocess.run(cmd, check=True)
         os.replace(tmp_lib, LIB)
         # Loaded by Python, so Python's symbols stay open; libringsim.so is found beside it.
-        cmd = [cc, "-shared", "-fPIC", "-o", BINDING + ".tmp", binding_obj, f"-L{torch_lib_dir()}", "-lc10",
+        cmd = [cc, "-shared", "-fPIC", "-o", BINDING + ".tmp", *binding_objs, f"-L{torch_lib_dir()}", "-lc10",
                "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", f"-L{PKG}", "-l:libringsim.so", "-Wl,-rpath,$ORIGIN"]
         if verbose:
             print(" ".join(cmd), flush=True)

@@ -1,0 +1,148 @@
+// attention_internal.h -- kernel arguments and launch rules of the
+// attention-step operators.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ringsim_attention.h"
+#include "kv_layout.h"
+#include "ops_internal.h"
+
+namespace ringsim {
+
+// Whole-number division by a value known at launch: n / d for n below 2^31 is
+// (n * mul) >> (32 + shift), with mul rounded up from 2^(32 + shift) / d and
+// 2^shift the least power of two that is not below d.
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t shift = 0;
+  while ((1ull << shift) < d) ++shift;
+  return FastDiv{d, (uint32_t)((((1ull << shift) - d) << 32) / d + 1), shift};
+}
+__host__ __device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) {
+  const uint32_t t = (uint32_t)(((uint64_t)n * f.mul) >> 32);
+  return (uint32_t)(((uint64_t)t + n) >> f.shift);
+}
+
+// Whole numbers of either width in device memory, [outer, inner].
+struct Index {
+  const void* p;
+  int64_t s0, s1;
+  int wide;  // 64 bits
+};
+
+// [outer, inner, heads, dim]
+struct HeadRows {
+  const void* p;
+  int64_t s0, s1, s2;
+};
+struct HeadRowsOut {
+  void* p;
+  int64_t s0, s1, s2;
+};
+
+struct RotaryArgs {
+  HeadRows x;
+  HeadRowsOut out;
+  Index positions;
+  const double* frequencies;
+  uint32_t tokens, inner, heads;
+  int dim, pairs;
+  int packs;        // items of a head
+  int turned;       // of them, those that hold pairs; the others copy
+  int block_tokens; // of a workgroup
+  int block_heads;
+  uint32_t blocks;  // of tokens
+  FastDiv by_packs, by_heads, by_pairs;
+  int interleaved;
+  float sign, scale;
+};
+hipError_t launch_rotary(RotaryArgs a, int dtype, hipStream_t s);
+
+struct KvCacheArgs {
+  uint8_t* data[2];    // keys, values
+  uint8_t* scales[2];
+  int64_t page, head;  // strides in bytes
+  int64_t scale_page, scale_head;
+  int32_t pages;
+  int heads, dim, page_shift;
+};
+
+struct KvAppendArgs {
+  KvCacheArgs cache;
+  HeadRows x[2];       // keys, values
+  Index slots, positions;
+  const double* frequencies;
+  uint32_t tokens, inner;
+  int pairs, interleaved;
+  float scale;
+  int block_tokens, block_heads;
+  uint32_t blocks;     // of tokens
+  FastDiv by_packs, by_tokens, by_pairs;
+};
+hipError_t launch_kv_append(KvAppendArgs a, int dtype, hipStream_t s);
+
+struct KvReadArgs {
+  KvCacheArgs cache;
+  HeadRowsOut out[2];  // p null: not wanted
+  Index slots;
+  uint32_t tokens, inner;
+  FastDiv by_packs, by_heads;
+};
+hipError_t launch_kv_read(KvReadArgs a, int dtype, hipStream_t s);
+
+struct AttentionArgs {
+  KvCacheArgs cache;
+  HeadRows q;          // {sequence, token, head}
+  HeadRowsOut out;
+  float* lse;
+  const int32_t* pages;
+  const int32_t* lengths;
+  const int32_t* starts;  // null: `each` tokens a sequence
+  float* part_out;        // [splits, tokens * heads, dim], with splits > 1
+  float* part_ml;         // [splits, tokens * heads, 2]: reference exponent and sum
+  int64_t page_stride;
+  int64_t cap;            // positions that a sequence can have
+  int64_t max_pages;
+  int64_t tokens, seqs;
+  int64_t window;
+  int64_t each;
+  int64_t chunk;          // positions of a split, a multiple of kKvStep
+  int splits;
+  int group;              // query heads of a key head
+  int heads;              // of queries
+  int tiles;              // of rows, over all sequences
+  int tile_rows;
+  int causal;
+  float scale_log2;       // scale * log2(e) / kQueryUnit
+};
+
+// Queries go into the first product times this power of two, which the scale
+// takes back: the largest queries have products with a cache's usual values
+// that fp32 would not hold.
+constexpr float kQueryUnit = 0x1p-8f;
+
+// How a call is cut: rows of a workgroup, workgroups, and parts of the context.
+struct AttentionPlan {
+  int wide;               // 1: many rows, a wave its own rows; 0: waves share rows
+  int tile_rows;
+  int64_t tiles;
+  int64_t chunk;
+  int splits;
+};
+AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
+                             int64_t cap, int64_t window);
+
+hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, int dtype, hipStream_t s);
+// One unit for each head size, so that they compile side by side.
+hipError_t launch_attention_64(const AttentionArgs&, const AttentionPlan&, int, hipStream_t);
+hipError_t launch_attention_96(const AttentionArgs&, const AttentionPlan&, int, hipStream_t);
+hipError_t launch_attention_128(const AttentionArgs&, const AttentionPlan&, int, hipStream_t);
+hipError_t launch_attention_192(const AttentionArgs&, const AttentionPlan&, int, hipStream_t);
+hipError_t launch_attention_256(const AttentionArgs&, const AttentionPlan&, int, hipStream_t);
+hipError_t launch_attention_join(const AttentionArgs& a, int dtype, hipStream_t s);
+
+}  // namespace ringsim

@@ -1,0 +1,81 @@
+// kv_layout.h -- where the paged cache keeps a token, how a block's exponent
+// is chosen, and which rows of queries a workgroup takes. Plain functions of
+// whole numbers, used by the kernels and tested on the host.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIPCC__)
+#define KV_FN __host__ __device__ __forceinline__
+#else
+#define KV_FN inline
+#endif
+
+namespace ringsim {
+
+constexpr int kKvBlock = 32;         // columns that share an exponent
+constexpr int kKvNan = 255;          // exponent byte of 32 NaN
+constexpr int kKvMinByte = 1;        // 2^-126, the smallest normal fp32
+constexpr int kKvMaxByte = 252;      // 2^125: 6 times it is still finite
+constexpr int kKvTile = 16;          // tokens of a matrix instruction's operand
+constexpr int kKvStep = 32;          // tokens of one pass of the attention's loop
+
+// Exponent byte of a block whose largest magnitude has the bits `top`: with
+// 2^x <= max < 2^(x+1), the least e with max <= 7 * 2^e is x - 2 if the
+// mantissa is at most 1.75 (7 = 1.75 * 4), else x - 1; the addition carries
+// into the exponent exactly above 1.75.
+KV_FN int kv_exponent_byte(uint32_t top) {
+  if (top >= 0x7f800000u) return kKvNan;
+  const int b = (int)((top + 0x1fffffu) >> 23) - 2;
+  return b < kKvMinByte ? kKvMinByte : b > kKvMaxByte ? kKvMaxByte : b;
+}
+
+// Whether a slot lies in the cache; its page and token there.
+KV_FN bool kv_slot(int64_t slot, int64_t pages, int page_shift, int32_t* page, int* token) {
+  if (slot < 0 || (slot >> page_shift) >= pages) return false;
+  *page = (int32_t)(slot >> page_shift);
+  *token = (int)(slot & ((1 << page_shift) - 1));
+  return true;
+}
+
+// Page of a sequence's tile of kKvTile tokens, -1 where there is none: past
+// the sequence, past its row of the table, or a number that is no page.
+// `table` is read only for a place inside it.
+KV_FN int32_t kv_page_of_tile(const int32_t* table, int64_t tile, int64_t end, int page_shift, int64_t max_pages,
+                              int64_t pages) {
+  const int64_t token = tile * kKvTile, place = token >> page_shift;
+  if (tile < 0 || token >= end || place >= max_pages) return -1;
+  const int32_t id = table[place];
+  return id >= 0 && id < pages ? id : -1;
+}
+
+// Rows of queries. Sequence b has (starts[b+1] - starts[b]) * group rows of a
+// key head, which are cut into tiles of `rows`; its tiles are numbered from
+// kv_first_tile(starts[b], ...). ceil(n / rows) <= floor((a + n) / rows) -
+// floor(a / rows) + 1, so that no two sequences share a number, and all
+// numbers lie below tokens * group / rows + seqs.
+KV_FN int64_t kv_first_tile(int64_t start, int64_t b, int64_t group, int64_t rows) { return start * group / rows + b; }
+
+KV_FN int64_t kv_clamp(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// The sequence whose tiles hold number `tile`: the last b with first(b) <= tile.
+KV_FN int64_t kv_seq_of_tile(const int32_t* starts, int64_t seqs, int64_t tokens, int64_t group, int64_t rows,
+                             int64_t tile) {
+  int64_t lo = 0, hi = seqs - 1;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) >> 1;
+    if (kv_first_tile(kv_clamp(starts[mid], 0, tokens), mid, group, rows) <= tile)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// Positions [*lo, *hi] that the token at position p sees, of `end` positions.
+KV_FN void kv_span(int64_t p, int64_t end, int causal, int64_t window, int64_t* lo, int64_t* hi) {
+  *hi = causal && p < end - 1 ? p : end - 1;
+  *lo = window > 0 && p - window + 1 > 0 ? p - window + 1 : 0;
+}
+
+}  // namespace ringsim

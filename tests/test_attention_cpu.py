@@ -1,0 +1,281 @@
+"""Host-side checks of the attention-step operators (include/ringsim_attention.h)
+that need no GPU: exports, structures, refusals of the C entry points and of the
+binding."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import ring_all_reduce_allreduce_amd as rs
+from ring_all_reduce_allreduce_amd import build
+
+if not (os.path.exists(build.LIB) and os.path.exists(build.BINDING)):
+    build.build()
+from ring_all_reduce_allreduce_amd import attention as att  # noqa: E402
+
+OK, BAD = 0, 4
+I32, I64, F32, BF16, F16, E4M3 = 0, 1, 2, 3, 16, 17
+P = 1 << 20  # an address that is never read: the call is refused first
+
+
+def _header():
+    with open(rs.ATTENTION_HEADER_PATH) as f:
+        return f.read()
+
+
+def _structs():
+    """ctypes structures with the fields the header declares."""
+    types = {"int": ctypes.c_int, "int64_t": ctypes.c_int64, "size_t": ctypes.c_size_t, "float": ctypes.c_float}
+    made = {}
+    for body, cname in re.findall(r"typedef struct \{((?:(?!typedef struct).)*?)\}\s*(\w+);", _header(), re.S):
+        body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
+        fields = []
+        for ctype, star, name, n in re.findall(r"^\s*(?:const\s+)?([a-z_0-9]+)(\*?)\s+([a-z_0-9]+)(?:\[(\d)\])?;", body,
+                                               re.M):
+            t = ctypes.c_void_p if star else types[ctype] if ctype in types else made[ctype]
+            fields.append((name, t * int(n) if n else t))
+        assert len(fields) == body.count(";"), cname
+        made[cname] = type(cname, (ctypes.Structure,), {"_fields_": fields})
+    return made
+
+
+S = _structs()
+
+
+@pytest.fixture(scope="module")
+def L():
+    lib = ctypes.CDLL(rs.lib()._name)
+    vp = ctypes.c_void_p
+    for name in ("rotary", "kv_append", "kv_read", "paged_attention"):
+        getattr(lib, "ringsim_" + name).argtypes = [vp, vp]
+    lib.ringsim_paged_attention_workspace.argtypes = [vp, ctypes.POINTER(ctypes.c_size_t)]
+    return lib
+
+
+def _fill(a, values):
+    for k, x in values.items():
+        f = getattr(a, k)
+        setattr(a, k, type(f)(*x) if isinstance(x, tuple) else x)
+    return a
+
+
+CACHE = dict(keys=P, values=P, key_scales=P, value_scales=P, stride=(1 << 20, 1 << 16), scale_stride=(1 << 16, 1 << 12),
+             pages=4, heads=2, page_size=64, dim=128)
+
+
+def _cache(**over):
+    return _fill(S["ringsim_kv_cache_t"](), {**CACHE, **over})
+
+
+def test_exports_every_declared_function(L):
+    declared = sorted(set(re.findall(r"^ringsim_result_t (ringsim_[a-z_]+)\(", _header(), re.M)))
+    assert len(declared) == 5
+    out = subprocess.run(["nm", "-D", "--defined-only", rs.LIB_PATH], check=True, capture_output=True, text=True).stdout
+    exported = {line.split()[-1] for line in out.splitlines() if line.strip()}
+    assert set(declared) <= exported
+    for f in ("rotary", "rotary_backward", "rotary_frequencies", "KvCache", "kv_cache", "kv_append", "kv_read",
+              "paged_attention"):
+        assert getattr(rs, f) is getattr(att, f)
+
+
+def _rotary(**over):
+    v = dict(x=P, out=2 * P, positions=P, frequencies=P, x_stride=(512, 0, 128), out_stride=(512, 0, 128),
+             position_stride=(1, 0), outer=4, inner=1, heads=4, dim=128, pairs=64, dtype=BF16, position_dtype=I64,
+             scale=1.0)
+    v.update(over)
+    return ctypes.byref(_fill(S["ringsim_rotary_t"](), v))
+
+
+@pytest.mark.parametrize("over", [
+    dict(x=None), dict(out=None), dict(positions=None), dict(frequencies=None), dict(x=P + 1), dict(out=P + 1),
+    dict(positions=P + 4), dict(positions=P + 2, position_dtype=I32), dict(frequencies=P + 4), dict(dtype=I32),
+    dict(dtype=E4M3), dict(dtype=99), dict(position_dtype=F32), dict(outer=-1), dict(inner=-1), dict(outer=1 << 31),
+    dict(outer=1 << 40, inner=1 << 40), dict(heads=-1), dict(heads=65536), dict(dim=0), dict(dim=2049, pairs=1),
+    dict(pairs=65), dict(pairs=-1), dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(out_stride=(511, 0, 128)), dict(out_stride=(512, 0, 127)), dict(out_stride=(0, 0, 128)),
+    dict(out_stride=(128, 0, 128)), dict(inner=2, out_stride=(512, 512, 128)), dict(x_stride=(1 << 60, 0, 128)),
+    dict(position_stride=(1 << 60, 0)), dict(out=P, out_stride=(1024, 0, 128)),
+], ids=str)
+def test_rotary_refuses(L, over):
+    assert L.ringsim_rotary(_rotary(**over), None) == BAD
+
+
+def test_rotary_without_rows(L):
+    assert L.ringsim_rotary(None, None) == BAD
+    for over in (dict(outer=0), dict(inner=0), dict(heads=0)):
+        assert L.ringsim_rotary(_rotary(x=None, out=None, positions=None, **over), None) == OK
+
+
+def _append(cache=None, **over):
+    v = dict(k=P, v=P, slots=P, positions=P, frequencies=P, k_stride=(256, 0, 128), v_stride=(256, 0, 128),
+             slot_stride=(1, 0), position_stride=(1, 0), outer=4, inner=1, pairs=64, dtype=BF16, slot_dtype=I64,
+             position_dtype=I32, scale=1.0)
+    v.update(over)
+    a = _fill(S["ringsim_kv_append_t"](), v)
+    a.cache = _cache(**(cache or {}))
+    return ctypes.byref(a)
+
+
+def _read(cache=None, **over):
+    v = dict(k=P, v=P, slots=P, k_stride=(256, 0, 128), v_stride=(256, 0, 128), slot_stride=(1, 0), outer=4, inner=1,
+             dtype=BF16, slot_dtype=I64)
+    v.update(over)
+    a = _fill(S["ringsim_kv_read_t"](), v)
+    a.cache = _cache(**(cache or {}))
+    return ctypes.byref(a)
+
+
+BAD_CACHES = [dict(keys=None), dict(values=None), dict(key_scales=None), dict(value_scales=None), dict(keys=P + 8),
+              dict(value_scales=P + 4), dict(stride=((1 << 20) + 8, 1 << 16)), dict(scale_stride=(1 << 16, (1 << 12) + 4)),
+              dict(pages=0), dict(pages=1 << 31), dict(heads=0), dict(heads=65536), dict(page_size=8),
+              dict(page_size=48), dict(page_size=2048), dict(page_size=0), dict(page_size=-16), dict(dim=0), dict(dim=32),
+              dict(dim=80), dict(dim=160), dict(dim=512), dict(stride=(1 << 60, 1 << 16))]
+
+
+@pytest.mark.parametrize("cache", BAD_CACHES, ids=str)
+def test_caches_refused(L, cache):
+    assert L.ringsim_kv_append(_append(cache), None) == BAD
+    assert L.ringsim_kv_read(_read(cache), None) == BAD
+    assert L.ringsim_paged_attention(_attention(cache), None) == BAD
+
+
+@pytest.mark.parametrize("cache", [dict(stride=(4080, 1 << 16)), dict(stride=(0, 1 << 16)), dict(stride=(1 << 20, 16)),
+                                   dict(scale_stride=(240, 1 << 12)), dict(scale_stride=(1 << 16, 128))], ids=str)
+def test_overlapping_caches_are_not_written(L, cache):
+    assert L.ringsim_kv_append(_append(cache), None) == BAD
+
+
+@pytest.mark.parametrize("over", [
+    dict(k=None), dict(v=None), dict(slots=None), dict(positions=None), dict(frequencies=None), dict(k=P + 1),
+    dict(v=P + 1), dict(slots=P + 4), dict(positions=P + 2), dict(frequencies=P + 4), dict(dtype=E4M3), dict(dtype=0),
+    dict(slot_dtype=F32), dict(position_dtype=BF16), dict(outer=-1), dict(outer=1 << 31), dict(pairs=65), dict(pairs=-1),
+    dict(scale=float("inf")), dict(k_stride=(1 << 60, 0, 128)), dict(slot_stride=(1 << 60, 0)),
+], ids=str)
+def test_append_refuses(L, over):
+    assert L.ringsim_kv_append(_append(**over), None) == BAD
+
+
+@pytest.mark.parametrize("over", [
+    dict(slots=None), dict(k=P + 1), dict(v=P + 1), dict(slots=P + 4), dict(dtype=E4M3), dict(slot_dtype=BF16),
+    dict(inner=-1), dict(k_stride=(255, 0, 128)), dict(v_stride=(256, 0, 64)), dict(v_stride=(0, 0, 128)),
+], ids=str)
+def test_read_refuses(L, over):
+    assert L.ringsim_kv_read(_read(**over), None) == BAD
+
+
+def test_without_tokens(L):
+    assert L.ringsim_kv_append(None, None) == BAD and L.ringsim_kv_read(None, None) == BAD
+    assert L.ringsim_kv_append(_append(outer=0, k=None, v=None, slots=None), None) == OK
+    assert L.ringsim_kv_read(_read(inner=0, k=None, v=None, slots=None), None) == OK
+    assert L.ringsim_kv_read(_read(k=None, v=None), None) == OK
+
+
+def _attention(cache=None, raw=False, **over):
+    v = dict(q=P, out=2 * P, lse=None, pages=P, lengths=P, starts=None, workspace=P, workspace_bytes=1 << 40,
+             q_stride=(512, 128), q_seq_stride=1024, out_stride=(512, 128), out_seq_stride=1024, page_stride=100,
+             tokens=6, heads=4, seqs=3, max_pages=100, max_length=0, window=0, dtype=BF16, causal=1, scale=0.1)
+    v.update(over)
+    a = _fill(S["ringsim_paged_attention_t"](), v)
+    a.cache = _cache(**(cache or {}))
+    return a if raw else ctypes.byref(a)
+
+
+@pytest.mark.parametrize("over", [
+    dict(q=None), dict(out=None), dict(pages=None), dict(lengths=None), dict(q=P + 1), dict(out=P + 1), dict(lse=P + 2),
+    dict(pages=P + 2), dict(lengths=P + 2), dict(starts=P + 2), dict(workspace=None), dict(workspace=P + 8),
+    dict(workspace_bytes=16), dict(dtype=E4M3), dict(dtype=I32), dict(tokens=-1), dict(tokens=7), dict(seqs=-1),
+    dict(seqs=4), dict(heads=0), dict(heads=3), dict(heads=65538), dict(tokens=3 * (1 << 28), heads=4),
+    dict(max_pages=-1), dict(max_pages=1 << 31), dict(max_length=-1), dict(window=-1), dict(scale=0.0), dict(scale=-1.0),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e38), dict(out_stride=(511, 128)),
+    dict(out_stride=(512, 64)), dict(out_seq_stride=512), dict(q_stride=(1 << 60, 128)), dict(page_stride=1 << 60),
+    dict(tokens=3 * (1 << 27), heads=2, max_pages=1),
+], ids=str)
+def test_attention_refuses(L, over):
+    assert L.ringsim_paged_attention(_attention(**over), None) == BAD
+
+
+def test_attention_without_tokens_and_workspaces(L):
+    n = ctypes.c_size_t(0)
+    assert L.ringsim_paged_attention(None, None) == BAD
+    assert L.ringsim_paged_attention_workspace(None, n) == BAD
+    assert L.ringsim_paged_attention_workspace(_attention(), None) == BAD
+    for over in (dict(tokens=0), dict(seqs=0, tokens=0)):
+        assert L.ringsim_paged_attention(_attention(q=None, out=None, pages=None, lengths=None, workspace=None, **over),
+                                         None) == OK
+        assert L.ringsim_paged_attention_workspace(_attention(**over), n) == OK and n.value == 0
+    # parts of a context: fp32 outputs with reference and sums, and none where sequences fill the card by themselves
+    assert L.ringsim_paged_attention_workspace(_attention(), n) == OK
+    assert n.value > 0 and n.value % (6 * 4) == 0
+    assert L.ringsim_paged_attention_workspace(_attention(tokens=1 << 14, seqs=1 << 14), n) == OK and n.value == 0
+    assert L.ringsim_paged_attention_workspace(_attention(max_length=17), n) == OK and n.value == 0
+    assert L.ringsim_paged_attention_workspace(_attention(max_pages=0), n) == OK and n.value == 0
+    for over in (dict(dtype=E4M3), dict(tokens=7), dict(heads=3)):
+        assert L.ringsim_paged_attention_workspace(_attention(**over), n) == BAD
+
+
+def _host():
+    cache = rs.kv_cache(2, 2, 16, 64, device="cpu")
+    x = torch.zeros(4, 2, 64)
+    i = torch.zeros(4, dtype=torch.int64)
+    f = torch.zeros(32, dtype=torch.float64)
+    pages, lengths = torch.zeros(4, 1, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    return cache, x, i, f, pages, lengths
+
+
+def test_binding_refuses_wrong_types():
+    cache, x, i, f, pages, lengths = _host()
+    for call in (lambda: rs.rotary(x.double(), i, f), lambda: rs.rotary(x, i.float(), f), lambda: rs.rotary(x, i, f.float()),
+                 lambda: rs.rotary(x, i, None), lambda: rs.rotary(x, i, f, out=x.half()),
+                 lambda: rs.rotary_backward(1, i, f), lambda: rs.rotary(x, i, f, scale="a"),
+                 lambda: rs.kv_append(1, x, x, i), lambda: rs.kv_append(cache[:3], x, x, i),
+                 lambda: rs.kv_append(rs.KvCache(*(t.int() for t in cache)), x, x, i),
+                 lambda: rs.kv_append(cache, x, x.half(), i), lambda: rs.kv_append(cache, x, x, i.float()),
+                 lambda: rs.kv_append(cache, x, x, i, i.float(), f), lambda: rs.kv_read(cache, i, dtype=torch.int32),
+                 lambda: rs.kv_read(cache, i.half()), lambda: rs.kv_read(cache, i, keys=x.half()),
+                 lambda: rs.paged_attention(x.double(), cache, pages, lengths),
+                 lambda: rs.paged_attention(x, cache, pages.long(), lengths),
+                 lambda: rs.paged_attention(x, cache, pages, lengths.long()),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, starts=torch.zeros(5, dtype=torch.int64)),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, out=x.half()),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, lse=torch.zeros(4, 2).double()),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, window=1.5)):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_binding_refuses_wrong_values():
+    cache, x, i, f, pages, lengths = _host()
+    odd = rs.KvCache(cache.keys, cache.values, cache.key_scales, cache.value_scales[:, :, :1])
+    gaps = rs.KvCache(*(torch.zeros(2, 2, 16, 64, dtype=torch.uint8)[..., ::2] for _ in range(2)), *cache[2:])
+    other = rs.KvCache(cache.keys, torch.zeros(2, 3, 16, 32, dtype=torch.uint8)[:, :2], *cache[2:])
+    starts = torch.zeros(5, dtype=torch.int32)
+    for call in (lambda: rs.rotary(x[0], i[:2], f), lambda: rs.rotary(x, i[:3], f), lambda: rs.rotary(x, i, f[:, None]),
+                 lambda: rs.rotary(x, i, torch.zeros(33, dtype=torch.float64)), lambda: rs.rotary(x, i, f[::2]),
+                 lambda: rs.rotary(x, i, f),  # host tensors
+                 lambda: rs.rotary(x.transpose(1, 2), i, f[:1]), lambda: rs.rotary(x, i, f, out=x[:3]),
+                 lambda: rs.rotary(x.view(2, 2, 2, 64), torch.zeros(3, dtype=torch.int64), f),
+                 lambda: rs.kv_cache(2, 2, 16, 80), lambda: rs.kv_cache(2, 2, 24, 64), lambda: rs.kv_cache(0, 2, 16, 64),
+                 lambda: rs.kv_append(odd, x, x, i), lambda: rs.kv_append(gaps, x, x, i),
+                 lambda: rs.kv_append(other, x, x, i), lambda: rs.kv_append(cache, x[:, :1], x[:, :1], i),
+                 lambda: rs.kv_append(cache, x, x[:3], i), lambda: rs.kv_append(cache, x, x, i[:3]),
+                 lambda: rs.kv_append(cache, x, x, i, None, f), lambda: rs.kv_append(cache, x, x, i),
+                 lambda: rs.kv_read(cache, i.view(1, 2, 2)), lambda: rs.kv_read(cache, i, dtype=torch.float32, keys=x[:3]),
+                 lambda: rs.kv_read(cache, i),
+                 lambda: rs.paged_attention(x[..., :32], cache, pages, lengths),
+                 lambda: rs.paged_attention(torch.zeros(4, 3, 64), cache, pages, lengths),
+                 lambda: rs.paged_attention(x, cache, pages[0], lengths),
+                 lambda: rs.paged_attention(x, cache, pages, lengths[:3]),
+                 lambda: rs.paged_attention(x, cache, pages[:3], lengths[:3]),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, starts=starts[:4]),
+                 lambda: rs.paged_attention(x.unsqueeze(1), cache, pages, lengths, starts=starts),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, window=-1),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, max_length=0),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, lse=torch.zeros(4, 3)),
+                 lambda: rs.paged_attention(x, cache, pages, lengths),
+                 lambda: rs.rotary_frequencies(7), lambda: rs.rotary_frequencies(8, factor=0.0),
+                 lambda: rs.rotary_frequencies(8, method="other"), lambda: rs.rotary_frequencies(8, method="ramp")):
+        with pytest.raises(ValueError):
+            call()
