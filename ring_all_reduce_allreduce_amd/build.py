@@ -16,6 +16,10 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libringsim.so")
 BINDING = os.path.join(PKG, "_ops_binding.so")
+# Results of matrix instructions in ordinary vector registers: in accumulation
+# registers, which only those instructions and moves reach, every rescaling of
+# them copies them over and back.
+MATRIX_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 # (source, object name, extra defines): the line kernel's instantiation unit
 # is compiled once per line mode, the attention's once per head size.
 SOURCES = [
@@ -34,7 +38,8 @@ SOURCES = [
     ("rotary.hip", "rotary", []),
     ("kv_cache.hip", "kv_cache", []),
     ("attention.hip", "attention", []),
-    *(("attention_inst.hip", f"attention_{d}", [f"-DRINGSIM_HEAD_DIM={d}"]) for d in (64, 96, 128, 192, 256)),
+    *(("attention_inst.hip", f"attention_{d}", [f"-DRINGSIM_HEAD_DIM={d}", *MATRIX_FLAGS])
+      for d in (64, 96, 128, 192, 256)),
 ]
 # The Python extension's sources: host code only.
 BINDING_SOURCES = ["ops_binding", "attention_binding"]

@@ -53,7 +53,7 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, i
 // splits in order. LANES lanes a row, 4 columns each.
 template <int DT, int LANES>
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs a) {
-  const int64_t all = a.tokens * a.heads;
+  const int64_t all = (int64_t)a.tokens * a.heads;
   const int64_t at = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   if (at >= all) return;
   const int64_t token = at / a.heads;
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
 
 template <int DT>
 static hipError_t launch_join(const AttentionArgs& a, hipStream_t s) {
-  const int64_t rows = a.tokens * a.heads;
+  const int64_t rows = (int64_t)a.tokens * a.heads;
   if (a.cache.dim <= 128)
     hipLaunchKernelGGL((attention_join_kernel<DT, 32>), dim3((unsigned)ceil_div(rows, 8)), dim3(256), 0, s, a);
   else

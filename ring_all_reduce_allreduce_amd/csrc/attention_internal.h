@@ -105,11 +105,12 @@ struct AttentionArgs {
   float* part_out;        // [splits, tokens * heads, dim], with splits > 1
   float* part_ml;         // [splits, tokens * heads, 2]: reference exponent and sum
   int64_t page_stride;
-  int64_t cap;            // positions that a sequence can have
   int64_t max_pages;
-  int64_t tokens, seqs;
   int64_t window;
-  int64_t each;
+  int cap;                // positions that a sequence can have
+  int tokens, seqs;
+  int each;               // tokens of a sequence without starts, and
+  int seq_tiles;          // tiles of its rows
   int64_t chunk;          // positions of a split, a multiple of kKvStep
   int splits;
   int group;              // query heads of a key head
@@ -117,13 +118,13 @@ struct AttentionArgs {
   int tiles;              // of rows, over all sequences
   int tile_rows;
   int causal;
-  float scale_log2;       // scale * log2(e) / kQueryUnit
+  float scale_log2;       // scale * log2(e) * 2^kQueryExponent
 };
 
-// Queries go into the first product times this power of two, which the scale
-// takes back: the largest queries have products with a cache's usual values
-// that fp32 would not hold.
-constexpr float kQueryUnit = 0x1p-8f;
+// Queries go into the first product divided by this power of two, which the
+// scale takes back: the largest queries have products with a cache's usual
+// values that fp32 would not hold.
+constexpr int kQueryExponent = 8;
 
 // How a call is cut: rows of a workgroup, workgroups, and parts of the context.
 struct AttentionPlan {

@@ -9,13 +9,16 @@
 // With S transposed, a lane's results S^T are the four positions 4 g + i (g
 // its group of 16 lanes) of one row, and two tiles of 16 positions are just
 // the eight positions that the lane has to bring into the second product: the
-// weights never change lanes. V's operand then has the same eight positions
-// of one column, so a lane reads a few columns of each of its positions,
-// dequantises pairs of columns, and swaps halves between positions.
+// weights never change lanes.
 //
-// Keys and values go from memory to registers and never through LDS. The
-// conversion instruction turns two codes and an exponent into two bf16, which
-// hold every value of the cache.
+// Keys go into the matrix unit as they lie in memory, 4-bit codes with an
+// exponent for every 32 columns, which is what its scaled instruction takes: a
+// lane's operand is one block. The other operand may be in 8 bits, so queries
+// are split once into parts of 8 bits with exponents of their own. Values are
+// needed by columns: a lane reads a few columns of each of its eight positions,
+// the conversion instruction turns two codes and an exponent into two bf16
+// (which hold every value of the cache), and halves are swapped between
+// positions. Nothing passes through LDS.
 #pragma once
 
 #include "attention_device.h"
@@ -24,7 +27,7 @@ namespace ringsim {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-typedef uint32_t u32x4a __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kAttentionWaves = 4;
 constexpr int kAttentionThreads = 64 * kAttentionWaves;
@@ -52,15 +55,32 @@ struct HeadParts {
   static constexpr int kRegs = regs(0) + (kParts == 2 ? regs(1) : 0);
 };
 
+// A head's columns in the first product: a matrix instruction takes 128 of
+// them. Of 4-bit operands group g of 16 lanes holds block g, columns 32 g to 32
+// g + 31; of 8-bit ones columns 16 g + j and 64 + 16 g + j, j below 16; a lane's
+// exponent is that of block g of either. Heads of 64 bring two parts of the
+// queries into one instruction; where a head ends, the last block is repeated
+// against zeros.
+template <int D, int TERMS>
+struct HeadBlocks {
+  static constexpr int kBlocks = D / 32;
+  static constexpr int kSets = (kBlocks + 3) / 4;  // of four blocks
+  static constexpr bool kPaired = kBlocks == 2;
+  static constexpr int kTurns = kPaired ? (TERMS + 1) / 2 : TERMS;  // instructions a set
+  static constexpr int kHalves = kPaired ? 1 : 2;  // of 16 columns that a lane holds of a set
+  static __device__ __forceinline__ int block(int set, int g) {
+    return kPaired ? g & 1 : min(4 * set + g, kBlocks - 1);
+  }
+  static __device__ __forceinline__ int column(int set, int half, int g) { return 128 * set + 64 * half + 16 * g; }
+};
+
 // 32 positions of the cache as they lie in memory.
 template <int D>
 struct KvRaw {
   using H = HeadParts<D>;
-  // A lane holds D / 4 columns of a key: one exponent where that is a whole
-  // part of a block, else two.
-  static constexpr int kKeyScales = 32 % (D / 4) == 0 ? 1 : 2;
-  uint32_t k[2][D / 32];
-  uint32_t ks[2][kKeyScales];
+  static constexpr int kSets = (D / 32 + 3) / 4;
+  u32x4 k[2][kSets];
+  uint32_t ks[2][kSets];
   uint32_t v[8][H::kRegs];
   uint32_t vs[2][H::kParts];
 };
@@ -73,29 +93,11 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, const uint8_t* p) {
     w[0] = *reinterpret_cast<const uint16_t*>(p);
   } else if constexpr (N == 4) {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if constexpr (N == 8) {
+  } else {
+    static_assert(N == 8, "bytes");
     const u32x2 x = *reinterpret_cast<const u32x2*>(p);
     w[0] = x[0];
     w[1] = x[1];
-  } else if constexpr (N == 12) {
-    typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
-    typedef u32x3 u32x3_e4 __attribute__((aligned(4)));
-    const u32x3_e4 x = *reinterpret_cast<const u32x3_e4*>(p);
-    w[0] = x[0];
-    w[1] = x[1];
-    w[2] = x[2];
-  } else if constexpr (N == 24) {
-    load_bytes<8>(w, p);
-    load_bytes<8>(w + 2, p + 8);
-    load_bytes<8>(w + 4, p + 16);
-  } else {
-    static_assert(N % 16 == 0, "bytes");
-#pragma unroll
-    for (int i = 0; i < N / 16; ++i) {
-      const u32x4a x = *reinterpret_cast<const u32x4a*>(p + 16 * i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[4 * i + j] = x[j];
-    }
   }
 }
 
@@ -119,7 +121,7 @@ __device__ __forceinline__ uint32_t two_columns(uint32_t codes, float unit, int 
   }
 }
 
-__device__ __forceinline__ f32x4 mfma(const u32x4a& x, const u32x4a& y, f32x4 acc) {
+__device__ __forceinline__ f32x4 mfma(const u32x4& x, const u32x4& y, f32x4 acc) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), acc, 0,
                                                  0, 0);
 }
@@ -134,23 +136,25 @@ __device__ __forceinline__ float groups_max(float v) {
   return fmaxf(__uint_as_float(t[0]), __uint_as_float(t[1]));
 }
 
-// bf16 parts that queries of a type are split into: their 8, 11 or 24 bits.
-template <int DT>
-constexpr int kQueryTerms = DT == RINGSIM_FLOAT32 ? 3 : DT == RINGSIM_FLOAT16 ? 2 : 1;
-
-// Splits x into bf16 parts whose sum it is, by cutting off (rounding could
-// carry a large x to infinity). Only the first part of an infinity is one.
-template <int TERMS>
-__device__ __forceinline__ void split_exact(float x, uint32_t (&part)[TERMS]) {
-  if (!(x == x)) x = __uint_as_float(0x7fc00000u);
-  const bool finite = fabsf(x) < __uint_as_float(0x7f800000u);
+// Codes of 4 bits with exponents `ks` times 8-bit ones with exponents `qs`.
+__device__ __forceinline__ f32x4 mfma_scaled(const u32x4& k, uint32_t ks, const i32x8& q, uint32_t qs, f32x4 acc) {
+  i32x8 x;  // 4-bit operands are the first half
 #pragma unroll
-  for (int t = 0; t < TERMS; ++t) {
-    const uint32_t hi = __float_as_uint(x) & 0xffff0000u;
-    part[t] = hi >> 16;
-    x = finite ? x - __uint_as_float(hi) : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i) x[i] = (int)k[i & 3];
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, q, acc, 4, 0, 0, (int)ks, 0, (int)qs);
 }
+
+// Parts that queries of a type are split into. With a row's largest magnitude
+// in [128, 256) a part keeps 4 bits, and each remainder is at most 8, so the
+// next part takes it times 32: 2 parts hold the 8 bits of bf16, 3 the 11 of
+// fp16, and what is left after 5 is a rounding of fp32. Columns that are small
+// beside their row's largest keep their place to 2^-22, 2^-27 and 2^-37 of it
+// (half the smallest step of the last part).
+template <int DT>
+constexpr int kQueryTerms = DT == RINGSIM_FLOAT32 ? 5 : DT == RINGSIM_FLOAT16 ? 3 : 2;
+constexpr int kTermBits = 5;
+constexpr float kTermStep = 1 << kTermBits;
+constexpr int kTermTop = 7;  // exponent of a row's largest magnitude in its first part
 
 // What a wave has to do, the same for all of its lanes.
 struct WaveJob {
@@ -159,23 +163,23 @@ struct WaveJob {
   const uint8_t* ks;
   const uint8_t* vs;
   const int32_t* pages;    // of the sequence
-  int64_t begin, end;      // positions, begin a multiple of kKvStep; `end` past the last one wanted
-  int64_t stride;          // from one pass of this wave to the next
-  int64_t full_lo, full_hi;// positions that every row of the wave sees
-  int64_t length;          // positions of the sequence
+  int begin, end;          // positions, begin a multiple of kKvStep; `end` past the last one wanted
+  int stride;              // from one pass of this wave to the next
+  int full_lo, full_hi;    // positions that every row of the wave sees
+  int length;              // positions of the sequence
 };
 
 template <int DT, int D, int NQ, int PT>
 struct AttentionWave {
   using H = HeadParts<D>;
-  static constexpr int kSteps = D / 32;  // matrix instructions over a head's columns
-  static constexpr int kQT = kQueryTerms<DT>;
+  using B = HeadBlocks<D, kQueryTerms<DT>>;
 
-  u32x4a q[NQ][kQT][kSteps];
+  i32x8 q[NQ][B::kSets][B::kTurns];
+  uint32_t qs[NQ][B::kSets][B::kTurns];
   f32x4 o[NQ][D / 16];
   f32x4 l[NQ];
   float m[NQ];             // reference exponent, minus infinity until a position is seen
-  int64_t lo[NQ], hi[NQ];  // positions that this lane's row sees
+  int lo[NQ], hi[NQ];      // positions that this lane's row sees
   int32_t ids;             // lane i: page of the wave's tile i of the next 64, -1: none
 
   __device__ __forceinline__ void clear() {
@@ -189,60 +193,113 @@ struct AttentionWave {
     }
   }
 
-  // Columns g * D / 4 + 8 s + i of the row are element i of step s.
+  // A lane's columns of its row in parts of 8 bits. A NaN or an infinity makes
+  // the row NaN.
   __device__ __forceinline__ void load_queries(int r, const typename OpElem<DT>::T* row) {
     const int g = (threadIdx.x & 63) >> 4;
+    float x[B::kSets][B::kHalves][16];
+    uint32_t top = 0;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      Packed<DT, 8> x;
-      x.load(row + g * (D / 4) + 8 * s);
+    for (int set = 0; set < B::kSets; ++set) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t a[kQT], b[kQT];
-        split_exact<kQT>(x.get(2 * j) * kQueryUnit, a);
-        split_exact<kQT>(x.get(2 * j + 1) * kQueryUnit, b);
+      for (int half = 0; half < B::kHalves; ++half) {
+        const int col = B::column(set, half, g);
 #pragma unroll
-        for (int t = 0; t < kQT; ++t) q[r][t][s][j] = a[t] | b[t] << 16;
+        for (int k = 0; k < 2; ++k) {
+          Packed<DT, 8> p;
+          p.load(row + (col < D ? col : 0) + 8 * k);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float v = col < D ? p.get(i) : 0.0f;
+            x[set][half][8 * k + i] = v;
+            top = MaxBits::of(top, __float_as_uint(v) & 0x7fffffffu);
+          }
+        }
+      }
+    }
+    const auto s = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+    top = MaxBits::of(s[0], s[1]);
+    const auto u = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+    top = MaxBits::of(u[0], u[1]);  // of the row
+    const bool finite = top < 0x7f800000u;
+    // Exponent of the first part; the last one's has to stay above 2^-127.
+    int e = (int)(top >> 23) - 127 - kTermTop;
+    e = max(e, kQueryExponent + kTermBits * kQueryTerms<DT> - 126);
+    // Two factors, as one might leave fp32's range.
+    const float up = __builtin_ldexpf(1.0f, -e / 2), more = __builtin_ldexpf(1.0f, -e - -e / 2);
+#pragma unroll
+    for (int set = 0; set < B::kSets; ++set) {
+#pragma unroll
+      for (int term = 0; term < kQueryTerms<DT>; ++term) {
+        const int turn = B::kPaired ? term / 2 : term;
+#pragma unroll
+        for (int half = 0; half < B::kHalves; ++half) {
+          float* v = x[set][half];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            if (term == 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[4 * w + i] *= up * more;
+            }
+            int c = 0;
+            c = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * w], v[4 * w + 1], c, false);
+            c = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * w + 2], v[4 * w + 3], c, true);
+            v[4 * w] = (v[4 * w] - __builtin_amdgcn_cvt_f32_fp8(c, 0)) * kTermStep;
+            v[4 * w + 1] = (v[4 * w + 1] - __builtin_amdgcn_cvt_f32_fp8(c, 1)) * kTermStep;
+            v[4 * w + 2] = (v[4 * w + 2] - __builtin_amdgcn_cvt_f32_fp8(c, 2)) * kTermStep;
+            v[4 * w + 3] = (v[4 * w + 3] - __builtin_amdgcn_cvt_f32_fp8(c, 3)) * kTermStep;
+            q[r][set][turn][4 * (B::kPaired ? term & 1 : half) + w] = finite ? c : 0x7f7f7f7f;  // NaN
+          }
+        }
+        const uint32_t scale = (uint32_t)(e - kTermBits * term - kQueryExponent + 127);
+        qs[r][set][turn] = B::kPaired && term % 2 == 1 && g < 2 ? qs[r][set][turn] : scale;
+      }
+      if (B::kPaired && kQueryTerms<DT> % 2 == 1) {
+#pragma unroll
+        for (int w = 4; w < 8; ++w) q[r][set][B::kTurns - 1][w] = 0;
       }
     }
   }
 
   // Pages of the 64 tiles of the next 32 passes, from position `at` on.
-  __device__ __forceinline__ void load_pages(const AttentionArgs& a, const WaveJob& job, int64_t at) {
+  __device__ __forceinline__ void load_pages(const AttentionArgs& a, const WaveJob& job, int at) {
     const int lane = threadIdx.x & 63;
-    const int64_t tile = (at + (lane >> 1) * job.stride) / kKvTile + (lane & 1);
+    const int64_t tile = ((int64_t)at + (int64_t)(lane >> 1) * job.stride) / kKvTile + (lane & 1);
     ids = kv_page_of_tile(job.pages, tile, job.length, a.cache.page_shift, a.max_pages, a.cache.pages);
   }
 
   // `n`: the pass's number modulo 32. A tile without a page is read from page 0 and not seen.
-  __device__ __forceinline__ void load(const AttentionArgs& a, const WaveJob& job, int64_t at, int n, KvRaw<D>& raw) {
+  __device__ __forceinline__ void load(const AttentionArgs& a, const WaveJob& job, int at, int n, KvRaw<D>& raw) {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
+      // Addresses: a place that is the same for all lanes, and a lane's own 32 bits.
       const int32_t id = __builtin_amdgcn_readlane(ids, 2 * n + t);
       const int64_t page = id < 0 ? 0 : id;
-      const int off = (int)((at + kKvTile * t) & ((1 << a.cache.page_shift) - 1));
-      const int64_t data = page * a.cache.page + (int64_t)off * (D / 2);
+      const int off = (at + kKvTile * t) & ((1 << a.cache.page_shift) - 1);
+      const int64_t data = page * a.cache.page + off * (D / 2);
       const int64_t scale = page * a.cache.scale_page + off;
-      load_bytes<D / 8>(raw.k[t], job.k + data + c * (D / 2) + g * (D / 8));
-      const int block = g * (D / 4) / 32;
+      const uint8_t *pk = job.k + data, *pv = job.v + data, *pks = job.ks + scale, *pvs = job.vs + scale;
 #pragma unroll
-      for (int i = 0; i < KvRaw<D>::kKeyScales; ++i)
-        raw.ks[t][i] = job.ks[scale + ((block + i < D / 32 ? block + i : block) << a.cache.page_shift) + c];
+      for (int set = 0; set < KvRaw<D>::kSets; ++set) {
+        const uint32_t block = B::block(set, g);
+        raw.k[t][set] = *reinterpret_cast<const u32x4*>(pk + (uint32_t)(c * (D / 2) + block * 16));
+        raw.ks[t][set] = pks[(block << a.cache.page_shift) + (uint32_t)c];
+      }
 #pragma unroll
       for (int p = 0; p < H::kParts; ++p) {
-        const int n_p = H::n(p);
+        constexpr int kRow = D / 2;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint8_t* from = job.v + data + (4 * g + i) * (D / 2) + H::base(p) / 2 + c * n_p;
+          const uint8_t* from = pv + (uint32_t)(4 * g * kRow + H::base(p) / 2 + c * H::n(p)) + i * kRow;
           uint32_t* to = raw.v[4 * t + i] + H::reg0(p);
-          if (n_p == 1) load_bytes<1>(to, from);
-          if (n_p == 2) load_bytes<2>(to, from);
-          if (n_p == 4) load_bytes<4>(to, from);
-          if (n_p == 8) load_bytes<8>(to, from);
+          if (H::n(p) == 1) load_bytes<1>(to, from);
+          if (H::n(p) == 2) load_bytes<2>(to, from);
+          if (H::n(p) == 4) load_bytes<4>(to, from);
+          if (H::n(p) == 8) load_bytes<8>(to, from);
         }
-        const int b = H::base(p) / 32 + c * n_p / 16;
-        raw.vs[t][p] = *reinterpret_cast<const uint32_t*>(job.vs + scale + (b << a.cache.page_shift) + 4 * g);
+        const uint32_t b = H::base(p) / 32 + c * H::n(p) / 16;
+        raw.vs[t][p] = *reinterpret_cast<const uint32_t*>(pvs + (b << a.cache.page_shift) + (uint32_t)(4 * g));
       }
     }
   }
@@ -250,7 +307,7 @@ struct AttentionWave {
   // One pass over the 32 positions from `at` on. SLOW: a position's NaN values
   // reach the rows that see it and no others, which 0 * NaN would not do.
   template <bool SLOW>
-  __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int64_t at, int n,
+  __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, int n,
                                        const KvRaw<D>& raw) {
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -258,23 +315,13 @@ struct AttentionWave {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
-      for (int r = 0; r < NQ; ++r) s[r][t] = zero;
+      for (int r = 0; r < NQ; ++r) {
+        s[r][t] = zero;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        float unit;
-        if constexpr (KvRaw<D>::kKeyScales == 1) {
-          unit = unit_of<0>(raw.ks[t][0]);
-        } else {
-          const bool next = (g * (D / 4) + 8 * k) / 32 != g * (D / 4) / 32;
-          unit = next ? unit_of<0>(raw.ks[t][1]) : unit_of<0>(raw.ks[t][0]);
-        }
-        const uint32_t w = raw.k[t][k];
-        const u32x4a key = {two_columns<0>(w, unit), two_columns<1>(w, unit), two_columns<2>(w, unit),
-                            two_columns<3>(w, unit)};
+        for (int set = 0; set < B::kSets; ++set) {
 #pragma unroll
-        for (int r = 0; r < NQ; ++r) {
-#pragma unroll
-          for (int e = kQT - 1; e >= 0; --e) s[r][t] = mfma(key, q[r][e][k], s[r][t]);
+          for (int turn = B::kTurns - 1; turn >= 0; --turn)
+            s[r][t] = mfma_scaled(raw.k[t][set], raw.ks[t][set], q[r][set][turn], qs[r][set][turn], s[r][t]);
         }
       }
     }
@@ -288,7 +335,7 @@ struct AttentionWave {
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int64_t j = at + kKvTile * t + 4 * g + i;
+            const int j = at + kKvTile * t + 4 * g + i;
             const bool on = j >= lo[r] && j <= hi[r] && (t ? there1 : there0);
             s[r][t][i] = on ? s[r][t][i] : -__builtin_inff();
             seen[r] |= (uint32_t)on << (4 * t + i);
@@ -296,7 +343,7 @@ struct AttentionWave {
         }
       }
     }
-    u32x4a p[NQ][PT];
+    u32x4 p[NQ][PT];
 #pragma unroll
     for (int r = 0; r < NQ; ++r) {
       float top = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
@@ -329,7 +376,7 @@ struct AttentionWave {
         }
         // The sums are those of the rounded weights, so a row that one
         // position rules gets that position's values.
-        const u32x4a ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+        const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
         l[r] = mfma(ones, p[r][e], l[r]);
       }
     }
@@ -360,7 +407,7 @@ struct AttentionWave {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint32_t pick = half ? 0x07060302u : 0x05040100u;
-          u32x4a v;
+          u32x4 v;
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], pick);
           const int d = H::base(part) / 16 + 2 * b + half;
@@ -369,7 +416,7 @@ struct AttentionWave {
 #pragma unroll
             for (int e = PT - 1; e >= 0; --e) o[r][d] = mfma(v, p[r][e], o[r][d]);
             if constexpr (SLOW) {
-              u32x4a x, y;
+              u32x4 x, y;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 x[j] = __builtin_amdgcn_perm(nan[2 * j + 1], nan[2 * j], pick);
@@ -389,24 +436,28 @@ struct AttentionWave {
   __device__ __forceinline__ void run(const AttentionArgs& a, const WaveJob& job) {
     clear();
     if (job.begin >= job.end) return;
+    // Two buffers in turn, each loaded while the other one is worked on.
     KvRaw<D> raw[2];
     load_pages(a, job, job.begin);
     load(a, job, job.begin, 0, raw[0]);
     int n = 0;
-    for (int64_t at = job.begin; at < job.end; at += job.stride) {
-      const int64_t next = at + job.stride;
-      const int32_t here = ids;
+    const auto turn = [&](int at, const KvRaw<D>& here, KvRaw<D>& next) {
+      const int32_t now = ids;
       const int n_next = (n + 1) & 31;
-      if (next < job.end) {
-        if (n_next == 0) load_pages(a, job, next);
-        load(a, job, next, n_next, raw[1]);
+      if (at + job.stride < job.end) {
+        if (n_next == 0) load_pages(a, job, at + job.stride);
+        load(a, job, at + job.stride, n_next, next);
       }
       const int32_t ahead = ids;
-      ids = here;
-      pass<SLOW>(a, job, at, n, raw[0]);
+      ids = now;
+      pass<SLOW>(a, job, at, n, here);
       ids = ahead;
-      raw[0] = raw[1];
       n = n_next;
+    };
+    for (int at = job.begin; at < job.end; at += 2 * job.stride) {
+      turn(at, raw[0], raw[1]);
+      if (at + job.stride >= job.end) break;
+      turn(at + job.stride, raw[1], raw[0]);
     }
   }
 
@@ -425,32 +476,40 @@ struct AttentionWave {
   }
 };
 
-// A workgroup's rows: sequence, first row, rows, tokens and positions.
+// A workgroup's rows: sequence, its first token in q and that one's position,
+// its rows, the first of them here, and its positions.
 struct RowTile {
-  int64_t seq, row, rows, token, length, first;  // first: position of the sequence's first token in q
+  int seq, token, first, rows, row, length;
 };
 
-__device__ __forceinline__ bool row_tile(const AttentionArgs& a, int64_t tile, RowTile& t) {
-  int64_t count;
+__device__ __forceinline__ bool row_tile(const AttentionArgs& a, int tile, RowTile& t) {
+  int count;
   if (a.starts) {
-    t.seq = kv_seq_of_tile(a.starts, a.seqs, a.tokens, a.group, a.tile_rows, tile);
-    t.token = kv_clamp(a.starts[t.seq], 0, a.tokens);
-    count = kv_clamp(a.starts[t.seq + 1], 0, a.tokens) - t.token;
-    tile -= kv_first_tile(t.token, t.seq, a.group, a.tile_rows);
+    t.seq = (int)kv_seq_of_tile(a.starts, a.seqs, a.tokens, a.group, a.tile_rows, tile);
+    t.token = (int)kv_clamp(a.starts[t.seq], 0, a.tokens);
+    count = (int)kv_clamp(a.starts[t.seq + 1], 0, a.tokens) - t.token;
+    tile -= (int)kv_first_tile(t.token, t.seq, a.group, a.tile_rows);
   } else {
-    const int64_t per = (a.each * a.group + a.tile_rows - 1) / a.tile_rows;
-    t.seq = tile / per;
+    t.seq = tile / a.seq_tiles;
     t.token = t.seq * a.each;
     count = a.each;
-    tile -= t.seq * per;
+    tile -= t.seq * a.seq_tiles;
   }
   t.row = tile * a.tile_rows;
   t.rows = count * a.group;
   if (tile < 0 || t.row >= t.rows) return false;
-  const int64_t n = a.lengths[t.seq];
-  t.length = kv_clamp(n, 0, a.cap);
-  t.first = (n < 0 ? 0 : n) - count;
+  const int n = max(a.lengths[t.seq], 0);
+  t.length = min(n, a.cap);
+  t.first = n - count;
   return true;
+}
+
+// Positions [lo, hi] that the token at position p sees.
+__device__ __forceinline__ void span(const AttentionArgs& a, int p, int length, int* lo, int* hi) {
+  int64_t l, h;
+  kv_span(p, length, a.causal, a.window, &l, &h);
+  *lo = (int)l;
+  *hi = (int)h;
 }
 
 template <int DT, int D, int NQ, int WT, int PT>
@@ -458,24 +517,26 @@ __global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const Atte
   using W = AttentionWave<DT, D, NQ, PT>;
   using T = typename OpElem<DT>::T;
   using H = HeadParts<D>;
-  const int key_head = (int)(blockIdx.x % a.cache.heads);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  // Told to be the same for all lanes of a wave, the loop's places are kept and counted in scalar registers.
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int row_block = blockIdx.x / a.cache.heads, key_head = blockIdx.x - row_block * a.cache.heads;
   RowTile tile;
-  if (!row_tile(a, blockIdx.x / a.cache.heads, tile)) return;
+  if (!row_tile(a, row_block, tile)) return;
 
   // Positions that any row of the workgroup sees, and this split's part of them.
-  const int64_t last = min(tile.row + a.tile_rows, tile.rows) - 1;
-  int64_t lo, hi, x;
-  kv_span(tile.first + tile.row / a.group, tile.length, a.causal, a.window, &lo, &x);
-  kv_span(tile.first + last / a.group, tile.length, a.causal, a.window, &x, &hi);
-  const int64_t begin = lo / kKvStep * kKvStep + blockIdx.y * a.chunk;
-  const int64_t end = min(begin + a.chunk, hi + 1);
+  const int last = min(tile.row + a.tile_rows, tile.rows) - 1;
+  int lo, hi, x;
+  span(a, tile.first + tile.row / a.group, tile.length, &lo, &x);
+  span(a, tile.first + last / a.group, tile.length, &x, &hi);
+  const int64_t split = (int64_t)(lo / kKvStep * kKvStep) + (int64_t)blockIdx.y * a.chunk;
+  const int begin = (int)min(split, (int64_t)hi + 1), end = (int)min(split + a.chunk, (int64_t)hi + 1);
 
-  const int64_t row0 = tile.row + (WT == 1 ? wave * NQ * 16 : 0);  // of this wave
+  const int row0 = tile.row + (WT == 1 ? wave * NQ * 16 : 0);  // of this wave
   W w;
   WaveJob job;
   {
-    const int64_t head = (int64_t)key_head * a.cache.head, scale_head = (int64_t)key_head * a.cache.scale_head;
+    const int64_t head = key_head * a.cache.head, scale_head = key_head * a.cache.scale_head;
     job.k = a.cache.data[0] + head;
     job.v = a.cache.data[1] + head;
     job.ks = a.cache.scales[0] + scale_head;
@@ -483,24 +544,23 @@ __global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const Atte
     job.pages = a.pages + tile.seq * a.page_stride;
     job.length = tile.length;
     job.stride = WT * kKvStep;
-    const int64_t row1 = min(row0 + NQ * 16, tile.rows) - 1;
-    int64_t wave_lo, wave_hi;
-    kv_span(tile.first + row0 / a.group, tile.length, a.causal, a.window, &wave_lo, &job.full_hi);
-    kv_span(tile.first + row1 / a.group, tile.length, a.causal, a.window, &job.full_lo, &wave_hi);
+    const int row1 = min(row0 + NQ * 16, tile.rows) - 1;
+    int wave_lo, wave_hi;
+    span(a, tile.first + row0 / a.group, tile.length, &wave_lo, &job.full_hi);
+    span(a, tile.first + row1 / a.group, tile.length, &job.full_lo, &wave_hi);
     job.begin = begin + (WT == 1 ? 0 : wave * kKvStep);
     job.end = min(end, wave_hi + 1);
     if (WT == 1) job.begin = max(job.begin, wave_lo / kKvStep * kKvStep);
-    if (row0 >= tile.rows) job.end = job.begin;
+    if (begin >= end || row0 >= tile.rows) job.end = job.begin;
   }
   // A row beyond the last one repeats it, and is not stored.
-  int64_t token[NQ];
-  int head[NQ];
+  int token[NQ], head[NQ];
 #pragma unroll
   for (int r = 0; r < NQ; ++r) {
-    const int64_t row = min(row0 + 16 * r + c, tile.rows - 1);
+    const int row = min(row0 + 16 * r + c, tile.rows - 1);
     token[r] = row / a.group;
-    head[r] = key_head * a.group + (int)(row - token[r] * a.group);
-    kv_span(tile.first + token[r], tile.length, a.causal, a.window, &w.lo[r], &w.hi[r]);
+    head[r] = key_head * a.group + row - token[r] * a.group;
+    span(a, tile.first + token[r], tile.length, &w.lo[r], &w.hi[r]);
   }
   const auto q_row = [&](int r) {
     const int64_t at = a.starts ? (tile.token + token[r]) * a.q.s1 : tile.seq * a.q.s0 + token[r] * a.q.s1;
@@ -512,12 +572,12 @@ __global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const Atte
   if (w.has_nan()) w.template run<true>(a, job);
 
   // A row's place among all rows, for lse and for the parts of a split.
-  const auto index_of = [&](int64_t t, int h) { return (tile.token + t) * a.heads + h; };
-  const auto out_row = [&](int64_t t, int h) {
+  const auto index_of = [&](int t, int h) { return (int64_t)(tile.token + t) * a.heads + h; };
+  const auto out_row = [&](int t, int h) {
     const int64_t at = a.starts ? (tile.token + t) * a.out.s1 : tile.seq * a.out.s0 + t * a.out.s1;
     return static_cast<T*>(a.out.p) + at + h * a.out.s2;
   };
-  const int64_t all = a.tokens * a.heads;
+  const int64_t all = (int64_t)a.tokens * a.heads;
   constexpr float kLn2 = 0.69314718055994531f;
   const auto lse_of = [&](float ref, float sum) {
     return ref == -__builtin_inff() && sum == 0.0f ? ref : (ref + __builtin_amdgcn_logf(sum)) * kLn2;
@@ -596,7 +656,7 @@ __global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const Atte
       }
     }
     __syncthreads();
-    const int rows = (int)min((int64_t)16, tile.rows - tile.row);
+    const int rows = min(16, tile.rows - tile.row);
     for (int k = threadIdx.x; k < rows * (D / 8); k += kAttentionThreads) {
       const int row = k / (D / 8), col = (k - row * (D / 8)) * 8;
       float best = refs[0][row], sum = 0.0f;
@@ -614,8 +674,8 @@ __global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const Atte
 #pragma unroll
         for (int i = 1; i < WT; ++i) f[e] += outs[i][row][col + e];
       }
-      const int64_t t = (tile.row + row) / a.group;
-      const int h = key_head * a.group + (int)(tile.row + row - t * a.group);
+      const int t = (tile.row + row) / a.group;
+      const int h = key_head * a.group + tile.row + row - t * a.group;
       const int64_t at = index_of(t, h);
       if (a.splits > 1) {
         if (col == 0) {
@@ -642,7 +702,7 @@ __global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const Atte
 
 template <int DT, int D, int NQ, int WT, int PT>
 hipError_t launch_shape(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.tiles * a.cache.heads), (unsigned)a.splits);
+  const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, (unsigned)a.splits);
   hipLaunchKernelGGL((attention_kernel<DT, D, NQ, WT, PT>), grid, dim3(kAttentionThreads), 0, s, a);
   return hipGetLastError();
 }

@@ -132,14 +132,14 @@ bool plan_of(const ringsim_paged_attention_t& a, AttentionPlan* plan, int64_t* c
   if (a.max_length < 0 || a.window < 0) return false;
   if (a.seqs == 0 || a.tokens == 0) return true;
   if (!a.starts && a.tokens % a.seqs) return false;
-  *cap = a.max_pages * c.page_size;
+  *cap = std::min<int64_t>(a.max_pages * c.page_size, INT32_MAX - kKvStep);
   if (a.max_length > 0) *cap = std::min(*cap, a.max_length);
   *plan = plan_attention(a.tokens, a.seqs, a.starts != nullptr, (int)a.heads, (int)c.heads, (int)c.dim, a.dtype, *cap,
                          a.window);
   return plan->tiles * c.heads <= kMaxBlocks;
 }
 
-float scale_log2(float scale) { return (float)((double)scale * 1.4426950408889634 / kQueryUnit); }
+float scale_log2(float scale) { return (float)std::ldexp((double)scale * 1.4426950408889634, kQueryExponent); }
 
 size_t attention_workspace(const ringsim_paged_attention_t& a, const AttentionPlan& plan) {
   return plan.splits == 1 ? 0 : sizeof(float) * (size_t)plan.splits * (size_t)(a.tokens * a.heads) * (size_t)(a.cache.dim + 2);
@@ -286,12 +286,13 @@ ringsim_result_t ringsim_paged_attention(const ringsim_paged_attention_t* a, rin
     k.part_ml = k.part_out + (size_t)plan.splits * (size_t)(a->tokens * a->heads) * (size_t)c.dim;
   }
   k.page_stride = a->page_stride;
-  k.cap = cap;
+  k.cap = (int)cap;
   k.max_pages = a->max_pages;
-  k.tokens = a->tokens;
-  k.seqs = a->seqs;
+  k.tokens = (int)a->tokens;
+  k.seqs = (int)a->seqs;
   k.window = a->window;
-  k.each = a->tokens / a->seqs;
+  k.each = (int)(a->tokens / a->seqs);
+  k.seq_tiles = (int)(plan.tiles / a->seqs);  // read without starts
   k.chunk = plan.chunk;
   k.splits = plan.splits;
   k.group = (int)(a->heads / c.heads);

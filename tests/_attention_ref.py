@@ -11,6 +11,9 @@ LEVELS = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4
 #: Relative error of a weight held in two or three bf16 parts (one part: half a step, 2^-8).
 WEIGHT_REL = {torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -16, torch.float32: 2.0 ** -24}
 ONE_PART = 2.0 ** -8
+#: Queries are split into 8-bit parts of 4 bits and 5 each further one, from the row's largest (in [128, 256)) down. What the last part leaves of a column, relative to that largest: half its smallest step, 2^-10 * 32^-(parts-1)
+#: of 128 (bf16 2 parts, fp16 3), or for fp32's 24 bits in 5 parts 8 * 32^-4 of 256.
+QUERY_REL = {torch.bfloat16: 2.0 ** -22, torch.float16: 2.0 ** -27, torch.float32: 2.0 ** -24}
 
 
 def half_step(want, dtype):
@@ -121,12 +124,14 @@ def attention(q, cache, pages, lengths, causal=True, window=0, scale=None, max_l
                 w = torch.exp(s - lse[i, h].unsqueeze(-1))
                 o = w @ v
                 out[i, h] = o
-                # A score sums dim products of up to 3 parts, each addition off by up to 2 u of the magnitudes; the
+                # A score sums dim products of up to 5 parts, each addition off by up to 2 u of the magnitudes; the
                 # exponent's argument adds 3 roundings of itself and of the reference (the reference is at most the
                 # row's largest score, and at least that less 8 log 2); exp2 2 ulp.
                 size = (x[i, h].abs() @ k.abs().t()) * scale
                 top = s.abs().amax(-1, keepdim=True)
-                rel = 2 * (3 * dim + 8) * U * size + 4 * U * (s.abs() + top + 8) + 4 * U
+                most = x[i, h].abs().amax(-1, keepdim=True)
+                kept = most * k.abs().sum(-1) * scale * QUERY_REL[dtype]
+                rel = kept + 2 * (5 * dim + 8) * U * size + 4 * U * (s.abs() + top + 8) + 4 * U
                 # Sums over n positions: each pass of 32 is one chain, then splits and waves; 2 u an addition. The
                 # weights' own rounding is in both sums.
                 n = int(pick.sum())
