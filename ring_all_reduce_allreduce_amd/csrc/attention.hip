@@ -4,7 +4,17 @@
 
 #include "attention_device.h"
 
+#ifndef RINGSIM_TARGET
+#define RINGSIM_TARGET 2048
+#define RINGSIM_LEAST 256
+#endif
+
 namespace ringsim {
+
+// A NaN counts as no maximum; it comes into the result through its sums.
+struct MaxF32 {
+  static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
+};
 
 namespace {
 
@@ -28,7 +38,7 @@ AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int head
   int64_t span = cap;
   if (window > 0) span = std::min(span, window + ceil_div(p.tile_rows, group) + 1);
   span += kKvStep;  // the first pass may begin before the first position
-  const int64_t groups = p.tiles * kv_heads, target = p.wide ? 512 : 2048, least = p.wide ? 1024 : 256;
+  const int64_t groups = p.tiles * kv_heads, target = p.wide ? 512 : RINGSIM_TARGET, least = p.wide ? 1024 : RINGSIM_LEAST;
   const int64_t splits = std::max<int64_t>(1, std::min(ceil_div(target, std::max<int64_t>(groups, 1)), span / least));
   p.chunk = ceil_div(ceil_div(span, splits), kKvStep) * kKvStep;
   p.splits = (int)ceil_div(span, p.chunk);
@@ -49,38 +59,71 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, i
   return launch_attention_join(a, dtype, s);
 }
 
-// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s with M the largest m_s,
-// splits in order. LANES lanes a row, 4 columns each.
-template <int DT, int LANES>
-__global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs a) {
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s with M the largest m_s. A
+// wave takes a row: its lanes first hold the splits' m and l (64 of them at a
+// time), then 4 columns each, so that no load waits for another one but the
+// outputs for the weights. Heads of 128 columns and fewer leave half of the lanes for
+// a second split: even splits go to the first half, odd ones to the second.
+constexpr int kJoinRows = 4;     // of a workgroup
+constexpr int kJoinAhead = 8;    // outputs whose loads are under way
+
+template <int DT, int HALVES>
+__global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const AttentionArgs a) {
   const int64_t all = (int64_t)a.tokens * a.heads;
-  const int64_t at = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+  const int64_t at = (int64_t)blockIdx.x * kJoinRows + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (at >= all) return;
-  const int64_t token = at / a.heads;
-  const int head = (int)(at - token * a.heads), col = (int)(threadIdx.x % LANES) * 4;
-  int64_t seq = 0;
+  const int token = (int)(at / a.heads), head = (int)(at - (int64_t)token * a.heads), lane = threadIdx.x & 63;
+  const int half = HALVES == 2 ? lane >> 5 : 0, col = (HALVES == 2 ? lane & 31 : lane) * 4;
+  int seq = 0;
   if (a.starts) {
     if (token < a.starts[0] || token >= a.starts[a.seqs]) return;  // of no sequence
   } else {
     seq = token / a.each;
   }
-  float best = -__builtin_inff();
-  for (int s = 0; s < a.splits; ++s) best = fmaxf(best, a.part_ml[2 * (s * all + at)]);
+  const float inf = __builtin_inff();
+  const auto ml_of = [&](int s) {  // of no split: nothing
+    const f32x2 v = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * (min(s, a.splits - 1) * all + at));
+    return s < a.splits ? v : f32x2{-inf, 0.0f};
+  };
+  float best = -inf;
+  for (int s = lane; s < a.splits; s += 64) best = fmaxf(best, ml_of(s).x);
+  best = lanes_reduce<64, MaxF32>(best);
   float sum = 0.0f, f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float ref = a.part_ml[2 * (s * all + at)], l = a.part_ml[2 * (s * all + at) + 1];
-    if (l == 0.0f) continue;  // no position there, nothing written
-    const float by = ref == best ? 1.0f : __builtin_amdgcn_exp2f(ref - best);
-    sum += l * by;
-    if (col < a.cache.dim) {
-      const f32x4 o = *reinterpret_cast<const f32x4*>(a.part_out + (s * all + at) * a.cache.dim + col);
+  const bool there = col < a.cache.dim;
+  const float* part = a.part_out + at * a.cache.dim + (there ? col : 0);
+  for (int base = 0; base < a.splits; base += 64) {
+    const f32x2 ml = ml_of(base + lane);
+    // A split without a position has written no output.
+    float w = ml.y == 0.0f ? 0.0f : ml.x == best ? 1.0f : __builtin_amdgcn_exp2f(ml.x - best);
+    sum += w * ml.y;
+    const uint64_t used = __ballot(ml.y != 0.0f);
+    const int n = min(64, a.splits - base);
+    for (int s0 = 0; s0 < n; s0 += kJoinAhead * HALVES) {
+      f32x4 o[kJoinAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[i] += o[i] * by;
+      for (int k = 0; k < kJoinAhead; ++k) {
+        const int s = s0 + HALVES * k + half;
+        const bool on = s < n && (used >> (s & 63) & 1);
+        o[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (on) o[k] = *reinterpret_cast<const f32x4*>(part + (int64_t)(base + s) * all * a.cache.dim);
+      }
+#pragma unroll
+      for (int k = 0; k < kJoinAhead; ++k) {
+        const int s = s0 + HALVES * k + half;
+        const float by = __shfl(w, s & 63);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] += s < n ? o[k][i] * by : 0.0f;
+      }
     }
   }
+  sum = lanes_reduce<64, AddF32>(sum);
+  if constexpr (HALVES == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] += __shfl_xor(f[i], 32);
+  }
   constexpr float kLn2 = 0.69314718055994531f;
-  if (a.lse && col == 0) a.lse[at] = sum == 0.0f ? -__builtin_inff() : (best + __builtin_amdgcn_logf(sum)) * kLn2;
-  if (col >= a.cache.dim) return;
+  if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? -inf : (best + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (!there || half) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] *= inv;
@@ -93,10 +136,11 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
 template <int DT>
 static hipError_t launch_join(const AttentionArgs& a, hipStream_t s) {
   const int64_t rows = (int64_t)a.tokens * a.heads;
+  const dim3 grid((unsigned)ceil_div(rows, kJoinRows)), block(64 * kJoinRows);
   if (a.cache.dim <= 128)
-    hipLaunchKernelGGL((attention_join_kernel<DT, 32>), dim3((unsigned)ceil_div(rows, 8)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attention_join_kernel<DT, 2>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((attention_join_kernel<DT, 64>), dim3((unsigned)ceil_div(rows, 4)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attention_join_kernel<DT, 1>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 

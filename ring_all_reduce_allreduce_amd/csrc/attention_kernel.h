@@ -31,6 +31,10 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kAttentionWaves = 4;
 constexpr int kAttentionThreads = 64 * kAttentionWaves;
+#ifndef RINGSIM_AHEAD
+#define RINGSIM_AHEAD 1
+#define RINGSIM_WAVES 1
+#endif
 
 // How far (as a power of two) weights may grow before a row's reference
 // exponent follows its maximum. Sums and products in fp32 lose nothing by it,
@@ -83,21 +87,40 @@ struct KvRaw {
   uint32_t ks[2][kSets];
   uint32_t v[8][H::kRegs];
   uint32_t vs[2][H::kParts];
+  bool there[2];           // whether the tiles have a page
 };
 
+// A place in device memory that is the same for all lanes, in scalar
+// registers: loads add a lane's own 32 bits to it by themselves. Without the
+// barrier the compiler would add the lane's part first, once for all passes, and
+// then two vector registers for every load.
+typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
+__device__ __forceinline__ GlobalBytes uniform(const uint8_t* p) {
+  asm("" : "+s"(p));
+  return (GlobalBytes)p;
+}
+
 template <int N>
-__device__ __forceinline__ void load_bytes(uint32_t* w, const uint8_t* p) {
+__device__ __forceinline__ void load_bytes(uint32_t* w, GlobalBytes p, uint32_t at) {
+  typedef const __attribute__((address_space(1))) uint16_t* P16;
+  typedef const __attribute__((address_space(1))) uint32_t* P32;
+  typedef const __attribute__((address_space(1))) u32x2* P64;
+  typedef const __attribute__((address_space(1))) u32x4* P128;
   if constexpr (N == 1) {
-    w[0] = *p;
+    w[0] = p[at];
   } else if constexpr (N == 2) {
-    w[0] = *reinterpret_cast<const uint16_t*>(p);
+    w[0] = *(P16)(p + at);
   } else if constexpr (N == 4) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else {
-    static_assert(N == 8, "bytes");
-    const u32x2 x = *reinterpret_cast<const u32x2*>(p);
+    w[0] = *(P32)(p + at);
+  } else if constexpr (N == 8) {
+    const u32x2 x = *(P64)(p + at);
     w[0] = x[0];
     w[1] = x[1];
+  } else {
+    static_assert(N == 16, "bytes");
+    const u32x4 x = *(P128)(p + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = x[i];
   }
 }
 
@@ -138,9 +161,8 @@ __device__ __forceinline__ float groups_max(float v) {
 
 // Codes of 4 bits with exponents `ks` times 8-bit ones with exponents `qs`.
 __device__ __forceinline__ f32x4 mfma_scaled(const u32x4& k, uint32_t ks, const i32x8& q, uint32_t qs, f32x4 acc) {
-  i32x8 x;  // 4-bit operands are the first half
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (int)k[i & 3];
+  // 4-bit operands are the first half.
+  const i32x8 x = __builtin_bit_cast(i32x8, __builtin_shufflevector(k, k, 0, 1, 2, 3, -1, -1, -1, -1));
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, q, acc, 4, 0, 0, (int)ks, 0, (int)qs);
 }
 
@@ -169,7 +191,13 @@ struct WaveJob {
   int length;              // positions of the sequence
 };
 
-template <int DT, int D, int NQ, int PT>
+// DT, D: type of queries and columns of a head. NQ: tiles of 16 rows. PT: bf16
+// parts of a weight. AHEAD: passes whose loads are under way. ONE: all rows of a
+// wave belong to one token, so a position is seen by all of them or none, and
+// what the cache holds where none sees is taken as ones; else a position's NaN
+// has to reach the rows that see it and no others, for which a wave that finds
+// a NaN in its sums starts again the slow way.
+template <int DT, int D, int NQ, int PT, int AHEAD, bool ONE>
 struct AttentionWave {
   using H = HeadParts<D>;
   using B = HeadBlocks<D, kQueryTerms<DT>>;
@@ -275,31 +303,35 @@ struct AttentionWave {
     for (int t = 0; t < 2; ++t) {
       // Addresses: a place that is the same for all lanes, and a lane's own 32 bits.
       const int32_t id = __builtin_amdgcn_readlane(ids, 2 * n + t);
+      raw.there[t] = id >= 0;
       const int64_t page = id < 0 ? 0 : id;
       const int off = (at + kKvTile * t) & ((1 << a.cache.page_shift) - 1);
       const int64_t data = page * a.cache.page + off * (D / 2);
       const int64_t scale = page * a.cache.scale_page + off;
-      const uint8_t *pk = job.k + data, *pv = job.v + data, *pks = job.ks + scale, *pvs = job.vs + scale;
+      const GlobalBytes pk = uniform(job.k + data), pv = uniform(job.v + data);
+      const GlobalBytes pks = uniform(job.ks + scale), pvs = uniform(job.vs + scale);
 #pragma unroll
       for (int set = 0; set < KvRaw<D>::kSets; ++set) {
         const uint32_t block = B::block(set, g);
-        raw.k[t][set] = *reinterpret_cast<const u32x4*>(pk + (uint32_t)(c * (D / 2) + block * 16));
-        raw.ks[t][set] = pks[(block << a.cache.page_shift) + (uint32_t)c];
+        uint32_t k[4];
+        load_bytes<16>(k, pk, (uint32_t)c * (D / 2) + block * 16);
+        raw.k[t][set] = u32x4{k[0], k[1], k[2], k[3]};
+        load_bytes<1>(&raw.ks[t][set], pks, (block << a.cache.page_shift) + (uint32_t)c);
       }
 #pragma unroll
       for (int p = 0; p < H::kParts; ++p) {
         constexpr int kRow = D / 2;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint8_t* from = pv + (uint32_t)(4 * g * kRow + H::base(p) / 2 + c * H::n(p)) + i * kRow;
+          const uint32_t from = (uint32_t)(4 * g * kRow + H::base(p) / 2 + c * H::n(p));
           uint32_t* to = raw.v[4 * t + i] + H::reg0(p);
-          if (H::n(p) == 1) load_bytes<1>(to, from);
-          if (H::n(p) == 2) load_bytes<2>(to, from);
-          if (H::n(p) == 4) load_bytes<4>(to, from);
-          if (H::n(p) == 8) load_bytes<8>(to, from);
+          if (H::n(p) == 1) load_bytes<1>(to, pv + i * kRow, from);
+          if (H::n(p) == 2) load_bytes<2>(to, pv + i * kRow, from);
+          if (H::n(p) == 4) load_bytes<4>(to, pv + i * kRow, from);
+          if (H::n(p) == 8) load_bytes<8>(to, pv + i * kRow, from);
         }
         const uint32_t b = H::base(p) / 32 + c * H::n(p) / 16;
-        raw.vs[t][p] = *reinterpret_cast<const uint32_t*>(pvs + (b << a.cache.page_shift) + (uint32_t)(4 * g));
+        load_bytes<4>(&raw.vs[t][p], pvs, (b << a.cache.page_shift) + (uint32_t)(4 * g));
       }
     }
   }
@@ -307,8 +339,7 @@ struct AttentionWave {
   // One pass over the 32 positions from `at` on. SLOW: a position's NaN values
   // reach the rows that see it and no others, which 0 * NaN would not do.
   template <bool SLOW>
-  __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, int n,
-                                       const KvRaw<D>& raw) {
+  __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, const KvRaw<D>& raw) {
     const int lane = threadIdx.x & 63, g = lane >> 4;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
     f32x4 s[NQ][2];
@@ -325,9 +356,10 @@ struct AttentionWave {
         }
       }
     }
-    const bool there0 = __builtin_amdgcn_readlane(ids, 2 * n) >= 0, there1 = __builtin_amdgcn_readlane(ids, 2 * n + 1) >= 0;
-    uint32_t seen[NQ];  // SLOW: a bit a position
-    if (SLOW || !there0 || !there1 || at < job.full_lo || at + kKvStep - 1 > job.full_hi) {
+    uint32_t seen[NQ];  // a bit a position
+    bool masked = SLOW;
+    if (SLOW || !raw.there[0] || !raw.there[1] || at < job.full_lo || at + kKvStep - 1 > job.full_hi) {
+      masked = true;
 #pragma unroll
       for (int r = 0; r < NQ; ++r) {
         seen[r] = 0;
@@ -336,7 +368,7 @@ struct AttentionWave {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = at + kKvTile * t + 4 * g + i;
-            const bool on = j >= lo[r] && j <= hi[r] && (t ? there1 : there0);
+            const bool on = j >= lo[r] && j <= hi[r] && raw.there[t];
             s[r][t][i] = on ? s[r][t][i] : -__builtin_inff();
             seen[r] |= (uint32_t)on << (4 * t + i);
           }
@@ -390,6 +422,13 @@ struct AttentionWave {
         unit[4 * t + 2] = unit_of<2>(raw.vs[t][part]);
         unit[4 * t + 3] = unit_of<3>(raw.vs[t][part]);
       }
+      if constexpr (ONE) {
+        // The lane's positions are those of its weights, and all rows see the same.
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) unit[i] = seen[0] >> i & 1 ? unit[i] : 1.0f;
+        }
+      }
 #pragma unroll
       for (int b = 0; b < H::n(part); ++b) {  // two columns a byte
         uint32_t w[8];
@@ -436,28 +475,28 @@ struct AttentionWave {
   __device__ __forceinline__ void run(const AttentionArgs& a, const WaveJob& job) {
     clear();
     if (job.begin >= job.end) return;
-    // Two buffers in turn, each loaded while the other one is worked on.
-    KvRaw<D> raw[2];
-    load_pages(a, job, job.begin);
-    load(a, job, job.begin, 0, raw[0]);
-    int n = 0;
-    const auto turn = [&](int at, const KvRaw<D>& here, KvRaw<D>& next) {
-      const int32_t now = ids;
-      const int n_next = (n + 1) & 31;
-      if (at + job.stride < job.end) {
-        if (n_next == 0) load_pages(a, job, at + job.stride);
-        load(a, job, at + job.stride, n_next, next);
-      }
-      const int32_t ahead = ids;
-      ids = now;
-      pass<SLOW>(a, job, at, n, here);
-      ids = ahead;
-      n = n_next;
+    // Buffers in turn, loaded AHEAD passes before they are worked on. No load
+    // stands under a condition: behind one, the compiler would wait for all that
+    // are under way and not for the oldest buffer's alone. So after the last
+    // pass's loads they are repeated, out of the cache.
+    KvRaw<D> raw[AHEAD + 1];
+    const int passes = (job.end - 1 - job.begin) / job.stride + 1;
+    int next = 0;  // pass to be loaded
+    const auto load_next = [&](KvRaw<D>& to) {
+      if ((next & 31) == 0) load_pages(a, job, job.begin + next * job.stride);
+      load(a, job, job.begin + next * job.stride, next & 31, to);
+      if (next < passes - 1) ++next;
     };
-    for (int at = job.begin; at < job.end; at += 2 * job.stride) {
-      turn(at, raw[0], raw[1]);
-      if (at + job.stride >= job.end) break;
-      turn(at + job.stride, raw[1], raw[0]);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) load_next(raw[i]);
+    for (int at = job.begin;;) {
+#pragma unroll
+      for (int i = 0; i <= AHEAD; ++i) {
+        load_next(raw[(i + AHEAD) % (AHEAD + 1)]);
+        pass<SLOW>(a, job, at, raw[i]);
+        at += job.stride;
+        if (at >= job.end) return;
+      }
     }
   }
 
@@ -512,9 +551,9 @@ __device__ __forceinline__ void span(const AttentionArgs& a, int p, int length, 
   *hi = (int)h;
 }
 
-template <int DT, int D, int NQ, int WT, int PT>
-__global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const AttentionArgs a) {
-  using W = AttentionWave<DT, D, NQ, PT>;
+template <int DT, int D, int NQ, int WT, int PT, int AHEAD, bool ONE>
+__global__ __launch_bounds__(kAttentionThreads, ONE ? RINGSIM_WAVES : 1) void attention_kernel(const AttentionArgs a) {
+  using W = AttentionWave<DT, D, NQ, PT, AHEAD, ONE>;
   using T = typename OpElem<DT>::T;
   using H = HeadParts<D>;
   // Told to be the same for all lanes of a wave, the loop's places are kept and counted in scalar registers.
@@ -569,7 +608,9 @@ __global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const Atte
 #pragma unroll
   for (int r = 0; r < NQ; ++r) w.load_queries(r, q_row(r));
   w.template run<false>(a, job);
-  if (w.has_nan()) w.template run<true>(a, job);
+  if constexpr (!ONE) {
+    if (w.has_nan()) w.template run<true>(a, job);
+  }
 
   // A row's place among all rows, for lse and for the parts of a split.
   const auto index_of = [&](int t, int h) { return (int64_t)(tile.token + t) * a.heads + h; };
@@ -700,26 +741,34 @@ __global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const Atte
   }
 }
 
-template <int DT, int D, int NQ, int WT, int PT>
+template <int DT, int D, int NQ, int WT, int PT, int AHEAD, bool ONE>
 hipError_t launch_shape(const AttentionArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, (unsigned)a.splits);
-  hipLaunchKernelGGL((attention_kernel<DT, D, NQ, WT, PT>), grid, dim3(kAttentionThreads), 0, s, a);
+  hipLaunchKernelGGL((attention_kernel<DT, D, NQ, WT, PT, AHEAD, ONE>), grid, dim3(kAttentionThreads), 0, s, a);
   return hipGetLastError();
 }
 
 // bf16 outputs: with few rows memory bounds, and weights in two parts cost
 // nothing; with many the matrix units do.
+template <int DT, int D>
+hipError_t launch_type(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t s) {
+  constexpr int kParts = DT == RINGSIM_FLOAT32 ? 3 : 2;
+  if (plan.wide) {
+    if constexpr (DT == RINGSIM_BFLOAT16)
+      return launch_shape<DT, D, 2, 1, 1, 1, false>(a, s);
+    else
+      return launch_shape<DT, D, 1, 1, kParts, 1, false>(a, s);
+  }
+  return !a.starts && a.each == 1 ? launch_shape<DT, D, 1, 4, kParts, RINGSIM_AHEAD, true>(a, s)
+                                  : launch_shape<DT, D, 1, 4, kParts, 1, false>(a, s);
+}
+
 template <int D>
 hipError_t launch_head(const AttentionArgs& a, const AttentionPlan& plan, int dtype, hipStream_t s) {
-  constexpr int kWide = 2;
   switch (dtype) {
-    case RINGSIM_FLOAT32:
-      return plan.wide ? launch_shape<RINGSIM_FLOAT32, D, 1, 1, 3>(a, s) : launch_shape<RINGSIM_FLOAT32, D, 1, 4, 3>(a, s);
-    case RINGSIM_BFLOAT16:
-      return plan.wide ? launch_shape<RINGSIM_BFLOAT16, D, kWide, 1, 1>(a, s)
-                       : launch_shape<RINGSIM_BFLOAT16, D, 1, 4, 2>(a, s);
-    case RINGSIM_FLOAT16:
-      return plan.wide ? launch_shape<RINGSIM_FLOAT16, D, 1, 1, 2>(a, s) : launch_shape<RINGSIM_FLOAT16, D, 1, 4, 2>(a, s);
+    case RINGSIM_FLOAT32: return launch_type<RINGSIM_FLOAT32, D>(a, plan, s);
+    case RINGSIM_BFLOAT16: return launch_type<RINGSIM_BFLOAT16, D>(a, plan, s);
+    case RINGSIM_FLOAT16: return launch_type<RINGSIM_FLOAT16, D>(a, plan, s);
     default: return hipErrorInvalidValue;
   }
 }
