@@ -2,12 +2,7 @@
 // kernel that joins the parts of contexts that were split.
 #include <algorithm>
 
-#include "attention_device.h"
-
-#ifndef RINGSIM_TARGET
-#define RINGSIM_TARGET 2048
-#define RINGSIM_LEAST 256
-#endif
+#include "attention_rows.h"
 
 namespace ringsim {
 
@@ -25,6 +20,14 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int wide_rows(int dtype) { return dtype == RINGSIM_BFLOAT16 ? 128 : 64; }
 constexpr int kNarrowRows = 16;
 
+// Workgroups that share a call's work: as many as the card runs at once.
+#ifndef RINGSIM_GROUPS
+#define RINGSIM_GROUPS 512
+#define RINGSIM_WIDE_GROUPS 256
+#endif
+constexpr int kNarrowGroups = RINGSIM_GROUPS;
+constexpr int kWideGroups = RINGSIM_WIDE_GROUPS;
+
 }  // namespace
 
 AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
@@ -34,14 +37,15 @@ AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int head
   p.wide = rows > 64;
   p.tile_rows = p.wide ? wide_rows(dtype) : kNarrowRows;
   p.tiles = ragged ? tokens * group / p.tile_rows + seqs : seqs * ceil_div(tokens / seqs * group, p.tile_rows);
-  // Positions that a workgroup may see: all, or a window for each of its tokens.
+  // Positions that a tile may see: all, or a window for each of its tokens. The
+  // first unit may begin before the first of them.
   int64_t span = cap;
   if (window > 0) span = std::min(span, window + ceil_div(p.tile_rows, group) + 1);
-  span += kKvStep;  // the first pass may begin before the first position
-  const int64_t groups = p.tiles * kv_heads, target = p.wide ? 512 : RINGSIM_TARGET, least = p.wide ? 1024 : RINGSIM_LEAST;
-  const int64_t splits = std::max<int64_t>(1, std::min(ceil_div(target, std::max<int64_t>(groups, 1)), span / least));
-  p.chunk = ceil_div(ceil_div(span, splits), kKvStep) * kKvStep;
-  p.splits = (int)ceil_div(span, p.chunk);
+  const int64_t units = kv_units(kKvStep - 1, kKvStep - 2 + std::max<int64_t>(span, 1));
+  const int64_t items = p.tiles * kv_heads;
+  p.groups = 0;
+  if (p.tiles <= kSharedTiles && units > 1)
+    p.groups = (int)std::min<int64_t>(p.wide ? kWideGroups : kNarrowGroups, ceil_div(items * units, 8) * 8);
   return p;
 }
 
@@ -55,57 +59,59 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, i
     case 256: e = launch_attention_256(a, plan, dtype, s); break;
     default: break;
   }
-  if (e != hipSuccess || a.splits == 1) return e;
+  if (e != hipSuccess || a.groups == 0) return e;
   return launch_attention_join(a, dtype, s);
 }
 
-// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s with M the largest m_s. A
-// wave takes a row: its lanes first hold the splits' m and l (64 of them at a
-// time), then 4 columns each, so that no load waits for another one but the
-// outputs for the weights. Heads of 128 columns and fewer leave half of the lanes for
-// a second split: even splits go to the first half, odd ones to the second.
+// out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the parts s of a
+// row's tile, M the largest m_s; tiles that one workgroup took whole are
+// done. A wave takes a row: its lanes first hold the parts' m and l (64 of them
+// at a time), then 4 columns each, so that no load waits for another one but
+// the outputs for the weights. Heads of 128 columns and fewer leave half of
+// the lanes for a second part: even ones go to the first half, odd ones to the
+// second.
 constexpr int kJoinRows = 4;     // of a workgroup
 constexpr int kJoinAhead = 8;    // outputs whose loads are under way
 
 template <int DT, int HALVES>
 __global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const AttentionArgs a) {
-  const int64_t all = (int64_t)a.tokens * a.heads;
-  const int64_t at = (int64_t)blockIdx.x * kJoinRows + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (at >= all) return;
-  const int token = (int)(at / a.heads), head = (int)(at - (int64_t)token * a.heads), lane = threadIdx.x & 63;
+  const int item = blockIdx.x, tile_index = item / a.cache.heads, key_head = item - tile_index * a.cache.heads;
+  RowTile tile;
+  if (!row_tile(a, a.starts, tile_index, tile)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int in_tile = blockIdx.y * kJoinRows + wave, row = tile.row + in_tile;
+  if (row >= tile.rows) return;
+  const int first = a.part_of[2 * item], parts = a.part_of[2 * item + 1] - first + 1;
+  if (parts == 1) return;
+  const int token = row / a.group, head = key_head * a.group + row - token * a.group;
   const int half = HALVES == 2 ? lane >> 5 : 0, col = (HALVES == 2 ? lane & 31 : lane) * 4;
-  int seq = 0;
-  if (a.starts) {
-    if (token < a.starts[0] || token >= a.starts[a.seqs]) return;  // of no sequence
-  } else {
-    seq = token / a.each;
-  }
   const float inf = __builtin_inff();
-  const auto ml_of = [&](int s) {  // of no split: nothing
-    const f32x2 v = *reinterpret_cast<const f32x2*>(a.part_ml + 2 * (min(s, a.splits - 1) * all + at));
-    return s < a.splits ? v : f32x2{-inf, 0.0f};
+  const auto row_of = [&](int s) { return (int64_t)part_slot(first + s, s == 0) * a.tile_rows + in_tile; };
+  const auto ml_of = [&](int s) {  // of no part: nothing
+    const f32x4 v = *reinterpret_cast<const f32x4*>(a.part_ml + 4 * row_of(min(s, parts - 1)));
+    return s < parts ? v : f32x4{-inf, 0.0f, 0.0f, 0.0f};
   };
   float best = -inf;
-  for (int s = lane; s < a.splits; s += 64) best = fmaxf(best, ml_of(s).x);
+  for (int s = lane; s < parts; s += 64) best = fmaxf(best, ml_of(s)[0]);
   best = lanes_reduce<64, MaxF32>(best);
-  float sum = 0.0f, f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float sum = 0.0f, exact = 0.0f, f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const bool there = col < a.cache.dim;
-  const float* part = a.part_out + at * a.cache.dim + (there ? col : 0);
-  for (int base = 0; base < a.splits; base += 64) {
-    const f32x2 ml = ml_of(base + lane);
-    // A split without a position has written no output.
-    float w = ml.y == 0.0f ? 0.0f : ml.x == best ? 1.0f : __builtin_amdgcn_exp2f(ml.x - best);
-    sum += w * ml.y;
-    const uint64_t used = __ballot(ml.y != 0.0f);
-    const int n = min(64, a.splits - base);
+  const float* out = a.part_out + (there ? col : 0);
+  for (int base = 0; base < parts; base += 64) {
+    const f32x4 ml = ml_of(base + lane);
+    // A part without a position has written no output.
+    const float w = ml[1] == 0.0f ? 0.0f : ml[0] == best ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - best);
+    sum += w * ml[1];
+    exact += w * ml[2];
+    const uint64_t used = __ballot(ml[1] != 0.0f);
+    const int n = min(64, parts - base);
     for (int s0 = 0; s0 < n; s0 += kJoinAhead * HALVES) {
       f32x4 o[kJoinAhead];
 #pragma unroll
       for (int k = 0; k < kJoinAhead; ++k) {
         const int s = s0 + HALVES * k + half;
-        const bool on = s < n && (used >> (s & 63) & 1);
         o[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (on) o[k] = *reinterpret_cast<const f32x4*>(part + (int64_t)(base + s) * all * a.cache.dim);
+        if (s < n && (used >> (s & 63) & 1)) o[k] = *reinterpret_cast<const f32x4*>(out + row_of(base + s) * a.cache.dim);
       }
 #pragma unroll
       for (int k = 0; k < kJoinAhead; ++k) {
@@ -117,26 +123,25 @@ __global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const At
     }
   }
   sum = lanes_reduce<64, AddF32>(sum);
+  exact = lanes_reduce<64, AddF32>(exact);
   if constexpr (HALVES == 2) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] += __shfl_xor(f[i], 32);
   }
-  constexpr float kLn2 = 0.69314718055994531f;
-  if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? -inf : (best + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (a.lse && lane == 0) a.lse[lse_index(a, tile, token, head)] = lse_of(best, exact);
   if (!there || half) return;
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] *= inv;
-  const int64_t to = a.starts ? token * a.out.s1 : seq * a.out.s0 + (token - seq * a.each) * a.out.s1;
+  for (int i = 0; i < 4; ++i) f[i] *= by;
   Packed<DT, 4> y;
   y.set(f);
-  y.store(static_cast<typename OpElem<DT>::T*>(a.out.p) + to + head * a.out.s2 + col);
+  y.store(out_row<DT>(a, tile, token, head) + col);
 }
 
 template <int DT>
 static hipError_t launch_join(const AttentionArgs& a, hipStream_t s) {
-  const int64_t rows = (int64_t)a.tokens * a.heads;
-  const dim3 grid((unsigned)ceil_div(rows, kJoinRows)), block(64 * kJoinRows);
+  const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, (unsigned)ceil_div(a.tile_rows, kJoinRows));
+  const dim3 block(64 * kJoinRows);
   if (a.cache.dim <= 128)
     hipLaunchKernelGGL((attention_join_kernel<DT, 2>), grid, block, 0, s, a);
   else

@@ -102,8 +102,11 @@ struct AttentionArgs {
   const int32_t* pages;
   const int32_t* lengths;
   const int32_t* starts;  // null: `each` tokens a sequence
-  float* part_out;        // [splits, tokens * heads, dim], with splits > 1
-  float* part_ml;         // [splits, tokens * heads, 2]: reference exponent and sum
+  // Shared work (groups > 0): workgroups take equal shares of all units, and
+  // leave what they hold of a tile that others hold parts of in a slot of theirs.
+  float* part_out;        // [2 * groups, tile_rows, dim]
+  float* part_ml;         // [2 * groups, tile_rows, 4]: reference exponent, sum, sum of unrounded weights
+  int32_t* part_of;       // [tiles * key heads, 2]: first and last workgroup of a tile
   int64_t page_stride;
   int64_t max_pages;
   int64_t window;
@@ -111,8 +114,7 @@ struct AttentionArgs {
   int tokens, seqs;
   int each;               // tokens of a sequence without starts, and
   int seq_tiles;          // tiles of its rows
-  int64_t chunk;          // positions of a split, a multiple of kKvStep
-  int splits;
+  int groups;             // workgroups that share the work; 0: a workgroup a tile and key head
   int group;              // query heads of a key head
   int heads;              // of queries
   int tiles;              // of rows, over all sequences
@@ -126,16 +128,21 @@ struct AttentionArgs {
 // values that fp32 would not hold.
 constexpr int kQueryExponent = 8;
 
-// How a call is cut: rows of a workgroup, workgroups, and parts of the context.
+// How a call is cut: rows of a tile, tiles, and workgroups that share them.
 struct AttentionPlan {
   int wide;               // 1: many rows, a wave its own rows; 0: waves share rows
   int tile_rows;
   int64_t tiles;
-  int64_t chunk;
-  int splits;
+  int groups;
 };
 AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
                              int64_t cap, int64_t window);
+
+// Most tiles whose work is shared: their units are counted in LDS.
+constexpr int kSharedTiles = 512;
+// Where a workgroup leaves its part of a tile: the one that it begins but does
+// not end last in its share, one that it only goes on with first.
+__host__ __device__ __forceinline__ int part_slot(int group, bool begins) { return 2 * group + (begins ? 1 : 0); }
 
 hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, int dtype, hipStream_t s);
 // One unit for each head size, so that they compile side by side.

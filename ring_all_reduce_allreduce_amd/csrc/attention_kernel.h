@@ -21,7 +21,9 @@
 // positions. Nothing passes through LDS.
 #pragma once
 
-#include "attention_device.h"
+#include <type_traits>
+
+#include "attention_rows.h"
 
 namespace ringsim {
 
@@ -31,10 +33,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kAttentionWaves = 4;
 constexpr int kAttentionThreads = 64 * kAttentionWaves;
-#ifndef RINGSIM_AHEAD
-#define RINGSIM_AHEAD 1
-#define RINGSIM_WAVES 1
-#endif
 
 // How far (as a power of two) weights may grow before a row's reference
 // exponent follows its maximum. Sums and products in fp32 lose nothing by it,
@@ -206,6 +204,7 @@ struct AttentionWave {
   uint32_t qs[NQ][B::kSets][B::kTurns];
   f32x4 o[NQ][D / 16];
   f32x4 l[NQ];
+  float exact[NQ];         // PT 1, with lse: the lane's sum of weights before their rounding
   float m[NQ];             // reference exponent, minus infinity until a position is seen
   int lo[NQ], hi[NQ];      // positions that this lane's row sees
   int32_t ids;             // lane i: page of the wave's tile i of the next 64, -1: none
@@ -215,6 +214,7 @@ struct AttentionWave {
 #pragma unroll
     for (int r = 0; r < NQ; ++r) {
       m[r] = -__builtin_inff();
+      exact[r] = 0.0f;
       l[r] = zero;
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) o[r][d] = zero;
@@ -386,6 +386,7 @@ struct AttentionWave {
         // exp2(-inf) = 0 on a row's first positions; a row without any keeps its zeros.
         const float by = next == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);
         m[r] = next;
+        exact[r] *= by;
         l[r] *= by;
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) o[r][d] *= by;
@@ -395,6 +396,7 @@ struct AttentionWave {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i / 4][i % 4], a.scale_log2, -ref));
+      if (PT == 1 && a.lse) exact[r] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
 #pragma unroll
       for (int e = 0; e < PT; ++e) {
 #pragma unroll
@@ -500,6 +502,14 @@ struct AttentionWave {
     }
   }
 
+  // A row's sum of weights as lse takes it: rounded to one bf16 they would be
+  // off by more than fp32's last bits.
+  __device__ __forceinline__ float exact_sum(int r) const {
+    if constexpr (PT > 1) return l[r][0];
+    float v = exact[r] + __shfl_xor(exact[r], 16);
+    return v + __shfl_xor(v, 32);
+  }
+
   // Whether a NaN of the cache (or of a query) has come into any row.
   __device__ __forceinline__ bool has_nan() const {
     bool bad = false;
@@ -515,64 +525,64 @@ struct AttentionWave {
   }
 };
 
-// A workgroup's rows: sequence, its first token in q and that one's position,
-// its rows, the first of them here, and its positions.
-struct RowTile {
-  int seq, token, first, rows, row, length;
+// What one kernel is made for. NQ: tiles of 16 rows of a wave; WT: waves that
+// share rows (1: each wave has its own); PT, AHEAD, ONE as above.
+template <int DT_, int D_, int NQ_, int WT_, int PT_, int AHEAD_, bool ONE_>
+struct AttentionShape {
+  static constexpr int DT = DT_, D = D_, NQ = NQ_, WT = WT_, PT = PT_, AHEAD = AHEAD_;
+  static constexpr bool ONE = ONE_;
+  using Wave = AttentionWave<DT, D, NQ, PT, AHEAD, ONE>;
 };
 
-__device__ __forceinline__ bool row_tile(const AttentionArgs& a, int tile, RowTile& t) {
-  int count;
-  if (a.starts) {
-    t.seq = (int)kv_seq_of_tile(a.starts, a.seqs, a.tokens, a.group, a.tile_rows, tile);
-    t.token = (int)kv_clamp(a.starts[t.seq], 0, a.tokens);
-    count = (int)kv_clamp(a.starts[t.seq + 1], 0, a.tokens) - t.token;
-    tile -= (int)kv_first_tile(t.token, t.seq, a.group, a.tile_rows);
+// Where waves that share rows join their parts.
+template <class S>
+struct JoinBuffers {
+  static constexpr int kRow = S::D + 4;  // rows start 4 banks apart
+  float refs[S::WT][16], sums[S::WT][16];
+  float outs[S::WT][16][kRow];
+};
+struct NoBuffers {};
+
+// A row's result, or with a slot its part.
+template <class S>
+__device__ __forceinline__ void store_sums(const AttentionArgs& a, const RowTile& tile, int slot, int in_tile, int token,
+                                           int head, float ref, float sum, float exact) {
+  if (slot >= 0)
+    *reinterpret_cast<f32x4*>(a.part_ml + 4 * ((int64_t)slot * a.tile_rows + in_tile)) = f32x4{ref, sum, exact, 0.0f};
+  else if (a.lse)
+    a.lse[lse_index(a, tile, token, head)] = lse_of(ref, exact);
+}
+template <class S>
+__device__ __forceinline__ void store_columns(const AttentionArgs& a, const RowTile& tile, int slot, int in_tile,
+                                              int token, int head, int col, float sum, float (&f)[8]) {
+  if (slot >= 0) {
+    if (sum == 0.0f) return;  // no position, nothing to join
+    Packed<RINGSIM_FLOAT32, 8> y;
+    y.set(f);
+    y.store(a.part_out + ((int64_t)slot * a.tile_rows + in_tile) * S::D + col);
   } else {
-    t.seq = tile / a.seq_tiles;
-    t.token = t.seq * a.each;
-    count = a.each;
-    tile -= t.seq * a.seq_tiles;
+    const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= by;
+    Packed<S::DT, 8> y;
+    y.set(f);
+    y.store(out_row<S::DT>(a, tile, token, head) + col);
   }
-  t.row = tile * a.tile_rows;
-  t.rows = count * a.group;
-  if (tile < 0 || t.row >= t.rows) return false;
-  const int n = max(a.lengths[t.seq], 0);
-  t.length = min(n, a.cap);
-  t.first = n - count;
-  return true;
 }
 
-// Positions [lo, hi] that the token at position p sees.
-__device__ __forceinline__ void span(const AttentionArgs& a, int p, int length, int* lo, int* hi) {
-  int64_t l, h;
-  kv_span(p, length, a.causal, a.window, &l, &h);
-  *lo = (int)l;
-  *hi = (int)h;
-}
-
-template <int DT, int D, int NQ, int WT, int PT, int AHEAD, bool ONE>
-__global__ __launch_bounds__(kAttentionThreads, ONE ? RINGSIM_WAVES : 1) void attention_kernel(const AttentionArgs a) {
-  using W = AttentionWave<DT, D, NQ, PT, AHEAD, ONE>;
-  using T = typename OpElem<DT>::T;
+// Rows of a tile with one key head over the positions [begin, end), begin a
+// multiple of kKvStep; the result goes out, or into a slot if it is a part.
+template <class S, class BUFFERS>
+__device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& tile, int key_head, int begin, int end,
+                                       int slot, BUFFERS& lds) {
+  constexpr int D = S::D, NQ = S::NQ, WT = S::WT;
   using H = HeadParts<D>;
-  // Told to be the same for all lanes of a wave, the loop's places are kept and counted in scalar registers.
+  // What is the same for all lanes of a wave, and told to be, stays in scalar
+  // registers: the loop's places and counts among it.
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int row_block = blockIdx.x / a.cache.heads, key_head = blockIdx.x - row_block * a.cache.heads;
-  RowTile tile;
-  if (!row_tile(a, row_block, tile)) return;
-
-  // Positions that any row of the workgroup sees, and this split's part of them.
-  const int last = min(tile.row + a.tile_rows, tile.rows) - 1;
-  int lo, hi, x;
-  span(a, tile.first + tile.row / a.group, tile.length, &lo, &x);
-  span(a, tile.first + last / a.group, tile.length, &x, &hi);
-  const int64_t split = (int64_t)(lo / kKvStep * kKvStep) + (int64_t)blockIdx.y * a.chunk;
-  const int begin = (int)min(split, (int64_t)hi + 1), end = (int)min(split + a.chunk, (int64_t)hi + 1);
-
   const int row0 = tile.row + (WT == 1 ? wave * NQ * 16 : 0);  // of this wave
-  W w;
+  typename S::Wave w;
   WaveJob job;
   {
     const int64_t head = key_head * a.cache.head, scale_head = key_head * a.cache.scale_head;
@@ -590,7 +600,7 @@ __global__ __launch_bounds__(kAttentionThreads, ONE ? RINGSIM_WAVES : 1) void at
     job.begin = begin + (WT == 1 ? 0 : wave * kKvStep);
     job.end = min(end, wave_hi + 1);
     if (WT == 1) job.begin = max(job.begin, wave_lo / kKvStep * kKvStep);
-    if (begin >= end || row0 >= tile.rows) job.end = job.begin;
+    if (row0 >= tile.rows) job.end = job.begin;
   }
   // A row beyond the last one repeats it, and is not stored.
   int token[NQ], head[NQ];
@@ -601,86 +611,49 @@ __global__ __launch_bounds__(kAttentionThreads, ONE ? RINGSIM_WAVES : 1) void at
     head[r] = key_head * a.group + row - token[r] * a.group;
     span(a, tile.first + token[r], tile.length, &w.lo[r], &w.hi[r]);
   }
-  const auto q_row = [&](int r) {
-    const int64_t at = a.starts ? (tile.token + token[r]) * a.q.s1 : tile.seq * a.q.s0 + token[r] * a.q.s1;
-    return static_cast<const T*>(a.q.p) + at + head[r] * a.q.s2;
-  };
 #pragma unroll
-  for (int r = 0; r < NQ; ++r) w.load_queries(r, q_row(r));
+  for (int r = 0; r < NQ; ++r) w.load_queries(r, query_row<S::DT>(a, tile, token[r], head[r]));
   w.template run<false>(a, job);
-  if constexpr (!ONE) {
+  if constexpr (!S::ONE) {
     if (w.has_nan()) w.template run<true>(a, job);
   }
-
-  // A row's place among all rows, for lse and for the parts of a split.
-  const auto index_of = [&](int t, int h) { return (int64_t)(tile.token + t) * a.heads + h; };
-  const auto out_row = [&](int t, int h) {
-    const int64_t at = a.starts ? (tile.token + t) * a.out.s1 : tile.seq * a.out.s0 + t * a.out.s1;
-    return static_cast<T*>(a.out.p) + at + h * a.out.s2;
-  };
-  const int64_t all = (int64_t)a.tokens * a.heads;
-  constexpr float kLn2 = 0.69314718055994531f;
-  const auto lse_of = [&](float ref, float sum) {
-    return ref == -__builtin_inff() && sum == 0.0f ? ref : (ref + __builtin_amdgcn_logf(sum)) * kLn2;
-  };
 
   if constexpr (WT == 1) {
 #pragma unroll
     for (int r = 0; r < NQ; ++r) {
-      if (row0 + 16 * r + c >= tile.rows) continue;
+      const int in_tile = row0 - tile.row + 16 * r + c;
+      const float exact = w.exact_sum(r);
+      if (tile.row + in_tile >= tile.rows) continue;
       const float sum = w.l[r][0];
-      const int64_t at = index_of(token[r], head[r]);
       const float ref = w.m[r] == -__builtin_inff() && sum != 0.0f ? 0.0f : w.m[r];
-      if (a.splits > 1) {
-        if (g == 0) {
-          float* ml = a.part_ml + 2 * (blockIdx.y * all + at);
-          ml[0] = ref;
-          ml[1] = sum;
-        }
-        if (sum == 0.0f) continue;
-      } else if (a.lse && g == 0) {
-        a.lse[at] = lse_of(ref, sum);
-      }
-      const float by = a.splits > 1 ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (g == 0) store_sums<S>(a, tile, slot, in_tile, token[r], head[r], ref, sum, exact);
 #pragma unroll
       for (int part = 0; part < H::kParts; ++part) {
         const int n = H::n(part), d0 = H::base(part) / 16;
-        const int col = H::base(part) + 8 * n * g;
 #pragma unroll
         for (int k = 0; k < n; ++k) {  // 8 columns each
           float f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int at_col = 8 * k + e, i = at_col / (2 * n), j = at_col % (2 * n);
-            f[e] = w.o[r][d0 + j][i] * by;
+            f[e] = w.o[r][d0 + j][i];
           }
-          if (a.splits > 1) {
-            Packed<RINGSIM_FLOAT32, 8> y;
-            y.set(f);
-            y.store(a.part_out + (blockIdx.y * all + at) * D + col + 8 * k);
-          } else {
-            Packed<DT, 8> y;
-            y.set(f);
-            y.store(out_row(token[r], head[r]) + col + 8 * k);
-          }
+          store_columns<S>(a, tile, slot, in_tile, token[r], head[r], H::base(part) + 8 * n * g + 8 * k, sum, f);
         }
       }
     }
   } else {
-    // The waves' parts of the positions, joined in LDS in a fixed order.
+    // The waves' parts of the positions, joined in a fixed order.
     static_assert(NQ == 1, "waves that share rows have one tile of them");
-    constexpr int kRow = D + 4;  // rows start 4 banks apart
-    __shared__ float refs[WT][16], sums[WT][16];
-    __shared__ float outs[WT][16][kRow];
     const float own = w.m[0] == -__builtin_inff() && w.l[0][0] != 0.0f ? 0.0f : w.m[0];  // NaN sums without a maximum
     if (g == 0) {
-      refs[wave][c] = own;
-      sums[wave][c] = w.l[0][0];
+      lds.refs[wave][c] = own;
+      lds.sums[wave][c] = w.l[0][0];
     }
     __syncthreads();
-    float top = refs[0][c];
+    float top = lds.refs[0][c];
 #pragma unroll
-    for (int i = 1; i < WT; ++i) top = fmaxf(top, refs[i][c]);
+    for (int i = 1; i < WT; ++i) top = fmaxf(top, lds.refs[i][c]);
     const float by = own == -__builtin_inff() ? 0.0f : own == top ? 1.0f : __builtin_amdgcn_exp2f(own - top);
 #pragma unroll
     for (int part = 0; part < H::kParts; ++part) {
@@ -693,58 +666,131 @@ __global__ __launch_bounds__(kAttentionThreads, ONE ? RINGSIM_WAVES : 1) void at
           const int at_col = 4 * k + e, i = at_col / (2 * n), j = at_col % (2 * n);
           f[e] = w.o[0][d0 + j][i] * by;
         }
-        *reinterpret_cast<f32x4*>(&outs[wave][c][H::base(part) + 8 * n * g + 4 * k]) = f;
+        *reinterpret_cast<f32x4*>(&lds.outs[wave][c][H::base(part) + 8 * n * g + 4 * k]) = f;
       }
     }
     __syncthreads();
     const int rows = min(16, tile.rows - tile.row);
     for (int k = threadIdx.x; k < rows * (D / 8); k += kAttentionThreads) {
       const int row = k / (D / 8), col = (k - row * (D / 8)) * 8;
-      float best = refs[0][row], sum = 0.0f;
+      float best = lds.refs[0][row], sum = 0.0f;
 #pragma unroll
-      for (int i = 1; i < WT; ++i) best = fmaxf(best, refs[i][row]);
+      for (int i = 1; i < WT; ++i) best = fmaxf(best, lds.refs[i][row]);
 #pragma unroll
       for (int i = 0; i < WT; ++i) {
-        const float ref = refs[i][row];
-        if (ref != -__builtin_inff()) sum += sums[i][row] * (ref == best ? 1.0f : __builtin_amdgcn_exp2f(ref - best));
+        const float ref = lds.refs[i][row];
+        if (ref != -__builtin_inff()) sum += lds.sums[i][row] * (ref == best ? 1.0f : __builtin_amdgcn_exp2f(ref - best));
       }
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        f[e] = outs[0][row][col + e];
+        f[e] = lds.outs[0][row][col + e];
 #pragma unroll
-        for (int i = 1; i < WT; ++i) f[e] += outs[i][row][col + e];
+        for (int i = 1; i < WT; ++i) f[e] += lds.outs[i][row][col + e];
       }
-      const int t = (tile.row + row) / a.group;
-      const int h = key_head * a.group + tile.row + row - t * a.group;
-      const int64_t at = index_of(t, h);
-      if (a.splits > 1) {
-        if (col == 0) {
-          float* ml = a.part_ml + 2 * (blockIdx.y * all + at);
-          ml[0] = best;
-          ml[1] = sum;
-        }
-        if (sum == 0.0f) continue;
-        Packed<RINGSIM_FLOAT32, 8> y;
-        y.set(f);
-        y.store(a.part_out + (blockIdx.y * all + at) * D + col);
-      } else {
-        if (a.lse && col == 0) a.lse[at] = lse_of(best, sum);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= inv;
-        Packed<DT, 8> y;
-        y.set(f);
-        y.store(out_row(t, h) + col);
-      }
+      const int t = (tile.row + row) / a.group, h = key_head * a.group + tile.row + row - t * a.group;
+      if (col == 0) store_sums<S>(a, tile, slot, row, t, h, best, sum, sum);
+      store_columns<S>(a, tile, slot, row, t, h, col, sum, f);
     }
+    __syncthreads();  // before the buffers are written again
   }
 }
 
-template <int DT, int D, int NQ, int WT, int PT, int AHEAD, bool ONE>
+// Units of all tiles, counted by each workgroup for itself.
+struct SharedUnits {
+  int32_t starts[kSharedTiles + 1];  // a copy, with starts
+  int32_t units[kSharedTiles];
+};
+
+// Either a workgroup a tile and key head, or an equal share of all units a
+// workgroup: it walks over the tiles that its share touches.
+template <class S>
+__global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const AttentionArgs a) {
+  __shared__ std::conditional_t<S::WT == 1, NoBuffers, JoinBuffers<S>> lds;
+  RowTile tile;
+  if (a.groups == 0) {
+    const int index = blockIdx.x / a.cache.heads;
+    if (!row_tile(a, a.starts, index, tile)) return;
+    tile = same_tile(tile);
+    int lo, hi;
+    tile_span(a, tile, &lo, &hi);
+    attend<S>(a, tile, blockIdx.x - index * a.cache.heads, lo / kKvStep * kKvStep, hi + 1, -1, lds);
+    return;
+  }
+  __shared__ SharedUnits all;
+  if (a.starts) {
+    for (int i = threadIdx.x; i <= a.seqs; i += kAttentionThreads) all.starts[i] = a.starts[i];
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < kSharedTiles; i += kAttentionThreads) {
+    int n = 0;
+    if (i < a.tiles && row_tile(a, all.starts, i, tile)) {
+      int lo, hi;
+      tile_span(a, tile, &lo, &hi);
+      n = (int)kv_units(lo, hi);
+    }
+    all.units[i] = n;
+  }
+  __syncthreads();
+  // Each wave: a lane adds kRun tiles, a scan over the lanes.
+  constexpr int kRun = kSharedTiles / 64;
+  const int lane = threadIdx.x & 63;
+  int own = 0;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) own += all.units[lane * kRun + i];
+  int upto = own;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int x = __shfl_up(upto, d);
+    upto += lane >= d ? x : 0;
+  }
+  const int64_t per_head = __builtin_amdgcn_readlane(upto, 63);
+  if (per_head == 0) return;
+  const int64_t units = per_head * a.cache.heads;
+  // No share is empty, so that the parts of a tile are those of consecutive
+  // workgroups. Neighbouring shares, which read the same keys where tiles of one
+  // sequence follow one another, go to workgroups of one XCD: those take turns.
+  const int groups = (int)min((int64_t)a.groups, units), per_xcd = (groups + 7) / 8;
+  const int group = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per_xcd || group >= groups) return;
+  int64_t at = kv_share_begin(units, group, groups);
+  const int64_t end = kv_share_begin(units, group + 1, groups);
+  int key_head = __builtin_amdgcn_readfirstlane((int)(at / per_head));
+  const int in_head = (int)(at - key_head * per_head);
+  const int run = __builtin_ctzll(__ballot(upto > in_head));  // the lane whose tiles hold the first unit
+  int index = run * kRun;
+  int before = __builtin_amdgcn_readlane(upto - own, run);  // units of the key head before tile `index`
+  while (at < end) {
+    while (at - key_head * per_head >= before + __builtin_amdgcn_readfirstlane(all.units[index])) {
+      before += __builtin_amdgcn_readfirstlane(all.units[index]);
+      if (++index == a.tiles) {
+        index = before = 0;
+        ++key_head;
+      }
+    }
+    const int n = __builtin_amdgcn_readfirstlane(all.units[index]);
+    const int64_t first = key_head * per_head + before;  // the tile's units are [first, first + n)
+    const int skip = (int)(at - first), take = (int)min((int64_t)n - skip, end - at);
+    row_tile(a, all.starts, index, tile);
+    tile = same_tile(tile);
+    int lo, hi;
+    tile_span(a, tile, &lo, &hi);
+    if (skip == 0 && threadIdx.x == 0) {
+      int32_t* of = a.part_of + 2 * ((int64_t)index * a.cache.heads + key_head);
+      of[0] = group;
+      of[1] = (int)kv_share_of(first + n - 1, units, groups);
+    }
+    const int begin = lo / kKvStep * kKvStep + skip * kKvUnit;
+    const int slot = take == n ? -1 : part_slot(group, skip == 0);
+    attend<S>(a, tile, key_head, begin, min(begin + take * kKvUnit, hi + 1), slot, lds);
+    at += take;
+  }
+}
+
+template <class S>
 hipError_t launch_shape(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, (unsigned)a.splits);
-  hipLaunchKernelGGL((attention_kernel<DT, D, NQ, WT, PT, AHEAD, ONE>), grid, dim3(kAttentionThreads), 0, s, a);
+  const unsigned grid = a.groups ? (unsigned)a.groups : (unsigned)a.tiles * (unsigned)a.cache.heads;
+  hipLaunchKernelGGL((attention_kernel<S>), dim3(grid), dim3(kAttentionThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -755,12 +801,12 @@ hipError_t launch_type(const AttentionArgs& a, const AttentionPlan& plan, hipStr
   constexpr int kParts = DT == RINGSIM_FLOAT32 ? 3 : 2;
   if (plan.wide) {
     if constexpr (DT == RINGSIM_BFLOAT16)
-      return launch_shape<DT, D, 2, 1, 1, 1, false>(a, s);
+      return launch_shape<AttentionShape<DT, D, 2, 1, 1, 1, false>>(a, s);
     else
-      return launch_shape<DT, D, 1, 1, kParts, 1, false>(a, s);
+      return launch_shape<AttentionShape<DT, D, 1, 1, kParts, 1, false>>(a, s);
   }
-  return !a.starts && a.each == 1 ? launch_shape<DT, D, 1, 4, kParts, RINGSIM_AHEAD, true>(a, s)
-                                  : launch_shape<DT, D, 1, 4, kParts, 1, false>(a, s);
+  return !a.starts && a.each == 1 ? launch_shape<AttentionShape<DT, D, 1, 4, kParts, 1, true>>(a, s)
+                                  : launch_shape<AttentionShape<DT, D, 1, 4, kParts, 1, false>>(a, s);
 }
 
 template <int D>

@@ -78,4 +78,16 @@ KV_FN void kv_span(int64_t p, int64_t end, int causal, int64_t window, int64_t* 
   *lo = window > 0 && p - window + 1 > 0 ? p - window + 1 : 0;
 }
 
+// Shares of the work. A tile of rows that sees positions lo to hi has units of
+// kKvUnit positions, at least one (rows that see nothing are written too). All
+// units of all tiles and key heads stand in one line, key heads outermost,
+// which is cut into equal shares, one for each workgroup.
+constexpr int kKvUnit = 128;
+KV_FN int64_t kv_units(int64_t lo, int64_t hi) {
+  return hi < lo ? 1 : (hi - lo / kKvStep * kKvStep) / kKvUnit + 1;
+}
+KV_FN int64_t kv_share_begin(int64_t units, int64_t group, int64_t groups) { return units * group / groups; }
+// The workgroup whose share holds unit p: the least one whose share ends behind it.
+KV_FN int64_t kv_share_of(int64_t p, int64_t units, int64_t groups) { return ((p + 1) * groups - 1) / units; }
+
 }  // namespace ringsim

@@ -141,8 +141,16 @@ bool plan_of(const ringsim_paged_attention_t& a, AttentionPlan* plan, int64_t* c
 
 float scale_log2(float scale) { return (float)std::ldexp((double)scale * 1.4426950408889634, kQueryExponent); }
 
-size_t attention_workspace(const ringsim_paged_attention_t& a, const AttentionPlan& plan) {
-  return plan.splits == 1 ? 0 : sizeof(float) * (size_t)plan.splits * (size_t)(a.tokens * a.heads) * (size_t)(a.cache.dim + 2);
+// What the parts of tiles take: outputs, {reference, sums}, and who holds them.
+struct PartSizes {
+  size_t out, ml, of;
+  size_t bytes() const { return out + ml + of; }
+};
+PartSizes part_sizes(const ringsim_paged_attention_t& a, const AttentionPlan& plan) {
+  const size_t rows = 2 * (size_t)plan.groups * (size_t)plan.tile_rows;
+  if (plan.groups == 0) return PartSizes{0, 0, 0};
+  return PartSizes{sizeof(float) * rows * (size_t)a.cache.dim, sizeof(float) * rows * 4,
+                   sizeof(int32_t) * 2 * (size_t)(plan.tiles * a.cache.heads)};
 }
 
 }  // namespace
@@ -242,9 +250,9 @@ ringsim_result_t ringsim_kv_read(const ringsim_kv_read_t* a, ringsim_stream_t st
 ringsim_result_t ringsim_paged_attention_workspace(const ringsim_paged_attention_t* a, size_t* bytes) {
   AttentionPlan plan;
   int64_t cap = 0;
-  plan.splits = 1;
+  plan.groups = 0;
   if (!a || !bytes || !plan_of(*a, &plan, &cap)) return RINGSIM_INVALID_ARGUMENT;
-  *bytes = attention_workspace(*a, plan);
+  *bytes = part_sizes(*a, plan).bytes();
   return RINGSIM_SUCCESS;
 }
 
@@ -269,8 +277,8 @@ ringsim_result_t ringsim_paged_attention(const ringsim_paged_attention_t* a, rin
   const int64_t table[1] = {a->seqs}, table_stride[1] = {a->page_stride};
   if (a->max_pages > 0 && (!a->pages || !aligned(a->pages, 4) || !strides_fit(table_stride, table, 1)))
     return RINGSIM_INVALID_ARGUMENT;
-  const size_t need = attention_workspace(*a, plan);
-  if (need > 0 && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need))
+  const PartSizes parts = part_sizes(*a, plan);
+  if (parts.bytes() > 0 && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < parts.bytes()))
     return RINGSIM_INVALID_ARGUMENT;
   AttentionArgs k;
   std::memset(&k, 0, sizeof(k));
@@ -281,9 +289,11 @@ ringsim_result_t ringsim_paged_attention(const ringsim_paged_attention_t* a, rin
   k.pages = a->pages;
   k.lengths = a->lengths;
   k.starts = a->starts;
-  if (need > 0) {
-    k.part_out = static_cast<float*>(a->workspace);
-    k.part_ml = k.part_out + (size_t)plan.splits * (size_t)(a->tokens * a->heads) * (size_t)c.dim;
+  if (parts.bytes() > 0) {
+    char* const at = static_cast<char*>(a->workspace);
+    k.part_out = reinterpret_cast<float*>(at);
+    k.part_ml = reinterpret_cast<float*>(at + parts.out);
+    k.part_of = reinterpret_cast<int32_t*>(at + parts.out + parts.ml);
   }
   k.page_stride = a->page_stride;
   k.cap = (int)cap;
@@ -293,8 +303,7 @@ ringsim_result_t ringsim_paged_attention(const ringsim_paged_attention_t* a, rin
   k.window = a->window;
   k.each = (int)(a->tokens / a->seqs);
   k.seq_tiles = (int)(plan.tiles / a->seqs);  // read without starts
-  k.chunk = plan.chunk;
-  k.splits = plan.splits;
+  k.groups = plan.groups;
   k.group = (int)(a->heads / c.heads);
   k.heads = (int)a->heads;
   k.tiles = (int)plan.tiles;

@@ -109,6 +109,31 @@ int main() {
             CHECK((j >= lo && j <= hi) == sees);
           }
         }
+  // Units: as many as cover a span, from the pass that holds its first position.
+  for (int64_t lo = 0; lo < 300; lo += 7)
+    for (int64_t hi = lo - 3; hi < lo + 700; ++hi) {
+      const int64_t n = kv_units(lo, hi), first = lo - lo % 32;
+      if (hi < lo) {
+        CHECK(n == 1);
+      } else {
+        CHECK(first + n * 128 > hi && first + (n - 1) * 128 <= hi);
+        CHECK(n <= kv_units(31, 30 + hi - lo + 1));  // the host's bound
+      }
+    }
+
+  // Shares: they follow one another, hold all units, differ by one at most, and each unit knows its share.
+  for (int64_t units = 1; units < 200; units += 3)
+    for (int64_t groups = 8; groups <= 64; groups += 8) {
+      CHECK(kv_share_begin(units, 0, groups) == 0 && kv_share_begin(units, groups, groups) == units);
+      for (int64_t w = 0; w < groups; ++w) {
+        const int64_t begin = kv_share_begin(units, w, groups), end = kv_share_begin(units, w + 1, groups);
+        CHECK(end - begin >= units / groups && end - begin <= units / groups + 1);
+        if (units >= groups) CHECK(end > begin);
+        for (int64_t p = begin; p < end; ++p) CHECK(kv_share_of(p, units, groups) == w);
+      }
+    }
+  const int64_t most = (int64_t)512 * 65535 * (1 << 24);
+  CHECK(kv_share_of(most - 1, most, 1024) == 1023 && kv_share_begin(most, 1024, 1024) == most);
   std::printf("ok\n");
   return 0;
 }
