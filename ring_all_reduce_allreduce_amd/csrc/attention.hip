@@ -15,15 +15,12 @@ namespace {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Rows of a workgroup whose waves have their own rows, by type: two tiles of
-// 16 a wave for bf16, one for the types whose products take several parts.
-int wide_rows(int dtype) { return dtype == RINGSIM_BFLOAT16 ? 128 : 64; }
 constexpr int kNarrowRows = 16;
 
 // Workgroups that share a call's work: as many as the card runs at once.
 #ifndef RINGSIM_GROUPS
 #define RINGSIM_GROUPS 512
-#define RINGSIM_WIDE_GROUPS 256
+#define RINGSIM_WIDE_GROUPS 512
 #endif
 constexpr int kNarrowGroups = RINGSIM_GROUPS;
 constexpr int kWideGroups = RINGSIM_WIDE_GROUPS;
@@ -35,7 +32,7 @@ AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int head
   AttentionPlan p;
   const int64_t group = heads / kv_heads, rows = tokens * group / seqs;  // of a sequence's key head, on average
   p.wide = rows > 64;
-  p.tile_rows = p.wide ? wide_rows(dtype) : kNarrowRows;
+  p.tile_rows = p.wide ? 64 * wide_tiles(dtype, dim) : kNarrowRows;
   p.tiles = ragged ? tokens * group / p.tile_rows + seqs : seqs * ceil_div(tokens / seqs * group, p.tile_rows);
   // Positions that a tile may see: all, or a window for each of its tokens. The
   // first unit may begin before the first of them.
@@ -70,19 +67,14 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, i
 // the outputs for the weights. Heads of 128 columns and fewer leave half of
 // the lanes for a second part: even ones go to the first half, odd ones to the
 // second.
-constexpr int kJoinRows = 4;     // of a workgroup
+constexpr int kJoinRows = 4;     // of a workgroup at a time
+constexpr int kJoinBlocks = 4;   // workgroups of a tile
 constexpr int kJoinAhead = 8;    // outputs whose loads are under way
 
 template <int DT, int HALVES>
-__global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const AttentionArgs a) {
-  const int item = blockIdx.x, tile_index = item / a.cache.heads, key_head = item - tile_index * a.cache.heads;
-  RowTile tile;
-  if (!row_tile(a, a.starts, tile_index, tile)) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int in_tile = blockIdx.y * kJoinRows + wave, row = tile.row + in_tile;
-  if (row >= tile.rows) return;
-  const int first = a.part_of[2 * item], parts = a.part_of[2 * item + 1] - first + 1;
-  if (parts == 1) return;
+__device__ __forceinline__ void join_row(const AttentionArgs& a, const RowTile& tile, int key_head, int in_tile,
+                                         int first, int parts) {
+  const int lane = threadIdx.x & 63, row = tile.row + in_tile;
   const int token = row / a.group, head = key_head * a.group + row - token * a.group;
   const int half = HALVES == 2 ? lane >> 5 : 0, col = (HALVES == 2 ? lane & 31 : lane) * 4;
   const float inf = __builtin_inff();
@@ -138,9 +130,21 @@ __global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const At
   y.store(out_row<DT>(a, tile, token, head) + col);
 }
 
+template <int DT, int HALVES>
+__global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const AttentionArgs a) {
+  const int item = blockIdx.x, tile_index = item / a.cache.heads, key_head = item - tile_index * a.cache.heads;
+  RowTile tile;
+  if (!row_tile(a, a.starts, tile_index, tile)) return;
+  const int first = a.part_of[2 * item], parts = a.part_of[2 * item + 1] - first + 1;
+  if (parts == 1) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int row = blockIdx.y * kJoinRows + wave; row < min(a.tile_rows, tile.rows - tile.row); row += gridDim.y * kJoinRows)
+    join_row<DT, HALVES>(a, tile, key_head, row, first, parts);
+}
+
 template <int DT>
 static hipError_t launch_join(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, (unsigned)ceil_div(a.tile_rows, kJoinRows));
+  const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, kJoinBlocks);
   const dim3 block(64 * kJoinRows);
   if (a.cache.dim <= 128)
     hipLaunchKernelGGL((attention_join_kernel<DT, 2>), grid, block, 0, s, a);

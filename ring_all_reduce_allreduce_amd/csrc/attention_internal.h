@@ -138,6 +138,12 @@ struct AttentionPlan {
 AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
                              int64_t cap, int64_t window);
 
+// Tiles of 16 rows of a wave with rows of its own: two where a wave's registers
+// hold them, else one (types whose products take several parts, long heads).
+__host__ __device__ constexpr int wide_tiles(int dtype, int dim) {
+  return dtype == RINGSIM_BFLOAT16 && dim <= 128 ? 2 : 1;
+}
+
 // Most tiles whose work is shared: their units are counted in LDS.
 constexpr int kSharedTiles = 512;
 // Where a workgroup leaves its part of a tile: the one that it begins but does

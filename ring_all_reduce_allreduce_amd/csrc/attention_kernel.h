@@ -142,6 +142,28 @@ __device__ __forceinline__ uint32_t two_columns(uint32_t codes, float unit, int 
   }
 }
 
+// A value's exponents of four positions.
+__device__ __forceinline__ void value_units(uint32_t w, float* unit) {
+  unit[0] = unit_of<0>(w);
+  unit[1] = unit_of<1>(w);
+  unit[2] = unit_of<2>(w);
+  unit[3] = unit_of<3>(w);
+}
+
+// Of eight positions' pairs of columns the first or the second column.
+__device__ __forceinline__ u32x4 one_column(const uint32_t (&w)[8], int half) {
+  u32x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], half ? 0x07060302u : 0x05040100u);
+  return v;
+}
+
+// The largest of three, NaN if one is: one instruction, which fmaxf, having to
+// look at the kinds of NaN, is not.
+__device__ __forceinline__ float larger(float x, float y, float z) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(x, y), z);
+}
+
 __device__ __forceinline__ f32x4 mfma(const u32x4& x, const u32x4& y, f32x4 acc) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), acc, 0,
                                                  0, 0);
@@ -176,27 +198,11 @@ constexpr int kTermBits = 5;
 constexpr float kTermStep = 1 << kTermBits;
 constexpr int kTermTop = 7;  // exponent of a row's largest magnitude in its first part
 
-// What a wave has to do, the same for all of its lanes.
-struct WaveJob {
-  const uint8_t* k;        // of the key head: keys, values and their scales of page 0
-  const uint8_t* v;
-  const uint8_t* ks;
-  const uint8_t* vs;
-  const int32_t* pages;    // of the sequence
-  int begin, end;          // positions, begin a multiple of kKvStep; `end` past the last one wanted
-  int stride;              // from one pass of this wave to the next
-  int full_lo, full_hi;    // positions that every row of the wave sees
-  int length;              // positions of the sequence
-};
-
-// DT, D: type of queries and columns of a head. NQ: tiles of 16 rows. PT: bf16
-// parts of a weight. AHEAD: passes whose loads are under way. ONE: all rows of a
-// wave belong to one token, so a position is seen by all of them or none, and
-// what the cache holds where none sees is taken as ones; else a position's NaN
-// has to reach the rows that see it and no others, for which a wave that finds
-// a NaN in its sums starts again the slow way.
-template <int DT, int D, int NQ, int PT, int AHEAD, bool ONE>
-struct AttentionWave {
+// The rows of a wave: queries, sums, and the mathematics of a pass of 32
+// positions. DT, D: type of queries and columns of a head. NQ: tiles of 16
+// rows. PT: bf16 parts of a weight.
+template <int DT, int D, int NQ, int PT>
+struct RowSums {
   using H = HeadParts<D>;
   using B = HeadBlocks<D, kQueryTerms<DT>>;
 
@@ -207,7 +213,6 @@ struct AttentionWave {
   float exact[NQ];         // PT 1, with lse: the lane's sum of weights before their rounding
   float m[NQ];             // reference exponent, minus infinity until a position is seen
   int lo[NQ], hi[NQ];      // positions that this lane's row sees
-  int32_t ids;             // lane i: page of the wave's tile i of the next 64, -1: none
 
   __device__ __forceinline__ void clear() {
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -289,6 +294,147 @@ struct AttentionWave {
     }
   }
 
+  // Products with the keys of two tiles; key(t, set, k, ks) gives a lane's block.
+  template <typename KEY>
+  __device__ __forceinline__ void scores(f32x4 (&s)[NQ][2], const KEY& key) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int r = 0; r < NQ; ++r) s[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int set = 0; set < B::kSets; ++set) {
+        u32x4 k;
+        uint32_t ks;
+        key(t, set, k, ks);
+#pragma unroll
+        for (int turn = B::kTurns - 1; turn >= 0; --turn) {
+#pragma unroll
+          for (int r = 0; r < NQ; ++r) s[r][t] = mfma_scaled(k, ks, q[r][set][turn], qs[r][set][turn], s[r][t]);
+        }
+      }
+    }
+  }
+
+  // Takes out what a row does not see. seen: a bit a position.
+  __device__ __forceinline__ void mask(f32x4 (&s)[NQ][2], int at, bool there0, bool there1, uint32_t (&seen)[NQ]) const {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+      seen[r] = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = at + kKvTile * t + 4 * g + i;
+          const bool on = j >= lo[r] && j <= hi[r] && (t ? there1 : there0);
+          s[r][t][i] = on ? s[r][t][i] : -__builtin_inff();
+          seen[r] |= (uint32_t)on << (4 * t + i);
+        }
+      }
+    }
+  }
+
+  // Weights of the lane's eight positions in PT parts, and their sums.
+  __device__ __forceinline__ void weights(const AttentionArgs& a, const f32x4 (&s)[NQ][2], u32x4 (&p)[NQ][PT]) {
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+      // A NaN stays one, so the row keeps its reference.
+      const float top = a.scale_log2 * larger(larger(larger(s[r][0][0], s[r][0][1], s[r][0][2]), s[r][0][3], s[r][1][0]),
+                                              s[r][1][1], larger(s[r][1][2], s[r][1][3], s[r][1][3]));
+      if (__any(top > m[r] + kSlack)) {
+        const float next = fmaxf(m[r], groups_max(top));
+        // exp2(-inf) = 0 on a row's first positions; a row without any keeps its zeros.
+        const float by = next == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);
+        m[r] = next;
+        exact[r] *= by;
+        l[r] *= by;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) o[r][d] *= by;
+      }
+      const float ref = m[r] == -__builtin_inff() ? 0.0f : m[r];
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i / 4][i % 4], a.scale_log2, -ref));
+      if (PT == 1 && a.lse) exact[r] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+#pragma unroll
+      for (int e = 0; e < PT; ++e) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = to_bf16x2(w[2 * j], w[2 * j + 1]);
+          p[r][e][j] = x;
+          if (e + 1 < PT) {
+            w[2 * j] -= bf16_lo(x);
+            w[2 * j + 1] -= bf16_hi(x);
+          }
+        }
+        // The sums are those of the rounded weights, so a row that one
+        // position rules gets that position's values.
+        const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+        l[r] = mfma(ones, p[r][e], l[r]);
+      }
+    }
+  }
+
+  // Adds 16 columns of the values, positions as the lane's weights have them.
+  __device__ __forceinline__ void add_values(int d, const u32x4& v, const u32x4 (&p)[NQ][PT]) {
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+#pragma unroll
+      for (int e = PT - 1; e >= 0; --e) o[r][d] = mfma(v, p[r][e], o[r][d]);
+    }
+  }
+
+  // A row's sum of weights as lse takes it: rounded to one bf16 they would be
+  // off by more than fp32's last bits.
+  __device__ __forceinline__ float exact_sum(int r) const {
+    if constexpr (PT > 1) return l[r][0];
+    float v = exact[r] + __shfl_xor(exact[r], 16);
+    return v + __shfl_xor(v, 32);
+  }
+
+  // Whether a NaN of the cache (or of a query) has come into any row.
+  __device__ __forceinline__ bool has_nan() const {
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad |= !(o[r][d][i] == o[r][d][i]);
+      }
+    }
+    return __any(bad);
+  }
+};
+
+// What a wave has to do, the same for all of its lanes.
+struct WaveJob {
+  const uint8_t* k;        // of the key head: keys, values and their scales of page 0
+  const uint8_t* v;
+  const uint8_t* ks;
+  const uint8_t* vs;
+  const int32_t* pages;    // of the sequence
+  int begin, end;          // positions, begin a multiple of kKvStep; `end` past the last one wanted
+  int stride;              // from one pass of this wave to the next
+  int full_lo, full_hi;    // positions that every row of the wave sees
+  int length;              // positions of the sequence
+};
+
+// A wave on its own: keys and values go from memory to its registers. AHEAD:
+// passes whose loads are under way. ONE: all rows of the wave belong to one
+// token, so a position is seen by all of them or none, and what the cache holds
+// where none sees is taken as ones. Else a position's NaN has to reach the rows
+// that see it and no others, for which there is the slow way.
+template <int DT, int D, int NQ, int PT, int AHEAD, bool ONE>
+struct AttentionWave : RowSums<DT, D, NQ, PT> {
+  using R = RowSums<DT, D, NQ, PT>;
+  using typename R::B;
+  using typename R::H;
+  using R::o;
+
+  int32_t ids;             // lane i: page of the wave's tile i of the next 64, -1: none
+
   // Pages of the 64 tiles of the next 32 passes, from position `at` on.
   __device__ __forceinline__ void load_pages(const AttentionArgs& a, const WaveJob& job, int at) {
     const int lane = threadIdx.x & 63;
@@ -340,90 +486,25 @@ struct AttentionWave {
   // reach the rows that see it and no others, which 0 * NaN would not do.
   template <bool SLOW>
   __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, const KvRaw<D>& raw) {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
     f32x4 s[NQ][2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int r = 0; r < NQ; ++r) {
-        s[r][t] = zero;
-#pragma unroll
-        for (int set = 0; set < B::kSets; ++set) {
-#pragma unroll
-          for (int turn = B::kTurns - 1; turn >= 0; --turn)
-            s[r][t] = mfma_scaled(raw.k[t][set], raw.ks[t][set], q[r][set][turn], qs[r][set][turn], s[r][t]);
-        }
-      }
-    }
-    uint32_t seen[NQ];  // a bit a position
+    R::scores(s, [&](int t, int set, u32x4& k, uint32_t& ks) {
+      k = raw.k[t][set];
+      ks = raw.ks[t][set];
+    });
+    uint32_t seen[NQ];
     bool masked = SLOW;
     if (SLOW || !raw.there[0] || !raw.there[1] || at < job.full_lo || at + kKvStep - 1 > job.full_hi) {
       masked = true;
-#pragma unroll
-      for (int r = 0; r < NQ; ++r) {
-        seen[r] = 0;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = at + kKvTile * t + 4 * g + i;
-            const bool on = j >= lo[r] && j <= hi[r] && raw.there[t];
-            s[r][t][i] = on ? s[r][t][i] : -__builtin_inff();
-            seen[r] |= (uint32_t)on << (4 * t + i);
-          }
-        }
-      }
+      R::mask(s, at, raw.there[0], raw.there[1], seen);
     }
     u32x4 p[NQ][PT];
-#pragma unroll
-    for (int r = 0; r < NQ; ++r) {
-      float top = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
-      top *= a.scale_log2;
-      if (__any(top > m[r] + kSlack)) {
-        const float next = fmaxf(m[r], groups_max(top));
-        // exp2(-inf) = 0 on a row's first positions; a row without any keeps its zeros.
-        const float by = next == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);
-        m[r] = next;
-        exact[r] *= by;
-        l[r] *= by;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) o[r][d] *= by;
-      }
-      const float ref = m[r] == -__builtin_inff() ? 0.0f : m[r];
-      float w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i / 4][i % 4], a.scale_log2, -ref));
-      if (PT == 1 && a.lse) exact[r] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
-#pragma unroll
-      for (int e = 0; e < PT; ++e) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t x = to_bf16x2(w[2 * j], w[2 * j + 1]);
-          p[r][e][j] = x;
-          if (e + 1 < PT) {
-            w[2 * j] -= bf16_lo(x);
-            w[2 * j + 1] -= bf16_hi(x);
-          }
-        }
-        // The sums are those of the rounded weights, so a row that one
-        // position rules gets that position's values.
-        const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-        l[r] = mfma(ones, p[r][e], l[r]);
-      }
-    }
+    R::weights(a, s, p);
 #pragma unroll
     for (int part = 0; part < H::kParts; ++part) {
       float unit[8];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        unit[4 * t] = unit_of<0>(raw.vs[t][part]);
-        unit[4 * t + 1] = unit_of<1>(raw.vs[t][part]);
-        unit[4 * t + 2] = unit_of<2>(raw.vs[t][part]);
-        unit[4 * t + 3] = unit_of<3>(raw.vs[t][part]);
-      }
+      for (int t = 0; t < 2; ++t) value_units(raw.vs[t][part], unit + 4 * t);
       if constexpr (ONE) {
         // The lane's positions are those of its weights, and all rows see the same.
         if (masked) {
@@ -433,10 +514,9 @@ struct AttentionWave {
       }
 #pragma unroll
       for (int b = 0; b < H::n(part); ++b) {  // two columns a byte
-        uint32_t w[8];
+        uint32_t w[8], nan[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = two_columns(raw.v[i][H::reg0(part) + b / 4], unit[i], b % 4);
-        uint32_t nan[8];
         if constexpr (SLOW) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -447,22 +527,16 @@ struct AttentionWave {
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint32_t pick = half ? 0x07060302u : 0x05040100u;
-          u32x4 v;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], pick);
           const int d = H::base(part) / 16 + 2 * b + half;
+          R::add_values(d, one_column(w, half), p);
+          if constexpr (SLOW) {
+            const u32x4 x = one_column(nan, half);
 #pragma unroll
-          for (int r = 0; r < NQ; ++r) {
+            for (int r = 0; r < NQ; ++r) {
+              u32x4 y;
 #pragma unroll
-            for (int e = PT - 1; e >= 0; --e) o[r][d] = mfma(v, p[r][e], o[r][d]);
-            if constexpr (SLOW) {
-              u32x4 x, y;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                x[j] = __builtin_amdgcn_perm(nan[2 * j + 1], nan[2 * j], pick);
+              for (int j = 0; j < 4; ++j)
                 y[j] = (seen[r] >> (2 * j) & 1 ? 0x3f80u : 0u) | (seen[r] >> (2 * j + 1) & 1 ? 0x3f800000u : 0u);
-              }
               const f32x4 hits = mfma(x, y, zero);
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[r][d][i] = hits[i] > 0.0f ? __builtin_nanf("") : o[r][d][i];
@@ -475,7 +549,7 @@ struct AttentionWave {
 
   template <bool SLOW>
   __device__ __forceinline__ void run(const AttentionArgs& a, const WaveJob& job) {
-    clear();
+    R::clear();
     if (job.begin >= job.end) return;
     // Buffers in turn, loaded AHEAD passes before they are worked on. No load
     // stands under a condition: behind one, the compiler would wait for all that
@@ -502,46 +576,193 @@ struct AttentionWave {
     }
   }
 
-  // A row's sum of weights as lse takes it: rounded to one bf16 they would be
-  // off by more than fp32's last bits.
-  __device__ __forceinline__ float exact_sum(int r) const {
-    if constexpr (PT > 1) return l[r][0];
-    float v = exact[r] + __shfl_xor(exact[r], 16);
-    return v + __shfl_xor(v, 32);
+};
+
+// The waves of a workgroup together, each with rows of its own. Per stage of 64
+// positions each wave brings a quarter of the keys and values: keys as they
+// lie in memory, values already as operands of the second product, so that the
+// conversion is done once for all rows of the workgroup. Two buffers, one
+// barrier a stage, the next stage's loads under way during it.
+constexpr int kStage = 64;
+constexpr int kStageTiles = kStage / kKvTile;
+
+template <int D>
+struct WideBuffers {
+  static constexpr int kSets = (D / 32 + 3) / 4;
+  u32x4 k[2][kStageTiles][kSets][64];
+  u32x4 v[2][2][D / 16][64];
+  uint32_t ks[2][kStageTiles][kSets][64];
+};
+
+template <int DT, int D, int NQ, int PT>
+struct WideWave : RowSums<DT, D, NQ, PT> {
+  using R = RowSums<DT, D, NQ, PT>;
+  using typename R::B;
+  using typename R::H;
+  static constexpr int kSets = B::kSets;
+
+  int32_t ids;             // lane i: page of tile i of the next 64, -1: none
+
+  // What a wave brings: the keys of tile `wave`, and of the values of 32
+  // positions (wave / 2 of two) one half of the bytes, wave % 2: half of each
+  // lane's, or where a head has two parts, one part.
+  struct Raw {
+    u32x4 k[kSets];
+    uint32_t ks[kSets];
+    uint32_t v[8];
+    uint32_t vs[2];
+  };
+  static constexpr int bytes(int half) { return H::kParts == 1 ? H::n(0) / 2 : H::n(half); }
+
+  template <int HALF>
+  __device__ __forceinline__ void load_values(const AttentionArgs& a, const uint8_t* v, const uint8_t* vs, Raw& raw, int t) {
+    constexpr int kPart = H::kParts == 1 ? 0 : HALF, kRow = D / 2, kBytes = bytes(HALF);
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const uint32_t from = (uint32_t)(4 * g * kRow + H::base(kPart) / 2 + c * H::n(kPart) + (H::kParts == 1 ? HALF * kBytes : 0));
+    const GlobalBytes pv = uniform(v), pvs = uniform(vs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_bytes<kBytes>(&raw.v[4 * t + i], pv + i * kRow, from);
+    const uint32_t b = H::base(kPart) / 32 + c * H::n(kPart) / 16;
+    load_bytes<4>(&raw.vs[t], pvs, (b << a.cache.page_shift) + (uint32_t)(4 * g));
   }
 
-  // Whether a NaN of the cache (or of a query) has come into any row.
-  __device__ __forceinline__ bool has_nan() const {
-    bool bad = false;
+  // Stage from position `at` on, its first tile number `first` of those in ids.
+  // Returns which of its tiles have a page, a bit each.
+  __device__ __forceinline__ uint32_t load_stage(const AttentionArgs& a, const WaveJob& job, int wave, int at, int first,
+                                                 Raw& raw) {
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const auto place = [&](int t, int64_t* data, int64_t* scale) {
+      const int32_t id = __builtin_amdgcn_readlane(ids, first + t);
+      const int64_t page = id < 0 ? 0 : id;
+      const int off = (at + kKvTile * t) & ((1 << a.cache.page_shift) - 1);
+      *data = page * a.cache.page + off * (D / 2);
+      *scale = page * a.cache.scale_page + off;
+    };
+    int64_t data, scale;
+    place(wave, &data, &scale);
+    const GlobalBytes pk = uniform(job.k + data), pks = uniform(job.ks + scale);
 #pragma unroll
-    for (int r = 0; r < NQ; ++r) {
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bad |= !(o[r][d][i] == o[r][d][i]);
-      }
+    for (int set = 0; set < kSets; ++set) {
+      const uint32_t block = B::block(set, g);
+      uint32_t k[4];
+      load_bytes<16>(k, pk, (uint32_t)c * (D / 2) + block * 16);
+      raw.k[set] = u32x4{k[0], k[1], k[2], k[3]};
+      load_bytes<1>(&raw.ks[set], pks, (block << a.cache.page_shift) + (uint32_t)c);
     }
-    return __any(bad);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      place((wave & 2) + t, &data, &scale);
+      if (wave & 1)
+        load_values<1>(a, job.v + data, job.vs + scale, raw, t);
+      else
+        load_values<0>(a, job.v + data, job.vs + scale, raw, t);
+    }
+    uint32_t there = 0;
+#pragma unroll
+    for (int t = 0; t < kStageTiles; ++t) there |= (uint32_t)(__builtin_amdgcn_readlane(ids, first + t) >= 0) << t;
+    return there;
+  }
+
+  template <int HALF>
+  __device__ __forceinline__ void put_values(const Raw& raw, u32x4 (&v)[D / 16][64]) {
+    constexpr int kPart = H::kParts == 1 ? 0 : HALF, kBytes = bytes(HALF);
+    constexpr int kFirst = H::base(kPart) / 16 + (H::kParts == 1 ? 2 * kBytes * HALF : 0);
+    const int lane = threadIdx.x & 63;
+    float unit[8];
+    value_units(raw.vs[0], unit);
+    value_units(raw.vs[1], unit + 4);
+#pragma unroll
+    for (int b = 0; b < kBytes; ++b) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = two_columns(raw.v[i], unit[i], b);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) v[kFirst + 2 * b + half][lane] = one_column(w, half);
+    }
+  }
+
+  __device__ __forceinline__ void put(WideBuffers<D>& lds, int buffer, int wave, const Raw& raw) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int set = 0; set < kSets; ++set) {
+      lds.k[buffer][wave][set][lane] = raw.k[set];
+      lds.ks[buffer][wave][set][lane] = raw.ks[set];
+    }
+    if (wave & 1)
+      put_values<1>(raw, lds.v[buffer][wave >> 1]);
+    else
+      put_values<0>(raw, lds.v[buffer][wave >> 1]);
+  }
+
+  // One pass over the 32 positions from `at` on, half `sub` of a stage.
+  __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, const WideBuffers<D>& lds,
+                                       int buffer, int sub, uint32_t there) {
+    const int lane = threadIdx.x & 63;
+    f32x4 s[NQ][2];
+    R::scores(s, [&](int t, int set, u32x4& k, uint32_t& ks) {
+      k = lds.k[buffer][2 * sub + t][set][lane];
+      ks = lds.ks[buffer][2 * sub + t][set][lane];
+    });
+    if (there != 3 || at < job.full_lo || at + kKvStep - 1 > job.full_hi) {
+      uint32_t seen[NQ];
+      R::mask(s, at, there & 1, there & 2, seen);
+    }
+    u32x4 p[NQ][PT];
+    R::weights(a, s, p);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) R::add_values(d, lds.v[buffer][sub][d][lane], p);
+  }
+
+  // job.begin to job.end: the workgroup's positions; [own_begin, own_end) of them this wave's rows see.
+  __device__ __forceinline__ void run(const AttentionArgs& a, const WaveJob& job, int wave, int own_begin, int own_end,
+                                      WideBuffers<D>& lds) {
+    R::clear();
+    if (job.begin >= job.end) return;
+    const int stages = (job.end - job.begin + kStage - 1) / kStage;
+    constexpr int kWindow = 64 / kStageTiles;  // stages whose pages `ids` holds
+    Raw raw;
+    const auto load = [&](int i) {
+      if (i % kWindow == 0) {
+        const int64_t tile = ((int64_t)job.begin + (int64_t)i * kStage) / kKvTile + (threadIdx.x & 63);
+        ids = kv_page_of_tile(job.pages, tile, job.length, a.cache.page_shift, a.max_pages, a.cache.pages);
+      }
+      return load_stage(a, job, wave, job.begin + i * kStage, i % kWindow * kStageTiles, raw);
+    };
+    uint32_t there = load(0);
+    __syncthreads();  // the buffers have been read
+    put(lds, 0, wave, raw);
+    __syncthreads();
+    for (int i = 0; i < stages; ++i) {
+      const int at = job.begin + i * kStage;
+      uint32_t next = 0;
+      if (i + 1 < stages) next = load(i + 1);
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const int from = at + sub * kKvStep;
+        if (from < own_end && from + kKvStep > own_begin) pass(a, job, from, lds, i & 1, sub, there >> (2 * sub) & 3);
+      }
+      if (i + 1 < stages) put(lds, (i + 1) & 1, wave, raw);
+      __syncthreads();
+      there = next;
+    }
   }
 };
 
-// What one kernel is made for. NQ: tiles of 16 rows of a wave; WT: waves that
-// share rows (1: each wave has its own); PT, AHEAD, ONE as above.
-template <int DT_, int D_, int NQ_, int WT_, int PT_, int AHEAD_, bool ONE_>
+// What one kernel is made for. WIDE: waves have rows of their own, NQ tiles of
+// 16 each; else they share one tile and take turns with the positions.
+template <int DT_, int D_, int NQ_, int PT_, bool WIDE_, bool ONE_>
 struct AttentionShape {
-  static constexpr int DT = DT_, D = D_, NQ = NQ_, WT = WT_, PT = PT_, AHEAD = AHEAD_;
-  static constexpr bool ONE = ONE_;
-  using Wave = AttentionWave<DT, D, NQ, PT, AHEAD, ONE>;
+  static constexpr int DT = DT_, D = D_, NQ = NQ_, PT = PT_;
+  static constexpr bool WIDE = WIDE_, ONE = ONE_;
 };
 
 // Where waves that share rows join their parts.
-template <class S>
+template <int D>
 struct JoinBuffers {
-  static constexpr int kRow = S::D + 4;  // rows start 4 banks apart
-  float refs[S::WT][16], sums[S::WT][16];
-  float outs[S::WT][16][kRow];
+  static constexpr int kRow = D + 4;  // rows start 4 banks apart
+  float refs[kAttentionWaves][16], sums[kAttentionWaves][16];
+  float outs[kAttentionWaves][16][kRow];
 };
-struct NoBuffers {};
 
 // A row's result, or with a slot its part.
 template <class S>
@@ -570,130 +791,190 @@ __device__ __forceinline__ void store_columns(const AttentionArgs& a, const RowT
   }
 }
 
-// Rows of a tile with one key head over the positions [begin, end), begin a
-// multiple of kKvStep; the result goes out, or into a slot if it is a part.
-template <class S, class BUFFERS>
-__device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& tile, int key_head, int begin, int end,
-                                       int slot, BUFFERS& lds) {
-  constexpr int D = S::D, NQ = S::NQ, WT = S::WT;
-  using H = HeadParts<D>;
-  // What is the same for all lanes of a wave, and told to be, stays in scalar
-  // registers: the loop's places and counts among it.
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int row0 = tile.row + (WT == 1 ? wave * NQ * 16 : 0);  // of this wave
-  typename S::Wave w;
+__device__ __forceinline__ WaveJob wave_job(const AttentionArgs& a, const RowTile& tile, int key_head) {
+  const int64_t head = key_head * a.cache.head, scale_head = key_head * a.cache.scale_head;
   WaveJob job;
-  {
-    const int64_t head = key_head * a.cache.head, scale_head = key_head * a.cache.scale_head;
-    job.k = a.cache.data[0] + head;
-    job.v = a.cache.data[1] + head;
-    job.ks = a.cache.scales[0] + scale_head;
-    job.vs = a.cache.scales[1] + scale_head;
-    job.pages = a.pages + tile.seq * a.page_stride;
-    job.length = tile.length;
-    job.stride = WT * kKvStep;
-    const int row1 = min(row0 + NQ * 16, tile.rows) - 1;
-    int wave_lo, wave_hi;
-    span(a, tile.first + row0 / a.group, tile.length, &wave_lo, &job.full_hi);
-    span(a, tile.first + row1 / a.group, tile.length, &job.full_lo, &wave_hi);
-    job.begin = begin + (WT == 1 ? 0 : wave * kKvStep);
-    job.end = min(end, wave_hi + 1);
-    if (WT == 1) job.begin = max(job.begin, wave_lo / kKvStep * kKvStep);
-    if (row0 >= tile.rows) job.end = job.begin;
-  }
-  // A row beyond the last one repeats it, and is not stored.
+  job.k = a.cache.data[0] + head;
+  job.v = a.cache.data[1] + head;
+  job.ks = a.cache.scales[0] + scale_head;
+  job.vs = a.cache.scales[1] + scale_head;
+  job.pages = a.pages + tile.seq * a.page_stride;
+  job.length = tile.length;
+  return job;
+}
+
+// The rows row0 to row0 + rows of a tile that a wave has: what all of them see
+// into job, and [*lo, *hi] what any of them sees.
+__device__ __forceinline__ void wave_span(const AttentionArgs& a, const RowTile& tile, int row0, int rows, WaveJob& job,
+                                          int* lo, int* hi) {
+  const int row1 = min(row0 + rows, tile.rows) - 1;
+  span(a, tile.first + row0 / a.group, tile.length, lo, &job.full_hi);
+  span(a, tile.first + row1 / a.group, tile.length, &job.full_lo, hi);
+}
+
+// A lane's row of each tile of 16 from row0 on. One beyond the tile's last row
+// repeats it, and is not stored.
+template <int NQ>
+struct LaneRows {
   int token[NQ], head[NQ];
+};
+template <int DT, int D, int NQ, int PT>
+__device__ __forceinline__ LaneRows<NQ> take_rows(const AttentionArgs& a, const RowTile& tile, int key_head, int row0,
+                                                  RowSums<DT, D, NQ, PT>& w) {
+  const int c = threadIdx.x & 15;
+  LaneRows<NQ> at;
 #pragma unroll
   for (int r = 0; r < NQ; ++r) {
     const int row = min(row0 + 16 * r + c, tile.rows - 1);
-    token[r] = row / a.group;
-    head[r] = key_head * a.group + row - token[r] * a.group;
-    span(a, tile.first + token[r], tile.length, &w.lo[r], &w.hi[r]);
+    at.token[r] = row / a.group;
+    at.head[r] = key_head * a.group + row - at.token[r] * a.group;
+    span(a, tile.first + at.token[r], tile.length, &w.lo[r], &w.hi[r]);
   }
 #pragma unroll
-  for (int r = 0; r < NQ; ++r) w.load_queries(r, query_row<S::DT>(a, tile, token[r], head[r]));
+  for (int r = 0; r < NQ; ++r) w.load_queries(r, query_row<DT>(a, tile, at.token[r], at.head[r]));
+  return at;
+}
+
+// The tile of 16 rows from row0 on out of a wave's sums.
+template <class S, int NQ>
+__device__ __forceinline__ void store_rows(const AttentionArgs& a, const RowTile& tile, int slot, int row0,
+                                           const RowSums<S::DT, S::D, NQ, S::PT>& w, const LaneRows<NQ>& at, int r) {
+  using H = HeadParts<S::D>;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int in_tile = row0 - tile.row + c;
+  const float exact = w.exact_sum(r);
+  if (row0 + c >= tile.rows) return;
+  const float sum = w.l[r][0];
+  const float ref = w.m[r] == -__builtin_inff() && sum != 0.0f ? 0.0f : w.m[r];  // NaN sums without a maximum
+  if (g == 0) store_sums<S>(a, tile, slot, in_tile, at.token[r], at.head[r], ref, sum, exact);
+#pragma unroll
+  for (int part = 0; part < H::kParts; ++part) {
+    const int n = H::n(part), d0 = H::base(part) / 16;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {  // 8 columns each
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int at_col = 8 * k + e, i = at_col / (2 * n), j = at_col % (2 * n);
+        f[e] = w.o[r][d0 + j][i];
+      }
+      store_columns<S>(a, tile, slot, in_tile, at.token[r], at.head[r], H::base(part) + 8 * n * g + 8 * k, sum, f);
+    }
+  }
+}
+
+// Rows of a tile with one key head over the positions [begin, end), begin a
+// multiple of kKvStep; the result goes out, or into a slot if it is a part.
+template <class S>
+__device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& tile, int key_head, int begin, int end,
+                                       int slot, WideBuffers<S::D>& lds) {
+  constexpr int D = S::D, NQ = S::NQ;
+  // What is the same for all lanes of a wave, and told to be, stays in scalar
+  // registers: the loop's places and counts among it.
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row0 = tile.row + wave * NQ * 16;
+  WaveJob job = wave_job(a, tile, key_head);
+  job.begin = begin;
+  job.end = end;
+  job.stride = kKvStep;
+  bool bad;
+  {
+    WideWave<S::DT, D, NQ, S::PT> w;
+    int lo, hi;
+    wave_span(a, tile, row0, NQ * 16, job, &lo, &hi);
+    if (row0 >= tile.rows) hi = lo - 1;
+    const auto at = take_rows(a, tile, key_head, row0, w);
+    w.run(a, job, wave, max(begin, lo), min(end, hi + 1), lds);
+    bad = w.has_nan();
+    if (!bad) {
+#pragma unroll
+      for (int r = 0; r < NQ; ++r) store_rows<S>(a, tile, slot, row0 + 16 * r, w, at, r);
+    }
+  }
+  if (bad) {
+    for (int r = 0; r < NQ; ++r) {
+      const int first = row0 + 16 * r;
+      if (first >= tile.rows) break;
+      AttentionWave<S::DT, D, 1, S::PT, 1, false> w;
+      int lo, hi;
+      wave_span(a, tile, first, 16, job, &lo, &hi);
+      job.begin = max(begin, lo / kKvStep * kKvStep);
+      job.end = min(end, hi + 1);
+      const auto at = take_rows(a, tile, key_head, first, w);
+      w.template run<true>(a, job);
+      store_rows<S>(a, tile, slot, first, w, at, 0);
+    }
+  }
+}
+
+template <class S>
+__device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& tile, int key_head, int begin, int end,
+                                       int slot, JoinBuffers<S::D>& lds) {
+  constexpr int D = S::D;
+  using H = HeadParts<D>;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  AttentionWave<S::DT, D, 1, S::PT, 1, S::ONE> w;
+  WaveJob job = wave_job(a, tile, key_head);
+  int lo, hi;
+  wave_span(a, tile, tile.row, 16, job, &lo, &hi);
+  job.stride = kAttentionWaves * kKvStep;
+  job.begin = begin + wave * kKvStep;
+  job.end = min(end, hi + 1);
+  take_rows(a, tile, key_head, tile.row, w);
   w.template run<false>(a, job);
   if constexpr (!S::ONE) {
     if (w.has_nan()) w.template run<true>(a, job);
   }
-
-  if constexpr (WT == 1) {
-#pragma unroll
-    for (int r = 0; r < NQ; ++r) {
-      const int in_tile = row0 - tile.row + 16 * r + c;
-      const float exact = w.exact_sum(r);
-      if (tile.row + in_tile >= tile.rows) continue;
-      const float sum = w.l[r][0];
-      const float ref = w.m[r] == -__builtin_inff() && sum != 0.0f ? 0.0f : w.m[r];
-      if (g == 0) store_sums<S>(a, tile, slot, in_tile, token[r], head[r], ref, sum, exact);
-#pragma unroll
-      for (int part = 0; part < H::kParts; ++part) {
-        const int n = H::n(part), d0 = H::base(part) / 16;
-#pragma unroll
-        for (int k = 0; k < n; ++k) {  // 8 columns each
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int at_col = 8 * k + e, i = at_col / (2 * n), j = at_col % (2 * n);
-            f[e] = w.o[r][d0 + j][i];
-          }
-          store_columns<S>(a, tile, slot, in_tile, token[r], head[r], H::base(part) + 8 * n * g + 8 * k, sum, f);
-        }
-      }
-    }
-  } else {
-    // The waves' parts of the positions, joined in a fixed order.
-    static_assert(NQ == 1, "waves that share rows have one tile of them");
-    const float own = w.m[0] == -__builtin_inff() && w.l[0][0] != 0.0f ? 0.0f : w.m[0];  // NaN sums without a maximum
-    if (g == 0) {
-      lds.refs[wave][c] = own;
-      lds.sums[wave][c] = w.l[0][0];
-    }
-    __syncthreads();
-    float top = lds.refs[0][c];
-#pragma unroll
-    for (int i = 1; i < WT; ++i) top = fmaxf(top, lds.refs[i][c]);
-    const float by = own == -__builtin_inff() ? 0.0f : own == top ? 1.0f : __builtin_amdgcn_exp2f(own - top);
-#pragma unroll
-    for (int part = 0; part < H::kParts; ++part) {
-      const int n = H::n(part), d0 = H::base(part) / 16;
-#pragma unroll
-      for (int k = 0; k < 2 * n; ++k) {  // 4 columns each
-        f32x4 f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at_col = 4 * k + e, i = at_col / (2 * n), j = at_col % (2 * n);
-          f[e] = w.o[0][d0 + j][i] * by;
-        }
-        *reinterpret_cast<f32x4*>(&lds.outs[wave][c][H::base(part) + 8 * n * g + 4 * k]) = f;
-      }
-    }
-    __syncthreads();
-    const int rows = min(16, tile.rows - tile.row);
-    for (int k = threadIdx.x; k < rows * (D / 8); k += kAttentionThreads) {
-      const int row = k / (D / 8), col = (k - row * (D / 8)) * 8;
-      float best = lds.refs[0][row], sum = 0.0f;
-#pragma unroll
-      for (int i = 1; i < WT; ++i) best = fmaxf(best, lds.refs[i][row]);
-#pragma unroll
-      for (int i = 0; i < WT; ++i) {
-        const float ref = lds.refs[i][row];
-        if (ref != -__builtin_inff()) sum += lds.sums[i][row] * (ref == best ? 1.0f : __builtin_amdgcn_exp2f(ref - best));
-      }
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        f[e] = lds.outs[0][row][col + e];
-#pragma unroll
-        for (int i = 1; i < WT; ++i) f[e] += lds.outs[i][row][col + e];
-      }
-      const int t = (tile.row + row) / a.group, h = key_head * a.group + tile.row + row - t * a.group;
-      if (col == 0) store_sums<S>(a, tile, slot, row, t, h, best, sum, sum);
-      store_columns<S>(a, tile, slot, row, t, h, col, sum, f);
-    }
-    __syncthreads();  // before the buffers are written again
+  // The waves' parts of the positions, joined in a fixed order.
+  const float own = w.m[0] == -__builtin_inff() && w.l[0][0] != 0.0f ? 0.0f : w.m[0];  // NaN sums without a maximum
+  if (g == 0) {
+    lds.refs[wave][c] = own;
+    lds.sums[wave][c] = w.l[0][0];
   }
+  __syncthreads();
+  float top = lds.refs[0][c];
+#pragma unroll
+  for (int i = 1; i < kAttentionWaves; ++i) top = fmaxf(top, lds.refs[i][c]);
+  const float by = own == -__builtin_inff() ? 0.0f : own == top ? 1.0f : __builtin_amdgcn_exp2f(own - top);
+#pragma unroll
+  for (int part = 0; part < H::kParts; ++part) {
+    const int n = H::n(part), d0 = H::base(part) / 16;
+#pragma unroll
+    for (int k = 0; k < 2 * n; ++k) {  // 4 columns each
+      f32x4 f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at_col = 4 * k + e, i = at_col / (2 * n), j = at_col % (2 * n);
+        f[e] = w.o[0][d0 + j][i] * by;
+      }
+      *reinterpret_cast<f32x4*>(&lds.outs[wave][c][H::base(part) + 8 * n * g + 4 * k]) = f;
+    }
+  }
+  __syncthreads();
+  const int rows = min(16, tile.rows - tile.row);
+  for (int k = threadIdx.x; k < rows * (D / 8); k += kAttentionThreads) {
+    const int row = k / (D / 8), col = (k - row * (D / 8)) * 8;
+    float best = lds.refs[0][row], sum = 0.0f;
+#pragma unroll
+    for (int i = 1; i < kAttentionWaves; ++i) best = fmaxf(best, lds.refs[i][row]);
+#pragma unroll
+    for (int i = 0; i < kAttentionWaves; ++i) {
+      const float ref = lds.refs[i][row];
+      if (ref != -__builtin_inff()) sum += lds.sums[i][row] * (ref == best ? 1.0f : __builtin_amdgcn_exp2f(ref - best));
+    }
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[e] = lds.outs[0][row][col + e];
+#pragma unroll
+      for (int i = 1; i < kAttentionWaves; ++i) f[e] += lds.outs[i][row][col + e];
+    }
+    const int t = (tile.row + row) / a.group, h = key_head * a.group + tile.row + row - t * a.group;
+    if (col == 0) store_sums<S>(a, tile, slot, row, t, h, best, sum, sum);
+    store_columns<S>(a, tile, slot, row, t, h, col, sum, f);
+  }
+  __syncthreads();  // before the buffers are written again
 }
 
 // Units of all tiles, counted by each workgroup for itself.
@@ -705,8 +986,8 @@ struct SharedUnits {
 // Either a workgroup a tile and key head, or an equal share of all units a
 // workgroup: it walks over the tiles that its share touches.
 template <class S>
-__global__ __launch_bounds__(kAttentionThreads) void attention_kernel(const AttentionArgs a) {
-  __shared__ std::conditional_t<S::WT == 1, NoBuffers, JoinBuffers<S>> lds;
+__global__ __launch_bounds__(kAttentionThreads, S::WIDE && S::D <= 192 ? 2 : 1) void attention_kernel(const AttentionArgs a) {
+  __shared__ std::conditional_t<S::WIDE, WideBuffers<S::D>, JoinBuffers<S::D>> lds;
   RowTile tile;
   if (a.groups == 0) {
     const int index = blockIdx.x / a.cache.heads;
@@ -799,14 +1080,10 @@ hipError_t launch_shape(const AttentionArgs& a, hipStream_t s) {
 template <int DT, int D>
 hipError_t launch_type(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t s) {
   constexpr int kParts = DT == RINGSIM_FLOAT32 ? 3 : 2;
-  if (plan.wide) {
-    if constexpr (DT == RINGSIM_BFLOAT16)
-      return launch_shape<AttentionShape<DT, D, 2, 1, 1, 1, false>>(a, s);
-    else
-      return launch_shape<AttentionShape<DT, D, 1, 1, kParts, 1, false>>(a, s);
-  }
-  return !a.starts && a.each == 1 ? launch_shape<AttentionShape<DT, D, 1, 4, kParts, 1, true>>(a, s)
-                                  : launch_shape<AttentionShape<DT, D, 1, 4, kParts, 1, false>>(a, s);
+  if (plan.wide)
+    return launch_shape<AttentionShape<DT, D, wide_tiles(DT, D), DT == RINGSIM_BFLOAT16 ? 1 : kParts, true, false>>(a, s);
+  return !a.starts && a.each == 1 ? launch_shape<AttentionShape<DT, D, 1, kParts, false, true>>(a, s)
+                                  : launch_shape<AttentionShape<DT, D, 1, kParts, false, false>>(a, s);
 }
 
 template <int D>
