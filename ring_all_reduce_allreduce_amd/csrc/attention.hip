@@ -22,6 +22,9 @@ constexpr int kNarrowRows = 16;
 #define RINGSIM_GROUPS 512
 #define RINGSIM_WIDE_GROUPS 512
 #endif
+#ifndef RINGSIM_DIRECT
+#define RINGSIM_DIRECT 512
+#endif
 constexpr int kNarrowGroups = RINGSIM_GROUPS;
 constexpr int kWideGroups = RINGSIM_WIDE_GROUPS;
 
@@ -41,7 +44,7 @@ AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int head
   const int64_t units = kv_units(kKvStep - 1, kKvStep - 2 + std::max<int64_t>(span, 1));
   const int64_t items = p.tiles * kv_heads;
   p.groups = 0;
-  if (p.tiles <= kSharedTiles && units > 1)
+  if (p.tiles <= kSharedTiles && units > 1 && !(p.wide && items >= RINGSIM_DIRECT))
     p.groups = (int)std::min<int64_t>(p.wide ? kWideGroups : kNarrowGroups, ceil_div(items * units, 8) * 8);
   return p;
 }
@@ -68,7 +71,6 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, i
 // the lanes for a second part: even ones go to the first half, odd ones to the
 // second.
 constexpr int kJoinRows = 4;     // of a workgroup at a time
-constexpr int kJoinBlocks = 4;   // workgroups of a tile
 constexpr int kJoinAhead = 8;    // outputs whose loads are under way
 
 template <int DT, int HALVES>
@@ -144,7 +146,7 @@ __global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const At
 
 template <int DT>
 static hipError_t launch_join(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, kJoinBlocks);
+  const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, (unsigned)std::max(1, std::min(a.tile_rows / kJoinRows, 2048 / std::max(1, a.tiles * a.cache.heads / 8))));
   const dim3 block(64 * kJoinRows);
   if (a.cache.dim <= 128)
     hipLaunchKernelGGL((attention_join_kernel<DT, 2>), grid, block, 0, s, a);

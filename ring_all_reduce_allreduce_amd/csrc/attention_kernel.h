@@ -334,15 +334,23 @@ struct RowSums {
     }
   }
 
-  // Weights of the lane's eight positions in PT parts, and their sums.
+  // Weights of the lane's eight positions in PT parts, and their sums. Few
+  // branches, each over all tiles, so that one tile's exponentials and another
+  // one's matrix instructions can be under way together.
   __device__ __forceinline__ void weights(const AttentionArgs& a, const f32x4 (&s)[NQ][2], u32x4 (&p)[NQ][PT]) {
+    float top[NQ];
+    bool above = false;
 #pragma unroll
     for (int r = 0; r < NQ; ++r) {
       // A NaN stays one, so the row keeps its reference.
-      const float top = a.scale_log2 * larger(larger(larger(s[r][0][0], s[r][0][1], s[r][0][2]), s[r][0][3], s[r][1][0]),
-                                              s[r][1][1], larger(s[r][1][2], s[r][1][3], s[r][1][3]));
-      if (__any(top > m[r] + kSlack)) {
-        const float next = fmaxf(m[r], groups_max(top));
+      top[r] = a.scale_log2 * larger(larger(larger(s[r][0][0], s[r][0][1], s[r][0][2]), s[r][0][3], s[r][1][0]),
+                                     s[r][1][1], larger(s[r][1][2], s[r][1][3], s[r][1][3]));
+      above |= top[r] > m[r] + kSlack;
+    }
+    if (__any(above)) {
+#pragma unroll
+      for (int r = 0; r < NQ; ++r) {
+        const float next = fmaxf(m[r], groups_max(top[r]));
         // exp2(-inf) = 0 on a row's first positions; a row without any keeps its zeros.
         const float by = next == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);
         m[r] = next;
@@ -351,21 +359,31 @@ struct RowSums {
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) o[r][d] *= by;
       }
+    }
+    float w[NQ][8];
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
       const float ref = m[r] == -__builtin_inff() ? 0.0f : m[r];
-      float w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i / 4][i % 4], a.scale_log2, -ref));
-      if (PT == 1 && a.lse) exact[r] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        w[r][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i / 4][i % 4], a.scale_log2, -ref));
+    }
+    if (PT == 1 && a.lse) {
+#pragma unroll
+      for (int r = 0; r < NQ; ++r)
+        exact[r] += ((w[r][0] + w[r][1]) + (w[r][2] + w[r][3])) + ((w[r][4] + w[r][5]) + (w[r][6] + w[r][7]));
+    }
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
 #pragma unroll
       for (int e = 0; e < PT; ++e) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t x = to_bf16x2(w[2 * j], w[2 * j + 1]);
+          const uint32_t x = to_bf16x2(w[r][2 * j], w[r][2 * j + 1]);
           p[r][e][j] = x;
           if (e + 1 < PT) {
-            w[2 * j] -= bf16_lo(x);
-            w[2 * j + 1] -= bf16_hi(x);
+            w[r][2 * j] -= bf16_lo(x);
+            w[r][2 * j + 1] -= bf16_hi(x);
           }
         }
         // The sums are those of the rounded weights, so a row that one
@@ -698,10 +716,25 @@ struct WideWave : RowSums<DT, D, NQ, PT> {
   __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, const WideBuffers<D>& lds,
                                        int buffer, int sub, uint32_t there) {
     const int lane = threadIdx.x & 63;
+    // All operands are asked for at once: left to itself the compiler reads
+    // each one where it is used, and waits for it.
+    u32x4 k[2][kSets], v[D / 16];
+    uint32_t ks[2][kSets];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int set = 0; set < kSets; ++set) {
+        k[t][set] = lds.k[buffer][2 * sub + t][set][lane];
+        ks[t][set] = lds.ks[buffer][2 * sub + t][set][lane];
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) v[d] = lds.v[buffer][sub][d][lane];
+    __builtin_amdgcn_sched_barrier(0);
     f32x4 s[NQ][2];
-    R::scores(s, [&](int t, int set, u32x4& k, uint32_t& ks) {
-      k = lds.k[buffer][2 * sub + t][set][lane];
-      ks = lds.ks[buffer][2 * sub + t][set][lane];
+    R::scores(s, [&](int t, int set, u32x4& x, uint32_t& xs) {
+      x = k[t][set];
+      xs = ks[t][set];
     });
     if (there != 3 || at < job.full_lo || at + kKvStep - 1 > job.full_hi) {
       uint32_t seen[NQ];
@@ -710,7 +743,7 @@ struct WideWave : RowSums<DT, D, NQ, PT> {
     u32x4 p[NQ][PT];
     R::weights(a, s, p);
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) R::add_values(d, lds.v[buffer][sub][d][lane], p);
+    for (int d = 0; d < D / 16; ++d) R::add_values(d, v[d], p);
   }
 
   // job.begin to job.end: the workgroup's positions; [own_begin, own_end) of them this wave's rows see.
@@ -990,12 +1023,13 @@ __global__ __launch_bounds__(kAttentionThreads, S::WIDE && S::D <= 192 ? 2 : 1) 
   __shared__ std::conditional_t<S::WIDE, WideBuffers<S::D>, JoinBuffers<S::D>> lds;
   RowTile tile;
   if (a.groups == 0) {
-    const int index = blockIdx.x / a.cache.heads;
+    // The last tiles first: in causal order they see most.
+    const int from_last = blockIdx.x / a.cache.heads, index = a.tiles - 1 - from_last;
     if (!row_tile(a, a.starts, index, tile)) return;
     tile = same_tile(tile);
     int lo, hi;
     tile_span(a, tile, &lo, &hi);
-    attend<S>(a, tile, blockIdx.x - index * a.cache.heads, lo / kKvStep * kKvStep, hi + 1, -1, lds);
+    attend<S>(a, tile, blockIdx.x - from_last * a.cache.heads, lo / kKvStep * kKvStep, hi + 1, -1, lds);
     return;
   }
   __shared__ SharedUnits all;
