@@ -200,8 +200,10 @@ constexpr int kTermTop = 7;  // exponent of a row's largest magnitude in its fir
 
 // The rows of a wave: queries, sums, and the mathematics of a pass of 32
 // positions. DT, D: type of queries and columns of a head. NQ: tiles of 16
-// rows. PT: bf16 parts of a weight.
-template <int DT, int D, int NQ, int PT>
+// rows. PT: bf16 parts of a weight. EXACT: sums of the weights before their
+// rounding too, which lse takes where there is one part: rounded, they would be
+// off by more than fp32's last bits.
+template <int DT, int D, int NQ, int PT, bool EXACT>
 struct RowSums {
   using H = HeadParts<D>;
   using B = HeadBlocks<D, kQueryTerms<DT>>;
@@ -210,7 +212,7 @@ struct RowSums {
   uint32_t qs[NQ][B::kSets][B::kTurns];
   f32x4 o[NQ][D / 16];
   f32x4 l[NQ];
-  float exact[NQ];         // PT 1, with lse: the lane's sum of weights before their rounding
+  float exact[NQ];         // EXACT: the lane's own part
   float m[NQ];             // reference exponent, minus infinity until a position is seen
   int lo[NQ], hi[NQ];      // positions that this lane's row sees
 
@@ -334,10 +336,9 @@ struct RowSums {
     }
   }
 
-  // Weights of the lane's eight positions in PT parts, and their sums. Few
-  // branches, each over all tiles, so that one tile's exponentials and another
-  // one's matrix instructions can be under way together.
-  __device__ __forceinline__ void weights(const AttentionArgs& a, const f32x4 (&s)[NQ][2], u32x4 (&p)[NQ][PT]) {
+  // Lets the rows' references follow their maxima where one has grown past the
+  // slack. One branch for all tiles.
+  __device__ __forceinline__ void follow(const AttentionArgs& a, const f32x4 (&s)[NQ][2]) {
     float top[NQ];
     bool above = false;
 #pragma unroll
@@ -347,43 +348,39 @@ struct RowSums {
                                      s[r][1][1], larger(s[r][1][2], s[r][1][3], s[r][1][3]));
       above |= top[r] > m[r] + kSlack;
     }
-    if (__any(above)) {
+    if (!__any(above)) return;
 #pragma unroll
-      for (int r = 0; r < NQ; ++r) {
-        const float next = fmaxf(m[r], groups_max(top[r]));
-        // exp2(-inf) = 0 on a row's first positions; a row without any keeps its zeros.
-        const float by = next == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);
-        m[r] = next;
-        exact[r] *= by;
-        l[r] *= by;
+    for (int r = 0; r < NQ; ++r) {
+      const float next = fmaxf(m[r], groups_max(top[r]));
+      // exp2(-inf) = 0 on a row's first positions; a row without any keeps its zeros.
+      const float by = next == m[r] ? 1.0f : __builtin_amdgcn_exp2f(m[r] - next);
+      m[r] = next;
+      exact[r] *= by;
+      l[r] *= by;
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) o[r][d] *= by;
-      }
+      for (int d = 0; d < D / 16; ++d) o[r][d] *= by;
     }
-    float w[NQ][8];
+  }
+
+  // Weights of the lane's eight positions in PT parts, and their sums.
+  __device__ __forceinline__ void weights(const AttentionArgs& a, const f32x4 (&s)[NQ][2], u32x4 (&p)[NQ][PT]) {
 #pragma unroll
     for (int r = 0; r < NQ; ++r) {
       const float ref = m[r] == -__builtin_inff() ? 0.0f : m[r];
+      float w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        w[r][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i / 4][i % 4], a.scale_log2, -ref));
-    }
-    if (PT == 1 && a.lse) {
-#pragma unroll
-      for (int r = 0; r < NQ; ++r)
-        exact[r] += ((w[r][0] + w[r][1]) + (w[r][2] + w[r][3])) + ((w[r][4] + w[r][5]) + (w[r][6] + w[r][7]));
-    }
-#pragma unroll
-    for (int r = 0; r < NQ; ++r) {
+        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][i / 4][i % 4], a.scale_log2, -ref));
+      if (EXACT) exact[r] += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
 #pragma unroll
       for (int e = 0; e < PT; ++e) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t x = to_bf16x2(w[r][2 * j], w[r][2 * j + 1]);
+          const uint32_t x = to_bf16x2(w[2 * j], w[2 * j + 1]);
           p[r][e][j] = x;
           if (e + 1 < PT) {
-            w[r][2 * j] -= bf16_lo(x);
-            w[r][2 * j + 1] -= bf16_hi(x);
+            w[2 * j] -= bf16_lo(x);
+            w[2 * j + 1] -= bf16_hi(x);
           }
         }
         // The sums are those of the rounded weights, so a row that one
@@ -403,10 +400,9 @@ struct RowSums {
     }
   }
 
-  // A row's sum of weights as lse takes it: rounded to one bf16 they would be
-  // off by more than fp32's last bits.
+  // A row's sum of weights as lse takes it.
   __device__ __forceinline__ float exact_sum(int r) const {
-    if constexpr (PT > 1) return l[r][0];
+    if constexpr (!EXACT) return l[r][0];
     float v = exact[r] + __shfl_xor(exact[r], 16);
     return v + __shfl_xor(v, 32);
   }
@@ -439,39 +435,72 @@ struct WaveJob {
   int length;              // positions of the sequence
 };
 
+// Where the 64 tiles of the next passes lie in memory, one a lane: the products
+// with the strides are done once for all of them in the vector unit, and a
+// pass reads its tiles' places out of the lanes. (In scalar registers they took
+// up to half of a pass's instructions.) The page numbers are asked for some
+// passes before they are needed.
+struct TileWindow {
+  uint64_t there;          // the tiles that have a page, a bit each
+  uint32_t data[2], scale[2];
+  int32_t asked;
+
+  __device__ __forceinline__ void ask(const AttentionArgs& a, const WaveJob& job, int64_t tile) {
+    int64_t place;
+    kv_place_of_tile(tile, job.length, a.cache.page_shift, a.max_pages, &place);
+    asked = job.pages[place];
+  }
+  // `tile` as it was asked for. Tiles without a page are read from page 0.
+  __device__ __forceinline__ void take(const AttentionArgs& a, const WaveJob& job, int64_t tile) {
+    int64_t place;
+    const bool on = kv_place_of_tile(tile, job.length, a.cache.page_shift, a.max_pages, &place) &&
+                    kv_is_page(asked, a.cache.pages);
+    there = __ballot(on);
+    const int64_t page = on ? asked : 0;
+    const int off = (int)(tile * kKvTile) & ((1 << a.cache.page_shift) - 1);
+    const uint64_t d = (uint64_t)(page * a.cache.page + (int64_t)off * (a.cache.dim / 2));
+    const uint64_t s = (uint64_t)(page * a.cache.scale_page + off);
+    data[0] = (uint32_t)d;
+    data[1] = (uint32_t)(d >> 32);
+    scale[0] = (uint32_t)s;
+    scale[1] = (uint32_t)(s >> 32);
+  }
+  static __device__ __forceinline__ int64_t of(const uint32_t (&x)[2], int i) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane(x[1], i) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane(x[0], i));
+  }
+  __device__ __forceinline__ int64_t data_of(int i) const { return of(data, i); }
+  __device__ __forceinline__ int64_t scale_of(int i) const { return of(scale, i); }
+};
+
 // A wave on its own: keys and values go from memory to its registers. AHEAD:
 // passes whose loads are under way. ONE: all rows of the wave belong to one
 // token, so a position is seen by all of them or none, and what the cache holds
 // where none sees is taken as ones. Else a position's NaN has to reach the rows
 // that see it and no others, for which there is the slow way.
 template <int DT, int D, int NQ, int PT, int AHEAD, bool ONE>
-struct AttentionWave : RowSums<DT, D, NQ, PT> {
-  using R = RowSums<DT, D, NQ, PT>;
+struct AttentionWave : RowSums<DT, D, NQ, PT, PT == 1> {
+  using R = RowSums<DT, D, NQ, PT, PT == 1>;
   using typename R::B;
   using typename R::H;
   using R::o;
 
-  int32_t ids;             // lane i: page of the wave's tile i of the next 64, -1: none
+  TileWindow window;       // of the next 32 passes
 
-  // Pages of the 64 tiles of the next 32 passes, from position `at` on.
-  __device__ __forceinline__ void load_pages(const AttentionArgs& a, const WaveJob& job, int at) {
+  // A lane's tile of pass `pass` and the 31 behind it.
+  __device__ __forceinline__ int64_t tile_of(const WaveJob& job, int pass) const {
     const int lane = threadIdx.x & 63;
-    const int64_t tile = ((int64_t)at + (int64_t)(lane >> 1) * job.stride) / kKvTile + (lane & 1);
-    ids = kv_page_of_tile(job.pages, tile, job.length, a.cache.page_shift, a.max_pages, a.cache.pages);
+    return ((int64_t)job.begin + (int64_t)(pass + (lane >> 1)) * job.stride) / kKvTile + (lane & 1);
   }
 
-  // `n`: the pass's number modulo 32. A tile without a page is read from page 0 and not seen.
-  __device__ __forceinline__ void load(const AttentionArgs& a, const WaveJob& job, int at, int n, KvRaw<D>& raw) {
+  // Pass `n` of the window's 32.
+  __device__ __forceinline__ void load(const AttentionArgs& a, const WaveJob& job, int n, KvRaw<D>& raw) {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       // Addresses: a place that is the same for all lanes, and a lane's own 32 bits.
-      const int32_t id = __builtin_amdgcn_readlane(ids, 2 * n + t);
-      raw.there[t] = id >= 0;
-      const int64_t page = id < 0 ? 0 : id;
-      const int off = (at + kKvTile * t) & ((1 << a.cache.page_shift) - 1);
-      const int64_t data = page * a.cache.page + off * (D / 2);
-      const int64_t scale = page * a.cache.scale_page + off;
+      const int64_t data = window.data_of(2 * n + t), scale = window.scale_of(2 * n + t);
+      raw.there[t] = window.there >> (2 * n + t) & 1;
       const GlobalBytes pk = uniform(job.k + data), pv = uniform(job.v + data);
       const GlobalBytes pks = uniform(job.ks + scale), pvs = uniform(job.vs + scale);
 #pragma unroll
@@ -517,6 +546,7 @@ struct AttentionWave : RowSums<DT, D, NQ, PT> {
       R::mask(s, at, raw.there[0], raw.there[1], seen);
     }
     u32x4 p[NQ][PT];
+    R::follow(a, s);
     R::weights(a, s, p);
 #pragma unroll
     for (int part = 0; part < H::kParts; ++part) {
@@ -576,9 +606,11 @@ struct AttentionWave : RowSums<DT, D, NQ, PT> {
     KvRaw<D> raw[AHEAD + 1];
     const int passes = (job.end - 1 - job.begin) / job.stride + 1;
     int next = 0;  // pass to be loaded
+    window.ask(a, job, tile_of(job, 0));
     const auto load_next = [&](KvRaw<D>& to) {
-      if ((next & 31) == 0) load_pages(a, job, job.begin + next * job.stride);
-      load(a, job, job.begin + next * job.stride, next & 31, to);
+      if ((next & 31) == 0) window.take(a, job, tile_of(job, next));
+      load(a, job, next & 31, to);
+      if ((next & 31) == 16) window.ask(a, job, tile_of(job, (next | 31) + 1));
       if (next < passes - 1) ++next;
     };
 #pragma unroll
@@ -606,20 +638,20 @@ constexpr int kStageTiles = kStage / kKvTile;
 
 template <int D>
 struct WideBuffers {
-  static constexpr int kSets = (D / 32 + 3) / 4;
-  u32x4 k[2][kStageTiles][kSets][64];
-  u32x4 v[2][2][D / 16][64];
-  uint32_t ks[2][kStageTiles][kSets][64];
+  static constexpr int kSets = (D / 32 + 3) / 4, kBuffers = 2;
+  u32x4 k[kBuffers][kStageTiles][kSets][64];
+  u32x4 v[kBuffers][2][D / 16][64];
+  uint32_t ks[kBuffers][kStageTiles][kSets][64];
 };
 
-template <int DT, int D, int NQ, int PT>
-struct WideWave : RowSums<DT, D, NQ, PT> {
-  using R = RowSums<DT, D, NQ, PT>;
+template <int DT, int D, int NQ, int PT, bool EXACT>
+struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
+  using R = RowSums<DT, D, NQ, PT, EXACT>;
   using typename R::B;
   using typename R::H;
   static constexpr int kSets = B::kSets;
 
-  int32_t ids;             // lane i: page of tile i of the next 64, -1: none
+  TileWindow window;       // of the next 16 stages
 
   // What a wave brings: the keys of tile `wave`, and of the values of 32
   // positions (wave / 2 of two) one half of the bytes, wave % 2: half of each
@@ -644,21 +676,13 @@ struct WideWave : RowSums<DT, D, NQ, PT> {
     load_bytes<4>(&raw.vs[t], pvs, (b << a.cache.page_shift) + (uint32_t)(4 * g));
   }
 
-  // Stage from position `at` on, its first tile number `first` of those in ids.
-  // Returns which of its tiles have a page, a bit each.
-  __device__ __forceinline__ uint32_t load_stage(const AttentionArgs& a, const WaveJob& job, int wave, int at, int first,
+  // The stage whose first tile is number `first` of the window. Returns which of
+  // its tiles have a page, a bit each.
+  __device__ __forceinline__ uint32_t load_stage(const AttentionArgs& a, const WaveJob& job, int wave, int first,
                                                  Raw& raw) {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const auto place = [&](int t, int64_t* data, int64_t* scale) {
-      const int32_t id = __builtin_amdgcn_readlane(ids, first + t);
-      const int64_t page = id < 0 ? 0 : id;
-      const int off = (at + kKvTile * t) & ((1 << a.cache.page_shift) - 1);
-      *data = page * a.cache.page + off * (D / 2);
-      *scale = page * a.cache.scale_page + off;
-    };
-    int64_t data, scale;
-    place(wave, &data, &scale);
-    const GlobalBytes pk = uniform(job.k + data), pks = uniform(job.ks + scale);
+    const GlobalBytes pk = uniform(job.k + window.data_of(first + wave));
+    const GlobalBytes pks = uniform(job.ks + window.scale_of(first + wave));
 #pragma unroll
     for (int set = 0; set < kSets; ++set) {
       const uint32_t block = B::block(set, g);
@@ -669,16 +693,14 @@ struct WideWave : RowSums<DT, D, NQ, PT> {
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      place((wave & 2) + t, &data, &scale);
+      const uint8_t* v = job.v + window.data_of(first + (wave & 2) + t);
+      const uint8_t* vs = job.vs + window.scale_of(first + (wave & 2) + t);
       if (wave & 1)
-        load_values<1>(a, job.v + data, job.vs + scale, raw, t);
+        load_values<1>(a, v, vs, raw, t);
       else
-        load_values<0>(a, job.v + data, job.vs + scale, raw, t);
+        load_values<0>(a, v, vs, raw, t);
     }
-    uint32_t there = 0;
-#pragma unroll
-    for (int t = 0; t < kStageTiles; ++t) there |= (uint32_t)(__builtin_amdgcn_readlane(ids, first + t) >= 0) << t;
-    return there;
+    return (uint32_t)(window.there >> first) & ((1 << kStageTiles) - 1);
   }
 
   template <int HALF>
@@ -712,7 +734,7 @@ struct WideWave : RowSums<DT, D, NQ, PT> {
       put_values<0>(raw, lds.v[buffer][wave >> 1]);
   }
 
-  // One pass over the 32 positions from `at` on, half `sub` of a stage.
+  // One pass over the 32 positions from `at` on, half `sub` of a stage; there: which of its two tiles have a page.
   __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, const WideBuffers<D>& lds,
                                        int buffer, int sub, uint32_t there) {
     const int lane = threadIdx.x & 63;
@@ -740,6 +762,7 @@ struct WideWave : RowSums<DT, D, NQ, PT> {
       uint32_t seen[NQ];
       R::mask(s, at, there & 1, there & 2, seen);
     }
+    R::follow(a, s);
     u32x4 p[NQ][PT];
     R::weights(a, s, p);
 #pragma unroll
@@ -754,27 +777,31 @@ struct WideWave : RowSums<DT, D, NQ, PT> {
     const int stages = (job.end - job.begin + kStage - 1) / kStage;
     constexpr int kWindow = 64 / kStageTiles;  // stages whose pages `ids` holds
     Raw raw;
-    const auto load = [&](int i) {
-      if (i % kWindow == 0) {
-        const int64_t tile = ((int64_t)job.begin + (int64_t)i * kStage) / kKvTile + (threadIdx.x & 63);
-        ids = kv_page_of_tile(job.pages, tile, job.length, a.cache.page_shift, a.max_pages, a.cache.pages);
-      }
-      return load_stage(a, job, wave, job.begin + i * kStage, i % kWindow * kStageTiles, raw);
+    const auto tile_of = [&](int i) {
+      return ((int64_t)job.begin + (int64_t)i * kStage) / kKvTile + (threadIdx.x & 63);
     };
+    const auto load = [&](int i) {
+      if (i % kWindow == 0) window.take(a, job, tile_of(i));
+      const uint32_t there = load_stage(a, job, wave, i % kWindow * kStageTiles, raw);
+      if (i % kWindow == kWindow / 2) window.ask(a, job, tile_of(i + kWindow / 2));
+      return there;
+    };
+    window.ask(a, job, tile_of(0));
     uint32_t there = load(0);
     __syncthreads();  // the buffers have been read
     put(lds, 0, wave, raw);
     __syncthreads();
     for (int i = 0; i < stages; ++i) {
       const int at = job.begin + i * kStage;
-      uint32_t next = 0;
-      if (i + 1 < stages) next = load(i + 1);
+      // Behind a condition the loads would be waited for at its end, not where
+      // they are used; the last stage's are repeated, and put where none reads.
+      const uint32_t next = load(min(i + 1, stages - 1));
 #pragma unroll
       for (int sub = 0; sub < 2; ++sub) {
         const int from = at + sub * kKvStep;
         if (from < own_end && from + kKvStep > own_begin) pass(a, job, from, lds, i & 1, sub, there >> (2 * sub) & 3);
       }
-      if (i + 1 < stages) put(lds, (i + 1) & 1, wave, raw);
+      put(lds, (i + 1) & 1, wave, raw);
       __syncthreads();
       there = next;
     }
@@ -783,10 +810,10 @@ struct WideWave : RowSums<DT, D, NQ, PT> {
 
 // What one kernel is made for. WIDE: waves have rows of their own, NQ tiles of
 // 16 each; else they share one tile and take turns with the positions.
-template <int DT_, int D_, int NQ_, int PT_, bool WIDE_, bool ONE_>
+template <int DT_, int D_, int NQ_, int PT_, bool WIDE_, bool ONE_, bool EXACT_ = false>
 struct AttentionShape {
   static constexpr int DT = DT_, D = D_, NQ = NQ_, PT = PT_;
-  static constexpr bool WIDE = WIDE_, ONE = ONE_;
+  static constexpr bool WIDE = WIDE_, ONE = ONE_, EXACT = EXACT_;
 };
 
 // Where waves that share rows join their parts.
@@ -851,9 +878,9 @@ template <int NQ>
 struct LaneRows {
   int token[NQ], head[NQ];
 };
-template <int DT, int D, int NQ, int PT>
+template <int DT, int D, int NQ, int PT, bool EXACT>
 __device__ __forceinline__ LaneRows<NQ> take_rows(const AttentionArgs& a, const RowTile& tile, int key_head, int row0,
-                                                  RowSums<DT, D, NQ, PT>& w) {
+                                                  RowSums<DT, D, NQ, PT, EXACT>& w) {
   const int c = threadIdx.x & 15;
   LaneRows<NQ> at;
 #pragma unroll
@@ -869,9 +896,10 @@ __device__ __forceinline__ LaneRows<NQ> take_rows(const AttentionArgs& a, const 
 }
 
 // The tile of 16 rows from row0 on out of a wave's sums.
-template <class S, int NQ>
+template <class S, int NQ, bool EXACT>
 __device__ __forceinline__ void store_rows(const AttentionArgs& a, const RowTile& tile, int slot, int row0,
-                                           const RowSums<S::DT, S::D, NQ, S::PT>& w, const LaneRows<NQ>& at, int r) {
+                                           const RowSums<S::DT, S::D, NQ, S::PT, EXACT>& w, const LaneRows<NQ>& at,
+                                           int r) {
   using H = HeadParts<S::D>;
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int in_tile = row0 - tile.row + c;
@@ -912,7 +940,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& ti
   job.stride = kKvStep;
   bool bad;
   {
-    WideWave<S::DT, D, NQ, S::PT> w;
+    WideWave<S::DT, D, NQ, S::PT, S::EXACT> w;
     int lo, hi;
     wave_span(a, tile, row0, NQ * 16, job, &lo, &hi);
     if (row0 >= tile.rows) hi = lo - 1;
@@ -1114,8 +1142,14 @@ hipError_t launch_shape(const AttentionArgs& a, hipStream_t s) {
 template <int DT, int D>
 hipError_t launch_type(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t s) {
   constexpr int kParts = DT == RINGSIM_FLOAT32 ? 3 : 2;
-  if (plan.wide)
-    return launch_shape<AttentionShape<DT, D, wide_tiles(DT, D), DT == RINGSIM_BFLOAT16 ? 1 : kParts, true, false>>(a, s);
+  if (plan.wide) {
+    constexpr int kTiles = wide_tiles(DT, D);
+    if constexpr (DT != RINGSIM_BFLOAT16)
+      return launch_shape<AttentionShape<DT, D, kTiles, kParts, true, false>>(a, s);
+    else
+      return a.lse ? launch_shape<AttentionShape<DT, D, kTiles, 1, true, false, true>>(a, s)
+                   : launch_shape<AttentionShape<DT, D, kTiles, 1, true, false>>(a, s);
+  }
   return !a.starts && a.each == 1 ? launch_shape<AttentionShape<DT, D, 1, kParts, false, true>>(a, s)
                                   : launch_shape<AttentionShape<DT, D, 1, kParts, false, false>>(a, s);
 }

@@ -38,16 +38,16 @@ KV_FN bool kv_slot(int64_t slot, int64_t pages, int page_shift, int32_t* page, i
   return true;
 }
 
-// Page of a sequence's tile of kKvTile tokens, -1 where there is none: past
-// the sequence, past its row of the table, or a number that is no page.
-// `table` is read only for a place inside it.
-KV_FN int32_t kv_page_of_tile(const int32_t* table, int64_t tile, int64_t end, int page_shift, int64_t max_pages,
-                              int64_t pages) {
-  const int64_t token = tile * kKvTile, place = token >> page_shift;
-  if (tile < 0 || token >= end || place >= max_pages) return -1;
-  const int32_t id = table[place];
-  return id >= 0 && id < pages ? id : -1;
+// Place of a sequence's tile of kKvTile tokens in its row of the table, kept
+// inside the row, which holds at least one; false where the tile has none: past
+// the sequence or past the row.
+KV_FN bool kv_place_of_tile(int64_t tile, int64_t end, int page_shift, int64_t max_pages, int64_t* place) {
+  const int64_t at = tile * kKvTile >> page_shift;
+  *place = at < 0 ? 0 : at < max_pages ? at : max_pages - 1;
+  return tile >= 0 && tile * kKvTile < end && at < max_pages;
 }
+// Whether a number of the table is a page.
+KV_FN bool kv_is_page(int32_t id, int64_t pages) { return id >= 0 && id < pages; }
 
 // Rows of queries. Sequence b has (starts[b+1] - starts[b]) * group rows of a
 // key head, which are cut into tiles of `rows`; its tiles are numbered from

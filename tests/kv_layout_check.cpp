@@ -55,22 +55,22 @@ int main() {
     }
   }
 
-  // Pages of tiles: the table is only read inside its row.
+  // Places of tiles: always inside the row, the tile's own where it has one.
   for (int shift = 4; shift <= 6; ++shift) {
-    std::vector<int32_t> table = {2, -1, 0, 7, 3, -2147483647 - 1, 2147483647, 1};
-    const int64_t pages = 4;
-    for (int64_t max_pages = 0; max_pages <= (int64_t)table.size(); ++max_pages) {
-      const std::vector<int32_t> row(table.begin(), table.begin() + max_pages);
+    for (int64_t max_pages = 1; max_pages <= 8; ++max_pages) {
       for (int64_t end = 0; end <= 9 << shift; end += 5) {
         for (int64_t tile = -2; tile < 10 << (shift - 4); ++tile) {
-          const int32_t got = kv_page_of_tile(row.data(), tile, end, shift, max_pages, pages);
-          const int64_t place = tile * 16 >> shift;
-          const bool there = tile >= 0 && tile * 16 < end && place < max_pages && row[place] >= 0 && row[place] < pages;
-          CHECK(got == (there ? row[place] : -1));
+          int64_t place = -1;
+          const bool got = kv_place_of_tile(tile, end, shift, max_pages, &place);
+          const int64_t own = tile * 16 >> shift;
+          CHECK(place >= 0 && place < max_pages);
+          CHECK(got == (tile >= 0 && tile * 16 < end && own < max_pages));
+          if (got) CHECK(place == own);
         }
       }
     }
   }
+  CHECK(kv_is_page(0, 1) && !kv_is_page(1, 1) && !kv_is_page(-1, 1) && !kv_is_page(INT32_MIN, 7) && !kv_is_page(INT32_MAX, 7));
 
   // Tiles of rows: each tile of each sequence has one number below the bound, and leads back to its sequence.
   uint32_t seed = 1;
