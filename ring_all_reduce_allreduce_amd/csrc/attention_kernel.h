@@ -89,9 +89,9 @@ struct KvRaw {
 };
 
 // A place in device memory that is the same for all lanes, in scalar
-// registers: loads add a lane's own 32 bits to it by themselves. Without the
-// barrier the compiler would add the lane's part first, once for all passes, and
-// then two vector registers for every load.
+// registers: a load adds a lane's own 32 bits to it by itself. Without the
+// barriers the compiler would add the lane's part first, or widen it, once for
+// all passes, and then spend an addition and two registers on every load.
 typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
 __device__ __forceinline__ GlobalBytes uniform(const uint8_t* p) {
   asm("" : "+s"(p));
@@ -104,6 +104,7 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, GlobalBytes p, uint32_t 
   typedef const __attribute__((address_space(1))) uint32_t* P32;
   typedef const __attribute__((address_space(1))) u32x2* P64;
   typedef const __attribute__((address_space(1))) u32x4* P128;
+  asm("" : "+v"(at));
   if constexpr (N == 1) {
     w[0] = p[at];
   } else if constexpr (N == 2) {
@@ -664,11 +665,13 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
   };
   static constexpr int bytes(int half) { return H::kParts == 1 ? H::n(0) / 2 : H::n(half); }
 
+  // Values of tile t of the two; `half` is HALF, or where a lane has half of its bytes a number of the wave.
   template <int HALF>
-  __device__ __forceinline__ void load_values(const AttentionArgs& a, const uint8_t* v, const uint8_t* vs, Raw& raw, int t) {
+  __device__ __forceinline__ void load_values(const AttentionArgs& a, const uint8_t* v, const uint8_t* vs, int half,
+                                              Raw& raw, int t) {
     constexpr int kPart = H::kParts == 1 ? 0 : HALF, kRow = D / 2, kBytes = bytes(HALF);
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const uint32_t from = (uint32_t)(4 * g * kRow + H::base(kPart) / 2 + c * H::n(kPart) + (H::kParts == 1 ? HALF * kBytes : 0));
+    const uint32_t from = (uint32_t)(4 * g * kRow + H::base(kPart) / 2 + c * H::n(kPart) + (H::kParts == 1 ? half * kBytes : 0));
     const GlobalBytes pv = uniform(v), pvs = uniform(vs);
 #pragma unroll
     for (int i = 0; i < 4; ++i) load_bytes<kBytes>(&raw.v[4 * t + i], pv + i * kRow, from);
@@ -695,18 +698,18 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
     for (int t = 0; t < 2; ++t) {
       const uint8_t* v = job.v + window.data_of(first + (wave & 2) + t);
       const uint8_t* vs = job.vs + window.scale_of(first + (wave & 2) + t);
-      if (wave & 1)
-        load_values<1>(a, v, vs, raw, t);
+      if (H::kParts == 2 && (wave & 1))
+        load_values<1>(a, v, vs, 1, raw, t);
       else
-        load_values<0>(a, v, vs, raw, t);
+        load_values<0>(a, v, vs, wave & 1, raw, t);
     }
     return (uint32_t)(window.there >> first) & ((1 << kStageTiles) - 1);
   }
 
   template <int HALF>
-  __device__ __forceinline__ void put_values(const Raw& raw, u32x4 (&v)[D / 16][64]) {
+  __device__ __forceinline__ void put_values(const Raw& raw, int half, u32x4 (&v)[D / 16][64]) {
     constexpr int kPart = H::kParts == 1 ? 0 : HALF, kBytes = bytes(HALF);
-    constexpr int kFirst = H::base(kPart) / 16 + (H::kParts == 1 ? 2 * kBytes * HALF : 0);
+    const int first = H::base(kPart) / 16 + (H::kParts == 1 ? 2 * kBytes * half : 0);
     const int lane = threadIdx.x & 63;
     float unit[8];
     value_units(raw.vs[0], unit);
@@ -717,7 +720,7 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = two_columns(raw.v[i], unit[i], b);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) v[kFirst + 2 * b + half][lane] = one_column(w, half);
+      for (int i = 0; i < 2; ++i) v[first + 2 * b + i][lane] = one_column(w, i);
     }
   }
 
@@ -728,10 +731,10 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
       lds.k[buffer][wave][set][lane] = raw.k[set];
       lds.ks[buffer][wave][set][lane] = raw.ks[set];
     }
-    if (wave & 1)
-      put_values<1>(raw, lds.v[buffer][wave >> 1]);
+    if (H::kParts == 2 && (wave & 1))
+      put_values<1>(raw, 1, lds.v[buffer][wave >> 1]);
     else
-      put_values<0>(raw, lds.v[buffer][wave >> 1]);
+      put_values<0>(raw, wave & 1, lds.v[buffer][wave >> 1]);
   }
 
   // One pass over the 32 positions from `at` on, half `sub` of a stage; there: which of its two tiles have a page.
