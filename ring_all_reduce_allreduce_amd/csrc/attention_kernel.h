@@ -123,6 +123,19 @@ __device__ __forceinline__ void load_bytes(uint32_t* w, GlobalBytes p, uint32_t 
   }
 }
 
+// One or two bytes at each of two places into the halves of a register.
+template <int N>
+__device__ __forceinline__ void load_two(uint32_t* w, GlobalBytes p, GlobalBytes q, uint32_t at) {
+  typedef const __attribute__((address_space(1))) uint16_t* P16;
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  static_assert(N == 1 || N == 2, "bytes");
+  asm("" : "+v"(at));
+  u16x2 x;
+  x[0] = N == 1 ? (uint16_t)p[at] : *(P16)(p + at);
+  x[1] = N == 1 ? (uint16_t)q[at] : *(P16)(q + at);
+  *w = __builtin_bit_cast(uint32_t, x);
+}
+
 // Exponent byte I of a word where the conversion reads it, in the exponent's
 // place of an fp32; it takes no notice of the other bits.
 template <int I>
@@ -633,7 +646,7 @@ struct AttentionWave : RowSums<DT, D, NQ, PT, PT == 1> {
 // positions each wave brings a quarter of the keys and values: keys as they
 // lie in memory, values already as operands of the second product, so that the
 // conversion is done once for all rows of the workgroup. Two buffers, one
-// barrier a stage, the next stage's loads under way during it.
+// barrier a stage, the loads of two stages under way.
 constexpr int kStage = 64;
 constexpr int kStageTiles = kStage / kKvTile;
 
@@ -657,13 +670,14 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
   // What a wave brings: the keys of tile `wave`, and of the values of 32
   // positions (wave / 2 of two) one half of the bytes, wave % 2: half of each
   // lane's, or where a head has two parts, one part.
+  static constexpr int bytes(int half) { return H::kParts == 1 ? H::n(0) / 2 : H::n(half); }
+  static constexpr int kWords = bytes(0) == 4 || bytes(1) == 4 ? 8 : 4;
   struct Raw {
     u32x4 k[kSets];
     uint32_t ks[kSets];
-    uint32_t v[8];
+    uint32_t v[kWords];    // of 8 positions: a register each, or two in one
     uint32_t vs[2];
   };
-  static constexpr int bytes(int half) { return H::kParts == 1 ? H::n(0) / 2 : H::n(half); }
 
   // Values of tile t of the two; `half` is HALF, or where a lane has half of its bytes a number of the wave.
   template <int HALF>
@@ -673,8 +687,13 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const uint32_t from = (uint32_t)(4 * g * kRow + H::base(kPart) / 2 + c * H::n(kPart) + (H::kParts == 1 ? half * kBytes : 0));
     const GlobalBytes pv = uniform(v), pvs = uniform(vs);
+    if constexpr (kBytes == 4) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_bytes<kBytes>(&raw.v[4 * t + i], pv + i * kRow, from);
+      for (int i = 0; i < 4; ++i) load_bytes<4>(&raw.v[4 * t + i], pv + i * kRow, from);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) load_two<kBytes>(&raw.v[2 * t + i], pv + 2 * i * kRow, pv + (2 * i + 1) * kRow, from);
+    }
     const uint32_t b = H::base(kPart) / 32 + c * H::n(kPart) / 16;
     load_bytes<4>(&raw.vs[t], pvs, (b << a.cache.page_shift) + (uint32_t)(4 * g));
   }
@@ -718,7 +737,8 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
     for (int b = 0; b < kBytes; ++b) {
       uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = two_columns(raw.v[i], unit[i], b);
+      for (int i = 0; i < 8; ++i)
+        w[i] = kBytes == 4 ? two_columns(raw.v[i], unit[i], b) : two_columns(raw.v[i / 2], unit[i], 2 * (i % 2) + b);
 #pragma unroll
       for (int i = 0; i < 2; ++i) v[first + 2 * b + i][lane] = one_column(w, i);
     }
@@ -741,9 +761,11 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
   __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, const WideBuffers<D>& lds,
                                        int buffer, int sub, uint32_t there) {
     const int lane = threadIdx.x & 63;
-    // All operands are asked for at once: left to itself the compiler reads
-    // each one where it is used, and waits for it.
-    u32x4 k[2][kSets], v[D / 16];
+    // Operands are asked for together: left to itself the compiler reads
+    // each one where it is used, and waits for it. The second half of the
+    // values follows while the first one is multiplied.
+    constexpr int kHalf = D / 32;
+    u32x4 k[2][kSets], v[kHalf];
     uint32_t ks[2][kSets];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -754,7 +776,7 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
       }
     }
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) v[d] = lds.v[buffer][sub][d][lane];
+    for (int d = 0; d < kHalf; ++d) v[d] = lds.v[buffer][sub][d][lane];
     __builtin_amdgcn_sched_barrier(0);
     f32x4 s[NQ][2];
     R::scores(s, [&](int t, int set, u32x4& x, uint32_t& xs) {
@@ -768,8 +790,14 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
     R::follow(a, s);
     u32x4 p[NQ][PT];
     R::weights(a, s, p);
+    u32x4 more[kHalf];
 #pragma unroll
-    for (int d = 0; d < D / 16; ++d) R::add_values(d, v[d], p);
+    for (int d = 0; d < kHalf; ++d) more[d] = lds.v[buffer][sub][kHalf + d][lane];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int d = 0; d < kHalf; ++d) R::add_values(d, v[d], p);
+#pragma unroll
+    for (int d = 0; d < kHalf; ++d) R::add_values(kHalf + d, more[d], p);
   }
 
   // job.begin to job.end: the workgroup's positions; [own_begin, own_end) of them this wave's rows see.
@@ -779,34 +807,39 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT> {
     if (job.begin >= job.end) return;
     const int stages = (job.end - job.begin + kStage - 1) / kStage;
     constexpr int kWindow = 64 / kStageTiles;  // stages whose pages `ids` holds
-    Raw raw;
+    Raw raw[2];
     const auto tile_of = [&](int i) {
       return ((int64_t)job.begin + (int64_t)i * kStage) / kKvTile + (threadIdx.x & 63);
     };
-    const auto load = [&](int i) {
+    // Behind a condition loads would be waited for at its end, not where they
+    // are used; so the last stage's are repeated, and put where none reads.
+    const auto load = [&](int stage, Raw& to) {
+      const int i = min(stage, stages - 1);
       if (i % kWindow == 0) window.take(a, job, tile_of(i));
-      const uint32_t there = load_stage(a, job, wave, i % kWindow * kStageTiles, raw);
+      const uint32_t there = load_stage(a, job, wave, i % kWindow * kStageTiles, to);
       if (i % kWindow == kWindow / 2) window.ask(a, job, tile_of(i + kWindow / 2));
       return there;
     };
     window.ask(a, job, tile_of(0));
-    uint32_t there = load(0);
+    uint32_t there = load(0, raw[0]), there_next = load(1, raw[1]);
     __syncthreads();  // the buffers have been read
-    put(lds, 0, wave, raw);
+    put(lds, 0, wave, raw[0]);
     __syncthreads();
-    for (int i = 0; i < stages; ++i) {
-      const int at = job.begin + i * kStage;
-      // Behind a condition the loads would be waited for at its end, not where
-      // they are used; the last stage's are repeated, and put where none reads.
-      const uint32_t next = load(min(i + 1, stages - 1));
+    for (int i = 0;;) {
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        const int from = at + sub * kKvStep;
-        if (from < own_end && from + kKvStep > own_begin) pass(a, job, from, lds, i & 1, sub, there >> (2 * sub) & 3);
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t later = load(i + 2, raw[u]);
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+          const int at = job.begin + i * kStage + sub * kKvStep;
+          if (at < own_end && at + kKvStep > own_begin) pass(a, job, at, lds, u, sub, there >> (2 * sub) & 3);
+        }
+        put(lds, u ^ 1, wave, raw[u ^ 1]);
+        __syncthreads();
+        there = there_next;
+        there_next = later;
+        if (++i == stages) return;
       }
-      put(lds, (i + 1) & 1, wave, raw);
-      __syncthreads();
-      there = next;
     }
   }
 };
