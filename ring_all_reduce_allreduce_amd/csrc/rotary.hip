@@ -17,7 +17,12 @@ namespace ringsim {
 
 constexpr int kRotaryThreads = 256;
 constexpr int kRotaryTable = 1024;  // most pairs of a workgroup's tokens: 8 KiB, or one token's
-constexpr int kRotaryAhead = 4;     // items of a thread, whose loads are under way together
+// Items of a thread: two where an item is one pack, else one, so two packs. More
+// of them leave fewer workgroups to be under way: 8192 tokens of 40 heads of
+// 128 take 27.6 us with one item (halves), 28.5 with two and 30.0 with four;
+// 20000 tokens of 9 heads of 100 fp32 (neighbours) 31.6, 29.6 and 36.9.
+template <bool NEXT>
+constexpr int kRotaryAhead = NEXT ? 2 : 1;
 
 // An item is a pack of N columns: one of each half, or N / 2 neighbouring
 // pairs, or columns that are copied (one by one where there are less than N).
@@ -35,15 +40,15 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(const RotaryArgs
     uint32_t t, head;
     int kind, c;  // 0 nothing, 1 turned, 2 copied, 3 one column copied; first column
     Packed<DT, N> u, v;
-  } item[kRotaryAhead];
+  } item[kRotaryAhead<NEXT>];
   for (uint32_t block = blockIdx.x; block < a.blocks; block += gridDim.x) {
     const uint32_t token0 = block * a.block_tokens;
     const uint32_t tokens = min((uint32_t)a.block_tokens, a.tokens - token0);
     const uint32_t items = tokens * a.block_heads * a.packs;
-    for (uint32_t base = 0; base < items; base += kRotaryThreads * kRotaryAhead) {
+    for (uint32_t base = 0; base < items; base += kRotaryThreads * kRotaryAhead<NEXT>) {
       // All loads, the first ones before the angles are formed.
 #pragma unroll
-      for (int k = 0; k < kRotaryAhead; ++k) {
+      for (int k = 0; k < kRotaryAhead<NEXT>; ++k) {
         const uint32_t n = base + k * kRotaryThreads + threadIdx.x;
         const uint32_t row = divide(n, a.by_packs);
         const int p = (int)(n - row * a.packs);
@@ -80,7 +85,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(const RotaryArgs
         __syncthreads();
       }
 #pragma unroll
-      for (int k = 0; k < kRotaryAhead; ++k) {
+      for (int k = 0; k < kRotaryAhead<NEXT>; ++k) {
         Item& e = item[k];
         if (e.kind == 0) continue;
         T* y = head_ptr<DT>(a.out, token_at(token0 + e.t, a.inner), e.head) + e.c;
@@ -127,7 +132,7 @@ static hipError_t launch_packed(RotaryArgs a, hipStream_t s) {
   if (a.packs == 0) return hipSuccess;
   // A thread's loads all at once, and the angles shared by as many heads as
   // there are; heads are cut where tokens are few, or a token's are many.
-  constexpr int kItems = kRotaryThreads * kRotaryAhead;
+  constexpr int kItems = kRotaryThreads * kRotaryAhead<NEXT>;
   const int64_t row = (int64_t)a.heads * a.packs;
   a.block_heads = (int)a.heads;
   a.block_tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kItems / std::max<int64_t>(row, 1), a.tokens));
