@@ -18,15 +18,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kNarrowRows = 16;
 
 // Workgroups that share a call's work: as many as the card runs at once.
-#ifndef RINGSIM_GROUPS
-#define RINGSIM_GROUPS 512
-#define RINGSIM_WIDE_GROUPS 512
-#endif
-#ifndef RINGSIM_DIRECT
-#define RINGSIM_DIRECT 512
-#endif
-constexpr int kNarrowGroups = RINGSIM_GROUPS;
-constexpr int kWideGroups = RINGSIM_WIDE_GROUPS;
+constexpr int kNarrowGroups = 2 * kComputeUnits;
+constexpr int kWideGroups = 2 * kComputeUnits;
 
 }  // namespace
 
@@ -44,7 +37,10 @@ AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int head
   const int64_t units = kv_units(kKvStep - 1, kKvStep - 2 + std::max<int64_t>(span, 1));
   const int64_t items = p.tiles * kv_heads;
   p.groups = 0;
-  if (p.tiles <= kSharedTiles && units > 1 && !(p.wide && items >= RINGSIM_DIRECT))
+  // Units are counted in 32 bits. Many rows and enough tiles to fill the card:
+  // shares would save less than the parts of tiles cost, which a workgroup
+  // writes and the join reads, 69 KB each.
+  if (p.tiles <= kSharedTiles && units > 1 && items <= INT32_MAX / units && !(p.wide && items >= kWideGroups))
     p.groups = (int)std::min<int64_t>(p.wide ? kWideGroups : kNarrowGroups, ceil_div(items * units, 8) * 8);
   return p;
 }
@@ -146,7 +142,11 @@ __global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const At
 
 template <int DT>
 static hipError_t launch_join(const AttentionArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.tiles * (unsigned)a.cache.heads, (unsigned)std::max(1, std::min(a.tile_rows / kJoinRows, 2048 / std::max(1, a.tiles * a.cache.heads / 8))));
+  // Rows of a tile over some workgroups, as far as that fills the card.
+  const int items = a.tiles * a.cache.heads;
+  const int rows = a.starts ? a.tile_rows : std::min(a.tile_rows, a.each * a.group);
+  const int blocks = std::min((int)ceil_div(rows, kJoinRows), std::max(1, 16 * kComputeUnits / items));
+  const dim3 grid((unsigned)items, (unsigned)blocks);
   const dim3 block(64 * kJoinRows);
   if (a.cache.dim <= 128)
     hipLaunchKernelGGL((attention_join_kernel<DT, 2>), grid, block, 0, s, a);

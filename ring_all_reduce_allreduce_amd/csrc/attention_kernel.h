@@ -609,8 +609,9 @@ struct AttentionWave : RowSums<DT, D, NQ, PT, PT == 1> {
     }
   }
 
-  template <bool SLOW>
-  __device__ __forceinline__ void run(const AttentionArgs& a, const WaveJob& job) {
+  // `prepare` is called with the first loads under way.
+  template <bool SLOW, typename PREPARE>
+  __device__ __forceinline__ void run(const AttentionArgs& a, const WaveJob& job, const PREPARE& prepare) {
     R::clear();
     if (job.begin >= job.end) return;
     // Buffers in turn, loaded AHEAD passes before they are worked on. No load
@@ -629,6 +630,7 @@ struct AttentionWave : RowSums<DT, D, NQ, PT, PT == 1> {
     };
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) load_next(raw[i]);
+    prepare();
     for (int at = job.begin;;) {
 #pragma unroll
       for (int i = 0; i <= AHEAD; ++i) {
@@ -998,7 +1000,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& ti
       job.begin = max(begin, lo / kKvStep * kKvStep);
       job.end = min(end, hi + 1);
       const auto at = take_rows(a, tile, key_head, first, w);
-      w.template run<true>(a, job);
+      w.template run<true>(a, job, [] {});
       store_rows<S>(a, tile, slot, first, w, at, 0);
     }
   }
@@ -1018,10 +1020,9 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& ti
   job.stride = kAttentionWaves * kKvStep;
   job.begin = begin + wave * kKvStep;
   job.end = min(end, hi + 1);
-  take_rows(a, tile, key_head, tile.row, w);
-  w.template run<false>(a, job);
+  w.template run<false>(a, job, [&] { take_rows(a, tile, key_head, tile.row, w); });
   if constexpr (!S::ONE) {
-    if (w.has_nan()) w.template run<true>(a, job);
+    if (w.has_nan()) w.template run<true>(a, job, [] {});
   }
   // The waves' parts of the positions, joined in a fixed order.
   const float own = w.m[0] == -__builtin_inff() && w.l[0][0] != 0.0f ? 0.0f : w.m[0];  // NaN sums without a maximum
@@ -1101,22 +1102,27 @@ __global__ __launch_bounds__(kAttentionThreads, S::WIDE && S::D <= 192 ? 2 : 1) 
     for (int i = threadIdx.x; i <= a.seqs; i += kAttentionThreads) all.starts[i] = a.starts[i];
     __syncthreads();
   }
-  for (int i = threadIdx.x; i < kSharedTiles; i += kAttentionThreads) {
-    int n = 0;
-    if (i < a.tiles && row_tile(a, all.starts, i, tile)) {
-      int lo, hi;
-      tile_span(a, tile, &lo, &hi);
-      n = (int)kv_units(lo, hi);
-    }
-    all.units[i] = n;
-  }
-  __syncthreads();
-  // Each wave: a lane adds kRun tiles, a scan over the lanes.
+  // Units of each tile: with up to 64 tiles one a lane, in each wave for itself;
+  // otherwise they are counted in LDS, and a lane adds kRun of them.
   constexpr int kRun = kSharedTiles / 64;
   const int lane = threadIdx.x & 63;
+  const bool few = !S::WIDE && a.tiles <= 64;  // with many rows the registers are needed
+  const auto units_of = [&](int i, RowTile& t) {
+    if (i >= a.tiles || !row_tile(a, all.starts, i, t)) return 0;
+    int lo, hi;
+    tile_span(a, t, &lo, &hi);
+    return (int)kv_units(lo, hi);
+  };
+  RowTile mine = {0, 0, 0, 0, 0, 0};
   int own = 0;
+  if (few) {
+    own = units_of(lane, mine);
+  } else {
+    for (int i = threadIdx.x; i < kSharedTiles; i += kAttentionThreads) all.units[i] = units_of(i, mine);
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kRun; ++i) own += all.units[lane * kRun + i];
+    for (int i = 0; i < kRun; ++i) own += all.units[lane * kRun + i];
+  }
   int upto = own;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
@@ -1125,43 +1131,51 @@ __global__ __launch_bounds__(kAttentionThreads, S::WIDE && S::D <= 192 ? 2 : 1) 
   }
   const int64_t per_head = __builtin_amdgcn_readlane(upto, 63);
   if (per_head == 0) return;
-  const int64_t units = per_head * a.cache.heads;
+  const uint32_t units = (uint32_t)per_head * (uint32_t)a.cache.heads;
   // No share is empty, so that the parts of a tile are those of consecutive
   // workgroups. Neighbouring shares, which read the same keys where tiles of one
   // sequence follow one another, go to workgroups of one XCD: those take turns.
-  const int groups = (int)min((int64_t)a.groups, units), per_xcd = (groups + 7) / 8;
+  const int groups = (int)min((uint32_t)a.groups, units), per_xcd = (groups + 7) / 8;
   const int group = (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
   if ((int)(blockIdx.x >> 3) >= per_xcd || group >= groups) return;
-  int64_t at = kv_share_begin(units, group, groups);
-  const int64_t end = kv_share_begin(units, group + 1, groups);
-  int key_head = __builtin_amdgcn_readfirstlane((int)(at / per_head));
+  int64_t at = __builtin_amdgcn_readfirstlane((int)kv_share_begin(units, group, groups));
+  const int64_t end = __builtin_amdgcn_readfirstlane((int)kv_share_begin(units, group + 1, groups));
+  int key_head = __builtin_amdgcn_readfirstlane((uint32_t)at / (uint32_t)per_head);
   const int in_head = (int)(at - key_head * per_head);
   const int run = __builtin_ctzll(__ballot(upto > in_head));  // the lane whose tiles hold the first unit
-  int index = run * kRun;
+  int index = few ? run : run * kRun;
   int before = __builtin_amdgcn_readlane(upto - own, run);  // units of the key head before tile `index`
   while (at < end) {
-    while (at - key_head * per_head >= before + __builtin_amdgcn_readfirstlane(all.units[index])) {
-      before += __builtin_amdgcn_readfirstlane(all.units[index]);
+    int n;
+    for (;;) {
+      n = few ? __builtin_amdgcn_readlane(own, index) : __builtin_amdgcn_readfirstlane(all.units[index]);
+      if (at - key_head * per_head < before + n) break;
+      before += n;
       if (++index == a.tiles) {
         index = before = 0;
         ++key_head;
       }
     }
-    const int n = __builtin_amdgcn_readfirstlane(all.units[index]);
     const int64_t first = key_head * per_head + before;  // the tile's units are [first, first + n)
     const int skip = (int)(at - first), take = (int)min((int64_t)n - skip, end - at);
-    row_tile(a, all.starts, index, tile);
+    if (few) {
+      tile = tile_of_lane(mine, index);
+    } else {
+      row_tile(a, all.starts, index, tile);
+    }
     tile = same_tile(tile);
     int lo, hi;
     tile_span(a, tile, &lo, &hi);
-    if (skip == 0 && threadIdx.x == 0) {
+    if (threadIdx.x == 0) {  // the first and the last workgroup with a part of the tile say so
       int32_t* of = a.part_of + 2 * ((int64_t)index * a.cache.heads + key_head);
-      of[0] = group;
-      of[1] = (int)kv_share_of(first + n - 1, units, groups);
+      if (skip == 0) of[0] = group;
+      if (skip + take == n) of[1] = group;
     }
     const int begin = lo / kKvStep * kKvStep + skip * kKvUnit;
     const int slot = take == n ? -1 : part_slot(group, skip == 0);
-    attend<S>(a, tile, key_head, begin, min(begin + take * kKvUnit, hi + 1), slot, lds);
+    const auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    attend<S>(a, tile, uniform(key_head), uniform(begin), uniform(min(begin + take * kKvUnit, hi + 1)), uniform(slot),
+              lds);
     at += take;
   }
 }

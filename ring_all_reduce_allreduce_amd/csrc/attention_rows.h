@@ -42,6 +42,13 @@ __device__ __forceinline__ RowTile same_tile(const RowTile& t) {
                  __builtin_amdgcn_readfirstlane(t.row),   __builtin_amdgcn_readfirstlane(t.length)};
 }
 
+// The tile that lane `i` holds.
+__device__ __forceinline__ RowTile tile_of_lane(const RowTile& t, int i) {
+  return RowTile{__builtin_amdgcn_readlane(t.seq, i),  __builtin_amdgcn_readlane(t.token, i),
+                 __builtin_amdgcn_readlane(t.first, i), __builtin_amdgcn_readlane(t.rows, i),
+                 __builtin_amdgcn_readlane(t.row, i),  __builtin_amdgcn_readlane(t.length, i)};
+}
+
 // Positions [lo, hi] that the token at position p sees.
 __device__ __forceinline__ void span(const AttentionArgs& a, int p, int length, int* lo, int* hi) {
   int64_t l, h;

@@ -86,8 +86,10 @@ constexpr int kKvUnit = 128;
 KV_FN int64_t kv_units(int64_t lo, int64_t hi) {
   return hi < lo ? 1 : (hi - lo / kKvStep * kKvStep) / kKvUnit + 1;
 }
-KV_FN int64_t kv_share_begin(int64_t units, int64_t group, int64_t groups) { return units * group / groups; }
-// The workgroup whose share holds unit p: the least one whose share ends behind it.
-KV_FN int64_t kv_share_of(int64_t p, int64_t units, int64_t groups) { return ((p + 1) * groups - 1) / units; }
+// Shares of units / groups each, some with one more, spread over the groups; up to 2^16 groups.
+KV_FN uint32_t kv_share_begin(uint32_t units, uint32_t group, uint32_t groups) {
+  const uint32_t each = units / groups, more = units - each * groups;
+  return group * each + group * more / groups;
+}
 
 }  // namespace ringsim
