@@ -67,6 +67,8 @@ ringsim_result_t ringsim_rotary(const ringsim_rotary_t* args, ringsim_stream_t s
 
 /* Tokens a page holds at most; pages hold a power of two of at least 16. */
 #define RINGSIM_KV_MAX_PAGE 1024
+/* Positions of a sequence that attention reads at most: 2^31 - 1024. */
+#define RINGSIM_ATTENTION_MAX_LENGTH 2147482624
 
 /* A paged cache of keys and values in 4 bits, in device memory. Of every
  * page, head and token the values of two neighbouring columns share a byte,
@@ -182,8 +184,8 @@ typedef struct {
  * q that belong to no sequence (before starts[0], from starts[seqs] on) are
  * not read, and their outputs stay as they are. `starts` must not decrease;
  * what leads outside q in it is cut off. Positions whose page is negative,
- * beyond the cache or beyond the table, and those from max_length on, are
- * left out. What the cache holds in positions that a token does not see does
+ * beyond the cache or beyond the table, and those from max_length (or
+ * RINGSIM_ATTENTION_MAX_LENGTH) on, are left out. What the cache holds in positions that a token does not see does
  * not reach it, NaN included.
  *
  * Products of keys with queries are exact in bf16 (those of fp16 and fp32 are

@@ -135,6 +135,7 @@ struct AttentionPlan {
   int64_t tiles;
   int groups;
 };
+// `window`: 0 where positions are not bounded by it from both sides.
 AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
                              int64_t cap, int64_t window);
 
@@ -144,6 +145,9 @@ __host__ __device__ constexpr int wide_tiles(int dtype, int dim) {
   return dtype == RINGSIM_BFLOAT16 && dim <= 128 ? 2 : 1;
 }
 
+// Most positions of a sequence: with the passes that waves and their loads are
+// ahead of each other, they are counted in 32 bits.
+constexpr int kMaxPositions = RINGSIM_ATTENTION_MAX_LENGTH;
 // Most tiles whose work is shared: their units are counted in LDS.
 constexpr int kSharedTiles = 512;
 // Where a workgroup leaves its part of a tile: the one that it begins but does

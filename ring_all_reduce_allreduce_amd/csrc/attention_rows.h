@@ -57,19 +57,25 @@ __device__ __forceinline__ void span(const AttentionArgs& a, int p, int length, 
   *hi = (int)h;
 }
 
-// Positions that any row of the tile sees.
+// Positions that any row of the tile sees; of none [0, -1], so that sums with
+// the first of them stay below kMaxPositions.
 __device__ __forceinline__ void tile_span(const AttentionArgs& a, const RowTile& t, int* lo, int* hi) {
   const int last = min(t.row + a.tile_rows, t.rows) - 1;
   int x;
   span(a, t.first + t.row / a.group, t.length, lo, &x);
   span(a, t.first + last / a.group, t.length, &x, hi);
+  if (*hi < *lo) {
+    *lo = 0;
+    *hi = -1;
+  }
 }
 
 __device__ __forceinline__ int64_t lse_index(const AttentionArgs& a, const RowTile& t, int token, int head) {
   return (int64_t)(t.token + token) * a.heads + head;
 }
 template <int DT>
-__device__ __forceinline__ typename OpElem<DT>::T* out_row(const AttentionArgs& a, const RowTile& t, int token, int head) {
+__device__ __forceinline__ typename OpElem<DT>::T* out_row(const AttentionArgs& a, const RowTile& t, int token,
+                                                           int head) {
   const int64_t at = a.starts ? (t.token + token) * a.out.s1 : t.seq * a.out.s0 + token * a.out.s1;
   return static_cast<typename OpElem<DT>::T*>(a.out.p) + at + head * a.out.s2;
 }

@@ -132,10 +132,10 @@ bool plan_of(const ringsim_paged_attention_t& a, AttentionPlan* plan, int64_t* c
   if (a.max_length < 0 || a.window < 0) return false;
   if (a.seqs == 0 || a.tokens == 0) return true;
   if (!a.starts && a.tokens % a.seqs) return false;
-  *cap = std::min<int64_t>(a.max_pages * c.page_size, INT32_MAX - kKvStep);
+  *cap = std::min<int64_t>(a.max_pages * c.page_size, kMaxPositions);
   if (a.max_length > 0) *cap = std::min(*cap, a.max_length);
   *plan = plan_attention(a.tokens, a.seqs, a.starts != nullptr, (int)a.heads, (int)c.heads, (int)c.dim, a.dtype, *cap,
-                         a.window);
+                         a.causal ? a.window : 0);
   return plan->tiles * c.heads <= kMaxBlocks;
 }
 

@@ -193,6 +193,34 @@ def test_pages_that_are_none():
     assert not bool(got.out.any()) and bool((got.lse == -math.inf).all())
 
 
+def test_the_longest_lengths():
+    """Lengths up to 2^31 - 1: in a small table, where a window leaves nothing, and in one of 2^31 positions, whose pages
+    repeat."""
+    most = 2 ** 31 - 1
+    cache, table = _cache([90, 90, 90], 16, 2, 64)
+    for shape in ((3, 4, 64), (3, 3, 4, 64), (3, 40, 4, 64)):
+        for window in (0, 50):
+            say(f"small table {shape} {window}")
+            got = _run(_q(shape, torch.bfloat16), cache, table, [most, most - 70, 90], f"window {window}",
+                       window=window, weight_rel=2.0 ** -8)
+            if window:
+                assert not bool(got.out[:2].any()) and bool((got.lse[:2] == -math.inf).all())
+    cache, table = _cache([4096], 1024, 1, 64)
+    table = torch.randint(0, cache.keys.shape[0], (1, 2 ** 21), generator=torch.Generator().manual_seed(5)).int().cuda()
+    for shape in ((1, 2, 64), (1, 100, 1, 64)):
+        for length in (most - 1023, most - 1025, most - 1100, most):
+            say(f"long table {shape} {length}")
+            q, n = _q(shape, torch.float16), torch.tensor([length], dtype=torch.int32).cuda()
+            got = rs.paged_attention(q, cache, table, n, window=1200, need_lse=True)
+            # The same with the pages that the window cannot reach taken away.
+            gone = (length - 1300) // 1024
+            (out, lse, bound, lse_bound), = ref.attention([q.reshape(-1, *shape[-2:])], cache, table[:, gone:],
+                                                          n - gone * 1024, window=1200,
+                                                          max_length=2 ** 31 - 1024 - gone * 1024)
+            ref.within(got.out.reshape(out.shape), out, bound + ref.half_step(out, q.dtype), f"length {length}: out")
+            ref.within(got.lse.reshape(lse.shape), lse, lse_bound, f"length {length}: lse")
+
+
 def test_queries_with_special_values():
     """NaN and infinities in a query stay in its row."""
     lengths = [40, 50]
