@@ -17,31 +17,51 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int kNarrowRows = 16;
 
-// Workgroups that share a call's work: as many as the card runs at once.
-constexpr int kNarrowGroups = 2 * kComputeUnits;
-constexpr int kWideGroups = 2 * kComputeUnits;
+// Workgroups that share a call's work: as many as the card runs at once, two a
+// CU. (64 sequences of 16384 with random pages of 64 positions take 212 us; with
+// half as many 244, with twice as many 220. 512 tokens of 32 heads at the end of
+// 32768: 324, 434 and 362.)
+constexpr int kGroups = 2 * kComputeUnits;
+
+// A tile that many rows share, over `units` of 128 positions: a workgroup alone
+// on its CU takes 3.2 us a unit; shares take 1 / 128 us a unit of all
+// items, but 75 us to write the parts of tiles and to join them (bf16, heads
+// of 128). 512 tokens of 32 heads at the end of 32768 positions: 324 us shared,
+// 804 a workgroup a tile; two sequences of 512 at the end of 4096: 154 and 110;
+// three prompts of 2048: 278 and 163.
+bool wide_shares(int64_t items, int64_t units) { return (410 - items) * units > 9600; }
 
 }  // namespace
 
+// With few rows of a key head all waves of a workgroup take the same 16, which
+// reads each tile of keys once for these alone; with many each wave has its own
+// and values are converted once for all. 64 sequences of 2048 positions: 56 us
+// against 64 with 32 rows, 150 against 85 with 96. (With 64 rows 105 against
+// 81, but the weights in two parts.) Where the work has to be shared that
+// pays later: 8 sequences of 8192, 71 us against 89 with 96 rows, 75 against
+// 110 with 128.
 AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
                              int64_t cap, int64_t window) {
-  AttentionPlan p;
   const int64_t group = heads / kv_heads, rows = tokens * group / seqs;  // of a sequence's key head, on average
-  p.wide = rows > 64;
-  p.tile_rows = p.wide ? 64 * wide_tiles(dtype, dim) : kNarrowRows;
-  p.tiles = ragged ? tokens * group / p.tile_rows + seqs : seqs * ceil_div(tokens / seqs * group, p.tile_rows);
-  // Positions that a tile may see: all, or a window for each of its tokens. The
-  // first unit may begin before the first of them.
-  int64_t span = cap;
-  if (window > 0) span = std::min(span, window + ceil_div(p.tile_rows, group) + 1);
-  const int64_t units = kv_units(kKvStep - 1, kKvStep - 2 + std::max<int64_t>(span, 1));
-  const int64_t items = p.tiles * kv_heads;
-  p.groups = 0;
-  // Units are counted in 32 bits. Many rows and enough tiles to fill the card:
-  // shares would save less than the parts of tiles cost, which a workgroup
-  // writes and the join reads, 69 KB each.
-  if (p.tiles <= kSharedTiles && units > 1 && items <= INT32_MAX / units && !(p.wide && items >= kWideGroups))
-    p.groups = (int)std::min<int64_t>(p.wide ? kWideGroups : kNarrowGroups, ceil_div(items * units, 8) * 8);
+  AttentionPlan p;
+  int64_t units, items;
+  const auto cut = [&](bool wide) {
+    p.wide = wide;
+    p.tile_rows = wide ? 64 * wide_tiles(dtype, dim) : kNarrowRows;
+    p.tiles = ragged ? tokens * group / p.tile_rows + seqs : seqs * ceil_div(tokens / seqs * group, p.tile_rows);
+    // Positions that a tile may see: all, or a window for each of its tokens.
+    // The first unit may begin before the first of them.
+    int64_t span = cap;
+    if (window > 0) span = std::min(span, window + ceil_div(p.tile_rows, group) + 1);
+    units = kv_units(kKvStep - 1, kKvStep - 2 + std::max<int64_t>(span, 1));
+    items = p.tiles * kv_heads;
+  };
+  cut(rows > 64);
+  bool shares = !p.wide || wide_shares(items, units);
+  if (p.wide && shares && rows <= 128) cut(false);
+  // Units are counted in 32 bits.
+  shares = shares && p.tiles <= kSharedTiles && units > 1 && items <= INT32_MAX / units;
+  p.groups = shares ? (int)std::min<int64_t>(kGroups, ceil_div(items * units, 8) * 8) : 0;
   return p;
 }
 
@@ -66,8 +86,8 @@ hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, i
 // the outputs for the weights. Heads of 128 columns and fewer leave half of
 // the lanes for a second part: even ones go to the first half, odd ones to the
 // second.
-constexpr int kJoinRows = 4;     // of a workgroup at a time
-constexpr int kJoinAhead = 8;    // outputs whose loads are under way
+constexpr int kJoinRows = 4;   // of a workgroup at a time
+constexpr int kJoinAhead = 8;  // outputs whose loads are under way
 
 template <int DT, int HALVES>
 __device__ __forceinline__ void join_row(const AttentionArgs& a, const RowTile& tile, int key_head, int in_tile,
@@ -101,7 +121,8 @@ __device__ __forceinline__ void join_row(const AttentionArgs& a, const RowTile& 
       for (int k = 0; k < kJoinAhead; ++k) {
         const int s = s0 + HALVES * k + half;
         o[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (s < n && (used >> (s & 63) & 1)) o[k] = *reinterpret_cast<const f32x4*>(out + row_of(base + s) * a.cache.dim);
+        if (s < n && (used >> (s & 63) & 1))
+          o[k] = *reinterpret_cast<const f32x4*>(out + row_of(base + s) * a.cache.dim);
       }
 #pragma unroll
       for (int k = 0; k < kJoinAhead; ++k) {
@@ -136,7 +157,8 @@ __global__ __launch_bounds__(64 * kJoinRows) void attention_join_kernel(const At
   const int first = a.part_of[2 * item], parts = a.part_of[2 * item + 1] - first + 1;
   if (parts == 1) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int row = blockIdx.y * kJoinRows + wave; row < min(a.tile_rows, tile.rows - tile.row); row += gridDim.y * kJoinRows)
+  const int rows = min(a.tile_rows, tile.rows - tile.row);
+  for (int row = blockIdx.y * kJoinRows + wave; row < rows; row += gridDim.y * kJoinRows)
     join_row<DT, HALVES>(a, tile, key_head, row, first, parts);
 }
 

@@ -227,9 +227,6 @@ hipError_t launch_kv_append(KvAppendArgs a, int dtype, hipStream_t s) {
 // in, a pack out, so that a wave's stores leave no gaps (16 columns a lane: 14.2
 // us for 8192 tokens of 8 heads of 128, now 9.6). blockIdx.y: keys or values.
 constexpr int kReadColumns = 8;
-#ifndef RINGSIM_READ_BLOCKS
-#define RINGSIM_READ_BLOCKS (1 << 20)
-#endif
 
 template <int DT>
 __global__ __launch_bounds__(kKvThreads) void kv_read_kernel(const KvReadArgs a) {
@@ -289,7 +286,7 @@ static hipError_t launch_read(KvReadArgs a, hipStream_t s) {
   a.by_packs = fast_div((uint32_t)packs);
   a.by_heads = fast_div((uint32_t)a.cache.heads);
   const int64_t groups = ((int64_t)a.tokens * a.cache.heads * packs + kKvThreads - 1) / kKvThreads;
-  const dim3 grid((unsigned)std::min<int64_t>(groups, RINGSIM_READ_BLOCKS), 2);
+  const dim3 grid((unsigned)std::min<int64_t>(groups, 1 << 20), 2);
   hipLaunchKernelGGL((kv_read_kernel<DT>), grid, dim3(kKvThreads), 0, s, a);
   return hipGetLastError();
 }

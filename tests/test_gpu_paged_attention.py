@@ -136,6 +136,15 @@ def test_prompt_over_a_split_context():
         _run_ragged([90], [5000], 128, 1, 1, 128, dtype, "split, window", weight_rel=rel, window=3000)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_many_rows_over_a_split_context(dim, dtype):
+    """More rows than a tile holds, whose context several workgroups share."""
+    rel = 2.0 ** -8 if dtype == torch.bfloat16 else None
+    say(f"many rows {dim} {dtype}")
+    _run_ragged([61, 80], [4200, 3900], 64, 1, 4, dim, dtype, "split", weight_rel=rel)
+
+
 def test_masked_places_do_not_leak():
     """NaN blocks of the cache reach the tokens that see them and no others: behind a sequence's end, behind a token
     in causal order, before its window; keys and values; narrow and wide calls; and no NaN in between."""
