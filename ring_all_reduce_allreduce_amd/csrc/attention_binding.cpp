@@ -55,7 +55,8 @@ void head_strides(const at::Tensor& t, const char* name, int64_t stride[3]) {
 
 int check_index(const at::Tensor& t, const char* name) {
   const int code = index_code(t.scalar_type());
-  if (code < 0) throw WrongType(std::string(name) + " must have dtype Int or Long, not " + c10::toString(t.scalar_type()));
+  if (code < 0)
+    throw WrongType(std::string(name) + " must have dtype Int or Long, not " + c10::toString(t.scalar_type()));
   return code;
 }
 
