@@ -190,9 +190,10 @@ typedef struct {
  *
  * Products of keys with queries are exact in bf16 (those of fp16 and fp32 are
  * split into two and three parts) and summed in fp32, infinite from 2^136 on;
- * statistics and sums are fp32. The weights go into the second product in bf16: for bf16 outputs
- * rounded to it where a call has many tokens a sequence, in two parts where it
- * has few; in two parts for fp16, in three for fp32. */
+ * statistics and sums are fp32. The weights go into the second product in
+ * bf16: for bf16 outputs rounded to it where the call's sizes give each key
+ * many rows of queries, else in two parts; in two parts for fp16, in three for
+ * fp32. */
 ringsim_result_t ringsim_paged_attention(const ringsim_paged_attention_t* args, ringsim_stream_t stream);
 
 /* Bytes of workspace that the call needs, which depend on its sizes only (0

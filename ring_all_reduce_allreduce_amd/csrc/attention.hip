@@ -25,21 +25,27 @@ constexpr int kGroups = 2 * kComputeUnits;
 
 // A tile that many rows share, over `units` of 128 positions: a workgroup alone
 // on its CU takes 3.2 us a unit; shares take 1 / 128 us a unit of all
-// items, but 75 us to write the parts of tiles and to join them (bf16, heads
-// of 128). 512 tokens of 32 heads at the end of 32768 positions: 324 us shared,
-// 804 a workgroup a tile; two sequences of 512 at the end of 4096: 154 and 110;
-// three prompts of 2048: 278 and 163.
-bool wide_shares(int64_t items, int64_t units) { return (410 - items) * units > 9600; }
+// items, but 28 us and items / 14 to write the parts of tiles and to join them
+// (bf16, heads of 128). 512 tokens of 32 heads at the end of 32768 positions:
+// 319 us shared, 804 a workgroup a tile; two sequences of 256 at the end of 8192:
+// 113 and 207; of 512 at the end of 4096: 118 and 111; three prompts of 2048: 254
+// and 160.
+bool wide_shares(int64_t items, int64_t units) { return (410 - items) * units > 3584 + 9 * items; }
+
+// Few tiles of many rows, in contexts long enough to matter and too short for
+// shares: waves that share 16 rows each are more workgroups. 8 sequences of 32
+// tokens of 32 heads: 22 us against 16 over 512 positions, 35 against 21 over
+// 1024, 61 against 29 over 2048, but 50 against 45 over 4096 and 68 against 76 over
+// 8192; one of 128 tokens over 1024 34 against 18; 8 of 64 over 1024 36 both.
+bool too_few(int64_t items, int64_t units) { return items < 128 && units > 4 && units <= 32; }
 
 }  // namespace
 
 // With few rows of a key head all waves of a workgroup take the same 16, which
 // reads each tile of keys once for these alone; with many each wave has its own
 // and values are converted once for all. 64 sequences of 2048 positions: 56 us
-// against 64 with 32 rows, 150 against 85 with 96. (With 64 rows 105 against
-// 81, but the weights in two parts.) Where the work has to be shared that
-// pays later: 8 sequences of 8192, 71 us against 89 with 96 rows, 75 against
-// 110 with 128.
+// against 64 with 32 rows, 150 against 84 with 96. (With 64 rows 105 against
+// 81, but the weights in two parts.)
 AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
                              int64_t cap, int64_t window) {
   const int64_t group = heads / kv_heads, rows = tokens * group / seqs;  // of a sequence's key head, on average
@@ -57,10 +63,10 @@ AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int head
     items = p.tiles * kv_heads;
   };
   cut(rows > 64);
-  bool shares = !p.wide || wide_shares(items, units);
-  if (p.wide && shares && rows <= 128) cut(false);
+  if (p.wide && too_few(items, units)) cut(false);
   // Units are counted in 32 bits.
-  shares = shares && p.tiles <= kSharedTiles && units > 1 && items <= INT32_MAX / units;
+  const bool shares = (!p.wide || wide_shares(items, units)) && p.tiles <= kSharedTiles && units > 1 &&
+                      items <= INT32_MAX / units;
   p.groups = shares ? (int)std::min<int64_t>(kGroups, ceil_div(items * units, 8) * 8) : 0;
   return p;
 }

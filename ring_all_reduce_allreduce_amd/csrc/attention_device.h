@@ -71,6 +71,9 @@ struct Packed {
       }
     }
   }
+  // KEEP: what is read again soon, or written by lanes that lie apart, whose
+  // bytes the L2 then puts together.
+  template <bool KEEP = false>
   __device__ __forceinline__ void store(void* p) const {
     if constexpr (kBytes == 2) {
       *static_cast<uint16_t*>(p) = (uint16_t)w[0];
@@ -80,9 +83,13 @@ struct Packed {
       *static_cast<u32x2_e2*>(p) = u32x2{w[0], w[1]};
     } else {
 #pragma unroll
-      for (int k = 0; k < kBytes / 16; ++k)
-        __builtin_nontemporal_store(u32x4{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]},
-                                    static_cast<u32x4_e2*>(p) + k);
+      for (int k = 0; k < kBytes / 16; ++k) {
+        const u32x4 v = {w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
+        if constexpr (KEEP)
+          static_cast<u32x4_e2*>(p)[k] = v;
+        else
+          __builtin_nontemporal_store(v, static_cast<u32x4_e2*>(p) + k);
+      }
     }
   }
   __device__ __forceinline__ float get(int i) const {

@@ -889,14 +889,14 @@ __device__ __forceinline__ void store_columns(const AttentionArgs& a, const RowT
     if (sum == 0.0f) return;  // no position, nothing to join
     Packed<RINGSIM_FLOAT32, 8> y;
     y.set(f);
-    y.store(a.part_out + ((int64_t)slot * a.tile_rows + in_tile) * S::D + col);
+    y.store<true>(a.part_out + ((int64_t)slot * a.tile_rows + in_tile) * S::D + col);
   } else {
     const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] *= by;
     Packed<S::DT, 8> y;
     y.set(f);
-    y.store(out_row<S::DT>(a, tile, token, head) + col);
+    y.template store<true>(out_row<S::DT>(a, tile, token, head) + col);
   }
 }
 

@@ -143,6 +143,8 @@ def test_many_rows_over_a_split_context(dim, dtype):
     rel = 2.0 ** -8 if dtype == torch.bfloat16 else None
     say(f"many rows {dim} {dtype}")
     _run_ragged([61, 80], [4200, 3900], 64, 1, 4, dim, dtype, "split", weight_rel=rel)
+    _run_ragged([100], [6000], 64, 1, 1, dim, dtype, "split, window", weight_rel=rel, window=4500)
+    _run_ragged([100], [1500], 64, 1, 1, dim, dtype, "few tiles", weight_rel=rel)
 
 
 def test_masked_places_do_not_leak():
