@@ -188,8 +188,10 @@ typedef struct {
  * RINGSIM_ATTENTION_MAX_LENGTH) on, are left out. What the cache holds in positions that a token does not see does
  * not reach it, NaN included.
  *
- * Products of keys with queries are exact in bf16 (those of fp16 and fp32 are
- * split into two and three parts) and summed in fp32, infinite from 2^136 on;
+ * Products of keys with queries are taken in two to five parts of a query and
+ * summed in fp32, infinite from 2^136 on; where the call's sizes give each key
+ * many rows of bf16 or fp16 queries, products below 2^-13 of the largest one of
+ * neighbouring columns may be left out, else and in fp32 below 2^-18 of it;
  * statistics and sums are fp32. The weights go into the second product in
  * bf16: for bf16 outputs rounded to it where the call's sizes give each key
  * many rows of queries, else in two parts; in two parts for fp16, in three for

@@ -252,6 +252,61 @@ def test_queries_with_special_values():
     ref.within(got, want[0][0], want[0][2] + ref.half_step(want[0][0], torch.float32), "large query")
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_small_columns_beside_large_ones(dtype):
+    """The lse of one position is its score: 1 + 2^-e, of two columns, and 1 - 2^-e. The score is exact in fp32; five
+    roundings follow (scale * log2(e), its product, ln 2, the product with it, and the sum with a logarithm of 1)."""
+    least = 16 if dtype == torch.bfloat16 else 20
+    for dim in (64, 128, 192):
+        cache, table, n = rs.kv_cache(1, 1, 16, dim), torch.zeros(1, 1), torch.ones(1)
+        k = torch.ones(1, 1, dim, device="cuda")
+        rs.kv_append(cache, k, k, torch.zeros(1, dtype=torch.long, device="cuda"))
+        q = torch.zeros(1, 3 * 2 * least, dim)
+        for i, other in enumerate((1, 7, 15)):
+            for e in range(1, least + 1):
+                for j, sign in enumerate((1, -1)):
+                    q[0, (i * least + e - 1) * 2 + j, 0] = 1.0
+                    q[0, (i * least + e - 1) * 2 + j, other] = sign * 2.0 ** -e
+        got = rs.paged_attention(q.to(dtype).cuda(), cache, table.int().cuda(), n.int().cuda(), scale=1.0, need_lse=True)
+        want = q.to(dtype).double().sum(-1)
+        # So many rows of a key head in 16 bits are split coarsely: the unit adds neighbouring products in 14 bits of the
+        # largest, here 1, so that the other one may be left out below 2^-13 of it, but for nothing above that.
+        coarse = 0.0 if dtype == torch.float32 else 2.0 ** -13
+        ref.within(got.lse, want, 5 * 2.0 ** -24 * want.abs() + coarse, f"{dim} {dtype}")
+        # The same rows, two a sequence, lose nothing.
+        few = q.to(dtype).cuda().view(-1, 2, dim)
+        seqs = few.shape[0]
+        got = rs.paged_attention(few, cache, table.int().cuda().expand(seqs, 1), n.int().cuda().expand(seqs).contiguous(),
+                                 scale=1.0, need_lse=True)
+        ref.within(got.lse.view(1, -1), want, 5 * 2.0 ** -24 * want.abs(), f"{dim} {dtype}, two rows a sequence")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_scores_keep_fp32(dim, dtype):
+    """Scores of random columns. Of T parts the first T - 2 lose nothing; products of the last two are off by at most
+    2^-13 of the part's largest one (its codes reach 256, a block's 6): 256 * 6 * 2^-13 * 2^(-5 (T - 2)) each, twice
+    that for both, against a row's largest column, which is 128 or more: 1.5 * 2^-8 * 2^(-5 (T - 2)) of it times the
+    block's power of two. The sums are fp32's: dim / 16 + T additions of at most 2^-23 of the magnitudes."""
+    parts = {torch.bfloat16: 3, torch.float16: 4, torch.float32: 5}[dtype]
+    gen, n = torch.Generator().manual_seed(dim), 64
+    cache = rs.kv_cache(n, 1, 16, dim)
+    k = torch.empty(n, 1, dim).normal_(0, 1, generator=gen) * torch.empty(dim).normal_(0, 0.5, generator=gen).exp()
+    rs.kv_append(cache, k.cuda(), k.cuda(), torch.arange(n, device="cuda") * 16)
+    q = torch.empty(n, 16, dim).normal_(0, 1.5, generator=gen).to(dtype)
+    table = torch.arange(n, dtype=torch.int32, device="cuda").view(n, 1)
+    got = rs.paged_attention(q.cuda(), cache, table, torch.ones(n, dtype=torch.int32, device="cuda"), scale=1.0,
+                             need_lse=True)
+    keys = ref.from_cache(cache, 0)[:, 0, 0]
+    units = torch.exp2(cache.key_scales.cpu()[:, 0, :, 0].double() - 127)
+    x = q.double()
+    want, size = (x * keys[:, None]).sum(-1), (x * keys[:, None]).abs().sum(-1)
+    lost = x.abs().amax(-1) * 32 * units.sum(-1, keepdim=True) * 1.5 * 2.0 ** (-8 - 5 * (parts - 2))
+    # What 5 parts leave of fp32, 2^-26 of the largest column for the smallest ones, is below `lost`.
+    bound = lost + (dim / 16 + parts) * 2.0 ** -23 * size + 6 * 2.0 ** -24 * want.abs()
+    ref.within(got.lse, want, bound, f"scores {dim} {dtype}")
+
+
 def test_large_scores():
     """One position rules a row, scores over a thousand apart, in any order."""
     lengths = [600]
