@@ -39,6 +39,12 @@ bool wide_shares(int64_t items, int64_t units) { return (410 - items) * units > 
 // 8192; one of 128 tokens over 1024 34 against 18; 8 of 64 over 1024 36 both.
 bool too_few(int64_t items, int64_t units) { return items < 128 && units > 4 && units <= 32; }
 
+// Rows of 16 bits that see few positions: the coarse split's errors of the scores
+// do not average out in their lse (1e-6 of it and more). That costs time: 6
+// sequences of up to 1774 tokens of 16 heads and a window of 27 take 73 us, with
+// tiles of 128 rows 31.
+bool short_window(int dtype, int64_t window) { return dtype != RINGSIM_FLOAT32 && window > 0 && window <= kKvUnit; }
+
 }  // namespace
 
 // With few rows of a key head all waves of a workgroup take the same 16, which
@@ -63,7 +69,7 @@ AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int head
     items = p.tiles * kv_heads;
   };
   cut(rows > 64);
-  if (p.wide && too_few(items, units)) cut(false);
+  if (p.wide && (too_few(items, units) || short_window(dtype, window))) cut(false);
   // Units are counted in 32 bits.
   const bool shares = (!p.wide || wide_shares(items, units)) && p.tiles <= kSharedTiles && units > 1 &&
                       items <= INT32_MAX / units;
