@@ -75,7 +75,8 @@ ringsim_result_t ringsim_rotary(const ringsim_rotary_t* args, ringsim_stream_t s
  * the even column in its low half, as sign, two bits of exponent and one of
  * mantissa (0, 0.5, 1, 1.5, 2, 3, 4, 6); each 32 columns have one exponent
  * byte s and stand for their values times 2^(s - 127). s is 1 to 252, or 255
- * where the 32 are NaN.
+ * where the 32 are NaN; what a token sees of other bytes is undefined, finite
+ * or not, and what it does not see may be anything.
  *   keys, values             [pages, heads, page_size, dim / 2]
  *   key_scales, value_scales [pages, heads, dim / 32, page_size]
  * The last two dimensions of each are contiguous; pages and heads are strides

@@ -519,8 +519,8 @@ struct TileWindow {
 // A wave on its own: keys and values go from memory to its registers. AHEAD:
 // passes whose loads are under way. ONE: all rows of the wave belong to one
 // token, so a position is seen by all of them or none, and what the cache holds
-// where none sees is taken as ones. Else a position's NaN has to reach the rows
-// that see it and no others, for which there is the slow way.
+// where none sees is taken as ones. Else what is not finite in a position has to
+// reach the rows that see it and no others, for which there is the slow way.
 template <int DT, int D, int NQ, int PT, int AHEAD, bool ONE>
 struct AttentionWave : RowSums<DT, D, NQ, PT, PT == 1, true> {
   using R = RowSums<DT, D, NQ, PT, PT == 1, true>;
@@ -572,8 +572,9 @@ struct AttentionWave : RowSums<DT, D, NQ, PT, PT == 1, true> {
     }
   }
 
-  // One pass over the 32 positions from `at` on. SLOW: a position's NaN values
-  // reach the rows that see it and no others, which 0 * NaN would not do.
+  // One pass over the 32 positions from `at` on. SLOW: a position's values that
+  // are not finite make NaN of the rows that see it and no others, which a weight
+  // of 0 times them would not do.
   template <bool SLOW>
   __device__ __forceinline__ void pass(const AttentionArgs& a, const WaveJob& job, int at, const KvRaw<D>& raw) {
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -609,11 +610,13 @@ struct AttentionWave : RowSums<DT, D, NQ, PT, PT == 1, true> {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = two_columns(raw.v[i][H::reg0(part) + b / 4], unit[i], b % 4);
         if constexpr (SLOW) {
+          // NaN blocks, and infinities, which exponents of 253 and 254 make of the larger codes.
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const bool bad = (raw.vs[i / 4][part] >> (8 * (i % 4)) & 0xff) == kKvNan;
-            w[i] = bad ? 0 : w[i];
-            nan[i] = bad ? 0x3f803f80u : 0;
+            const uint32_t bad = ((w[i] & 0x7f80u) == 0x7f80u ? 0xffffu : 0) |
+                                 ((w[i] & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0);
+            w[i] &= ~bad;
+            nan[i] = bad & 0x3f803f80u;
           }
         }
 #pragma unroll
