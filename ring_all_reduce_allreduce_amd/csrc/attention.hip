@@ -64,7 +64,7 @@ AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int head
     // Positions that a tile may see: all, or a window for each of its tokens.
     // The first unit may begin before the first of them.
     int64_t span = cap;
-    if (window > 0) span = std::min(span, window + ceil_div(p.tile_rows, group) + 1);
+    if (window > 0 && window < cap) span = std::min(span, window + ceil_div(p.tile_rows, group) + 1);
     units = kv_units(kKvStep - 1, kKvStep - 2 + std::max<int64_t>(span, 1));
     items = p.tiles * kv_heads;
   };

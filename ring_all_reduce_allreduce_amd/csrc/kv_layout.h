@@ -72,10 +72,11 @@ KV_FN int64_t kv_seq_of_tile(const int32_t* starts, int64_t seqs, int64_t tokens
   return lo;
 }
 
-// Positions [*lo, *hi] that the token at position p sees, of `end` positions.
+// Positions [*lo, *hi] that the token at position p sees, of `end` positions. A
+// window may be any number: it is only subtracted where the result is one of p's.
 KV_FN void kv_span(int64_t p, int64_t end, int causal, int64_t window, int64_t* lo, int64_t* hi) {
   *hi = causal && p < end - 1 ? p : end - 1;
-  *lo = window > 0 && p - window + 1 > 0 ? p - window + 1 : 0;
+  *lo = window > 0 && p >= window ? p - window + 1 : 0;
 }
 
 // Shares of the work. A tile of rows that sees positions lo to hi has units of

@@ -1,0 +1,25 @@
+"""The C entries of the attention-step operators at the ends of their arguments'
+ranges. Needs no GPU: a call is refused before anything is enqueued, and sizes of
+workspaces are the host's."""
+import ctypes
+
+import pytest
+
+from tests.test_attention_cpu import BAD, OK, L, _append, _attention, _rotary  # noqa: F401
+
+MOST = 2 ** 63 - 1
+
+
+def _bytes(L, **over):  # noqa: F811
+    n = ctypes.c_size_t(12345)
+    assert L.ringsim_paged_attention_workspace(_attention(**over), n) == OK
+    return n.value
+
+
+@pytest.mark.parametrize("sizes", [dict(tokens=1, seqs=1, max_pages=512), dict(tokens=64, seqs=64, max_pages=256),
+                                   dict(tokens=512, seqs=1, max_pages=512), dict(tokens=3 * 2048, seqs=3, max_pages=94)],
+                         ids=str)
+def test_windows_past_every_position_cut_a_call_as_none_does(L, sizes):  # noqa: F811
+    want = _bytes(L, **sizes)
+    for window in (1 << 31, 1 << 40, MOST - 1000, MOST - 1, MOST):
+        assert _bytes(L, window=window, **sizes) == want
