@@ -164,7 +164,7 @@ ringsim_result_t ringsim_rotary(const ringsim_rotary_t* a, ringsim_stream_t stre
       !token_count(a->outer, a->inner, &tokens))
     return RINGSIM_INVALID_ARGUMENT;
   if (a->heads < 0 || a->heads > kMaxHeads || a->dim < 1 || a->dim > RINGSIM_ROTARY_MAX_DIM || a->pairs < 0 ||
-      2 * a->pairs > a->dim)
+      a->pairs > a->dim / 2)
     return RINGSIM_INVALID_ARGUMENT;
   if (tokens == 0 || a->heads == 0) return RINGSIM_SUCCESS;
   const int64_t size[3] = {a->outer, a->inner, a->heads};
@@ -197,7 +197,7 @@ ringsim_result_t ringsim_kv_append(const ringsim_kv_append_t* a, ringsim_stream_
   const RoctxRange range("ringsim_kv_append");
   int64_t tokens = 0;
   if (!a || !value_type(a->dtype) || !std::isfinite(a->scale) || !valid_cache(a->cache, true) ||
-      !token_count(a->outer, a->inner, &tokens) || a->pairs < 0 || 2 * a->pairs > a->cache.dim)
+      !token_count(a->outer, a->inner, &tokens) || a->pairs < 0 || a->pairs > a->cache.dim / 2)
     return RINGSIM_INVALID_ARGUMENT;
   if (!index_type(a->slot_dtype) || (a->pairs > 0 && !index_type(a->position_dtype))) return RINGSIM_INVALID_ARGUMENT;
   if (tokens == 0) return RINGSIM_SUCCESS;

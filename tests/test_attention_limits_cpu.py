@@ -23,3 +23,11 @@ def test_windows_past_every_position_cut_a_call_as_none_does(L, sizes):  # noqa:
     want = _bytes(L, **sizes)
     for window in (1 << 31, 1 << 40, MOST - 1000, MOST - 1, MOST):
         assert _bytes(L, window=window, **sizes) == want
+
+
+@pytest.mark.parametrize("pairs", [1 << 62, (1 << 62) + 1, (1 << 62) + (1 << 20), MOST, -(1 << 62), -MOST - 1])
+def test_pairs_beyond_a_head_are_refused(L, pairs):  # noqa: F811
+    """2 * pairs does not fit 64 bits: it must not look like a small number. Calls without tokens, which enqueue nothing."""
+    assert L.ringsim_rotary(_rotary(pairs=pairs, outer=0), None) == BAD
+    assert L.ringsim_kv_append(_append(pairs=pairs, outer=0), None) == BAD
+    assert L.ringsim_rotary(_rotary(outer=0), None) == OK and L.ringsim_kv_append(_append(outer=0), None) == OK
