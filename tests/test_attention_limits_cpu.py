@@ -31,3 +31,11 @@ def test_pairs_beyond_a_head_are_refused(L, pairs):  # noqa: F811
     assert L.ringsim_rotary(_rotary(pairs=pairs, outer=0), None) == BAD
     assert L.ringsim_kv_append(_append(pairs=pairs, outer=0), None) == BAD
     assert L.ringsim_rotary(_rotary(outer=0), None) == OK and L.ringsim_kv_append(_append(outer=0), None) == OK
+
+
+@pytest.mark.parametrize("cache", [dict(page_size=1 << 62), dict(page_size=MOST), dict(page_size=2048), dict(page_size=48),
+                                   dict(dim=80), dict(dim=1 << 40), dict(dim=MOST)], ids=str)
+def test_workspaces_of_impossible_caches_are_refused(L, cache):  # noqa: F811
+    """As the call itself refuses them: sizes whose products leave 64 bits have no workspace."""
+    n = ctypes.c_size_t(0)
+    assert L.ringsim_paged_attention_workspace(_attention(cache), n) == BAD
