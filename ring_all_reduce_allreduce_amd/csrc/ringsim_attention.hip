@@ -83,15 +83,16 @@ int shift_of(int64_t page) {
   return s;
 }
 
-bool valid_cache_sizes(const ringsim_kv_cache_t& c) {
+// Sizes of a cache but its number of pages.
+bool valid_page(const ringsim_kv_cache_t& c) {
   if (c.dim != 64 && c.dim != 96 && c.dim != 128 && c.dim != 192 && c.dim != 256) return false;
   if (c.page_size < kKvTile || c.page_size > RINGSIM_KV_MAX_PAGE || (c.page_size & (c.page_size - 1))) return false;
-  return c.pages >= 1 && c.pages <= INT32_MAX && c.heads >= 1 && c.heads <= kMaxHeads;
+  return c.heads >= 1 && c.heads <= kMaxHeads;
 }
 
 // `written`: no two pages or heads may overlap.
 bool valid_cache(const ringsim_kv_cache_t& c, bool written) {
-  if (!valid_cache_sizes(c)) return false;
+  if (!valid_page(c) || c.pages < 1 || c.pages > INT32_MAX) return false;
   for (const void* p : {c.keys, c.values, c.key_scales, c.value_scales})
     if (!p || !aligned(p, 16)) return false;
   const int64_t size[2] = {c.pages, c.heads};
@@ -130,7 +131,7 @@ bool valid_frequencies(const double* f, int64_t pairs) { return pairs == 0 || (f
 // Sizes and types of an attention call, and how it is cut.
 bool plan_of(const ringsim_paged_attention_t& a, AttentionPlan* plan, int64_t* cap) {
   const ringsim_kv_cache_t& c = a.cache;
-  if (!value_type(a.dtype) || !valid_cache_sizes(c)) return false;
+  if (!value_type(a.dtype) || !valid_page(c)) return false;
   if (a.tokens < 0 || a.seqs < 0 || a.heads < 1 || a.heads > kMaxHeads || a.heads % c.heads) return false;
   if (a.tokens > INT32_MAX / a.heads || a.seqs > INT32_MAX || a.max_pages < 0 || a.max_pages > INT32_MAX) return false;
   if (a.max_length < 0 || a.window < 0) return false;

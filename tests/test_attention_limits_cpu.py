@@ -39,3 +39,9 @@ def test_workspaces_of_impossible_caches_are_refused(L, cache):  # noqa: F811
     """As the call itself refuses them: sizes whose products leave 64 bits have no workspace."""
     n = ctypes.c_size_t(0)
     assert L.ringsim_paged_attention_workspace(_attention(cache), n) == BAD
+
+
+def test_workspaces_do_not_depend_on_the_number_of_pages(L):  # noqa: F811
+    n, want = ctypes.c_size_t(0), _bytes(L)
+    for pages in (0, 1, MOST):
+        assert L.ringsim_paged_attention_workspace(_attention(dict(pages=pages)), n) == OK and n.value == want
