@@ -196,7 +196,7 @@ typedef struct {
  * statistics and sums are fp32. The weights go into the second product in
  * bf16: for bf16 outputs rounded to it where the call's sizes give each key
  * many rows of queries, else in two parts; in two parts for fp16, in three for
- * fp32. */
+ * fp32. lse is formed of the weights before that, in fp32. */
 ringsim_result_t ringsim_paged_attention(const ringsim_paged_attention_t* args, ringsim_stream_t stream);
 
 /* Bytes of workspace that the call needs, which depend on its sizes only (0

@@ -239,8 +239,9 @@ constexpr float kTermLeast = 2.0f;
 // The rows of a wave: queries, sums, and the mathematics of a pass of 32
 // positions. DT, D: type of queries and columns of a head. NQ: tiles of 16
 // rows. PT: bf16 parts of a weight. EXACT: sums of the weights before their
-// rounding too, which lse takes where there is one part: rounded, they would be
-// off by more than fp32's last bits. FINE: how queries are split.
+// rounding too, which lse takes where there are one or two parts: rounded, they
+// would be off by 2^-8 or 2^-17, and not by fp32's last bits. FINE: how queries
+// are split.
 template <int DT, int D, int NQ, int PT, bool EXACT, bool FINE>
 struct RowSums {
   static constexpr int kTerms = query_terms(DT, FINE);
@@ -522,8 +523,8 @@ struct TileWindow {
 // where none sees is taken as ones. Else what is not finite in a position has to
 // reach the rows that see it and no others, for which there is the slow way.
 template <int DT, int D, int NQ, int PT, int AHEAD, bool ONE>
-struct AttentionWave : RowSums<DT, D, NQ, PT, PT == 1, true> {
-  using R = RowSums<DT, D, NQ, PT, PT == 1, true>;
+struct AttentionWave : RowSums<DT, D, NQ, PT, (PT < 3), true> {
+  using R = RowSums<DT, D, NQ, PT, (PT < 3), true>;
   using typename R::B;
   using typename R::H;
   using R::o;
@@ -891,6 +892,7 @@ template <int D>
 struct JoinBuffers {
   static constexpr int kRow = D + 4;  // rows start 4 banks apart
   float refs[kAttentionWaves][16], sums[kAttentionWaves][16];
+  float exact[kAttentionWaves][16];  // sums of unrounded weights
   float outs[kAttentionWaves][16][kRow];
 };
 
@@ -1058,9 +1060,11 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& ti
   }
   // The waves' parts of the positions, joined in a fixed order.
   const float own = w.m[0] == -__builtin_inff() && w.l[0][0] != 0.0f ? 0.0f : w.m[0];  // NaN sums without a maximum
+  const float unrounded = w.exact_sum(0);
   if (g == 0) {
     lds.refs[wave][c] = own;
     lds.sums[wave][c] = w.l[0][0];
+    lds.exact[wave][c] = unrounded;
   }
   __syncthreads();
   float top = lds.refs[0][c];
@@ -1085,13 +1089,16 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& ti
   const int rows = min(16, tile.rows - tile.row);
   for (int k = threadIdx.x; k < rows * (D / 8); k += kAttentionThreads) {
     const int row = k / (D / 8), col = (k - row * (D / 8)) * 8;
-    float best = lds.refs[0][row], sum = 0.0f;
+    float best = lds.refs[0][row], sum = 0.0f, exact = 0.0f;
 #pragma unroll
     for (int i = 1; i < kAttentionWaves; ++i) best = fmaxf(best, lds.refs[i][row]);
 #pragma unroll
     for (int i = 0; i < kAttentionWaves; ++i) {
       const float ref = lds.refs[i][row];
-      if (ref != -__builtin_inff()) sum += lds.sums[i][row] * (ref == best ? 1.0f : __builtin_amdgcn_exp2f(ref - best));
+      if (ref == -__builtin_inff()) continue;
+      const float scale = ref == best ? 1.0f : __builtin_amdgcn_exp2f(ref - best);
+      sum += lds.sums[i][row] * scale;
+      exact += lds.exact[i][row] * scale;
     }
     float f[8];
 #pragma unroll
@@ -1101,7 +1108,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& ti
       for (int i = 1; i < kAttentionWaves; ++i) f[e] += lds.outs[i][row][col + e];
     }
     const int t = (tile.row + row) / a.group, h = key_head * a.group + tile.row + row - t * a.group;
-    if (col == 0) store_sums<S>(a, tile, slot, row, t, h, best, sum, sum);
+    if (col == 0) store_sums<S>(a, tile, slot, row, t, h, best, sum, exact);
     store_columns<S>(a, tile, slot, row, t, h, col, sum, f);
   }
   __syncthreads();  // before the buffers are written again
@@ -1228,11 +1235,10 @@ hipError_t launch_type(const AttentionArgs& a, const AttentionPlan& plan, hipStr
   constexpr int kParts = DT == RINGSIM_FLOAT32 ? 3 : 2;
   if (plan.wide) {
     constexpr int kTiles = wide_tiles(DT, D);
-    if constexpr (DT != RINGSIM_BFLOAT16)
-      return launch_shape<AttentionShape<DT, D, kTiles, kParts, true, false>>(a, s);
-    else
-      return a.lse ? launch_shape<AttentionShape<DT, D, kTiles, 1, true, false, true>>(a, s)
-                   : launch_shape<AttentionShape<DT, D, kTiles, 1, true, false>>(a, s);
+    constexpr int kWideParts = DT == RINGSIM_BFLOAT16 ? 1 : kParts;
+    if constexpr (kWideParts < 3)
+      if (a.lse) return launch_shape<AttentionShape<DT, D, kTiles, kWideParts, true, false, true>>(a, s);
+    return launch_shape<AttentionShape<DT, D, kTiles, kWideParts, true, false>>(a, s);
   }
   return !a.starts && a.each == 1 ? launch_shape<AttentionShape<DT, D, 1, kParts, false, true>>(a, s)
                                   : launch_shape<AttentionShape<DT, D, 1, kParts, false, false>>(a, s);
