@@ -192,8 +192,10 @@ typedef struct {
  * Products of keys with queries are taken in two to five parts of a query and
  * summed in fp32, infinite from 2^136 on; where the call's sizes give each key
  * many rows of bf16 or fp16 queries, products below 2^-13 of the largest one of
- * neighbouring columns may be left out, else and in fp32 below 2^-18 of it;
- * statistics and sums are fp32. The weights go into the second product in
+ * neighbouring columns may be left out, else and in fp32 below 2^-18 of it (also
+ * with many rows where `lse` is wanted and max_length, or with `causal` the
+ * window, leaves a token no more than 128 positions); statistics and sums are
+ * fp32. The weights go into the second product in
  * bf16: for bf16 outputs rounded to it where the call's sizes give each key
  * many rows of queries, else in two parts; in two parts for fp16, in three for
  * fp32. lse is formed of the weights before that, in fp32. */

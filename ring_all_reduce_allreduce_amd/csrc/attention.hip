@@ -1,5 +1,5 @@
-// attention.hip -- how an attention call is cut into workgroups, and the
-// kernel that joins the parts of contexts that were split.
+// attention.hip -- the attention kernel's launch, and the kernel that joins the
+// parts of contexts that were split.
 #include <algorithm>
 
 #include "attention_rows.h"
@@ -11,71 +11,7 @@ struct MaxF32 {
   static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
 };
 
-namespace {
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-constexpr int kNarrowRows = 16;
-
-// Workgroups that share a call's work: as many as the card runs at once, two a
-// CU. (64 sequences of 16384 with random pages of 64 positions take 212 us; with
-// half as many 244, with twice as many 220. 512 tokens of 32 heads at the end of
-// 32768: 324, 434 and 362.)
-constexpr int kGroups = 2 * kComputeUnits;
-
-// A tile that many rows share, over `units` of 128 positions: a workgroup alone
-// on its CU takes 3.2 us a unit; shares take 1 / 128 us a unit of all
-// items, but 28 us and items / 14 to write the parts of tiles and to join them
-// (bf16, heads of 128). 512 tokens of 32 heads at the end of 32768 positions:
-// 319 us shared, 804 a workgroup a tile; two sequences of 256 at the end of 8192:
-// 113 and 207; of 512 at the end of 4096: 118 and 111; three prompts of 2048: 254
-// and 160.
-bool wide_shares(int64_t items, int64_t units) { return (410 - items) * units > 3584 + 9 * items; }
-
-// Few tiles of many rows, in contexts long enough to matter and too short for
-// shares: waves that share 16 rows each are more workgroups. 8 sequences of 32
-// tokens of 32 heads: 22 us against 16 over 512 positions, 35 against 21 over
-// 1024, 61 against 29 over 2048, but 50 against 45 over 4096 and 68 against 76 over
-// 8192; one of 128 tokens over 1024 34 against 18; 8 of 64 over 1024 36 both.
-bool too_few(int64_t items, int64_t units) { return items < 128 && units > 4 && units <= 32; }
-
-// Rows of 16 bits that see few positions: the coarse split's errors of the scores
-// do not average out in their lse (1e-6 of it and more). That costs time: 6
-// sequences of up to 1774 tokens of 16 heads and a window of 27 take 73 us, with
-// tiles of 128 rows 31.
-bool short_window(int dtype, int64_t window) { return dtype != RINGSIM_FLOAT32 && window > 0 && window <= kKvUnit; }
-
-}  // namespace
-
-// With few rows of a key head all waves of a workgroup take the same 16, which
-// reads each tile of keys once for these alone; with many each wave has its own
-// and values are converted once for all. 64 sequences of 2048 positions: 56 us
-// against 64 with 32 rows, 150 against 84 with 96. (With 64 rows 105 against
-// 81, but the weights in two parts.)
-AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
-                             int64_t cap, int64_t window) {
-  const int64_t group = heads / kv_heads, rows = tokens * group / seqs;  // of a sequence's key head, on average
-  AttentionPlan p;
-  int64_t units, items;
-  const auto cut = [&](bool wide) {
-    p.wide = wide;
-    p.tile_rows = wide ? 64 * wide_tiles(dtype, dim) : kNarrowRows;
-    p.tiles = ragged ? tokens * group / p.tile_rows + seqs : seqs * ceil_div(tokens / seqs * group, p.tile_rows);
-    // Positions that a tile may see: all, or a window for each of its tokens.
-    // The first unit may begin before the first of them.
-    int64_t span = cap;
-    if (window > 0 && window < cap) span = std::min(span, window + ceil_div(p.tile_rows, group) + 1);
-    units = kv_units(kKvStep - 1, kKvStep - 2 + std::max<int64_t>(span, 1));
-    items = p.tiles * kv_heads;
-  };
-  cut(rows > 64);
-  if (p.wide && (too_few(items, units) || short_window(dtype, window))) cut(false);
-  // Units are counted in 32 bits.
-  const bool shares = (!p.wide || wide_shares(items, units)) && p.tiles <= kSharedTiles && units > 1 &&
-                      items <= INT32_MAX / units;
-  p.groups = shares ? (int)std::min<int64_t>(kGroups, ceil_div(items * units, 8) * 8) : 0;
-  return p;
-}
+static_assert(kGroups == 2 * kComputeUnits, "workgroups that share a call's work");
 
 hipError_t launch_attention(const AttentionArgs& a, const AttentionPlan& plan, int dtype, hipStream_t s) {
   hipError_t e = hipErrorInvalidValue;
@@ -179,7 +115,7 @@ static hipError_t launch_join(const AttentionArgs& a, hipStream_t s) {
   // Rows of a tile over some workgroups, as far as that fills the card.
   const int items = a.tiles * a.cache.heads;
   const int rows = a.starts ? a.tile_rows : std::min(a.tile_rows, a.each * a.group);
-  const int blocks = std::min((int)ceil_div(rows, kJoinRows), std::max(1, 16 * kComputeUnits / items));
+  const int blocks = std::min((rows + kJoinRows - 1) / kJoinRows, std::max(1, 16 * kComputeUnits / items));
   const dim3 grid((unsigned)items, (unsigned)blocks);
   const dim3 block(64 * kJoinRows);
   if (a.cache.dim <= 128)

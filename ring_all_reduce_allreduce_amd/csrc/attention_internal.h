@@ -5,8 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "../../include/ringsim_attention.h"
-#include "kv_layout.h"
+#include "attention_plan.h"
 #include "ops_internal.h"
 
 namespace ringsim {
@@ -128,29 +127,9 @@ struct AttentionArgs {
 // values that fp32 would not hold.
 constexpr int kQueryExponent = 8;
 
-// How a call is cut: rows of a tile, tiles, and workgroups that share them.
-struct AttentionPlan {
-  int wide;               // 1: many rows, a wave its own rows; 0: waves share rows
-  int tile_rows;
-  int64_t tiles;
-  int groups;
-};
-// `window`: 0 where positions are not bounded by it from both sides.
-AttentionPlan plan_attention(int64_t tokens, int64_t seqs, bool ragged, int heads, int kv_heads, int dim, int dtype,
-                             int64_t cap, int64_t window);
-
-// Tiles of 16 rows of a wave with rows of its own: two where a wave's registers
-// hold them, else one (types whose products take several parts, long heads).
-// Three prompts of 2048 tokens of 32 heads of 128: 163 us, with one 212.
-__host__ __device__ constexpr int wide_tiles(int dtype, int dim) {
-  return dtype == RINGSIM_BFLOAT16 && dim <= 128 ? 2 : 1;
-}
-
 // Most positions of a sequence: with the passes that waves and their loads are
 // ahead of each other, they are counted in 32 bits.
 constexpr int kMaxPositions = RINGSIM_ATTENTION_MAX_LENGTH;
-// Most tiles whose work is shared: their units are counted in LDS.
-constexpr int kSharedTiles = 512;
 // Where a workgroup leaves its part of a tile: the one that it begins but does
 // not end last in its share, one that it only goes on with first.
 __host__ __device__ __forceinline__ int part_slot(int group, bool begins) { return 2 * group + (begins ? 1 : 0); }

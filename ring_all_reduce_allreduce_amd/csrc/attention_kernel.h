@@ -227,7 +227,8 @@ __device__ __forceinline__ f32x4 mfma_scaled(const u32x4& k, uint32_t ks, const 
 // each part before. Scores of 192 columns in fp32 are 8e-8 of their size off, 5e-6
 // without. With few rows memory bounds, and the part costs nothing; with many
 // bf16 and fp16 stay with the coarse split, whose errors are below those of
-// weights and outputs in 16 bits.
+// weights and outputs in 16 bits, but where lse, which is fp32, is wanted over
+// few positions.
 constexpr int query_terms(int dtype, bool fine) {
   return dtype == RINGSIM_FLOAT32 ? 5 : (dtype == RINGSIM_FLOAT16 ? 3 : 2) + (fine ? 1 : 0);
 }
@@ -692,9 +693,9 @@ struct WideBuffers {
   uint32_t ks[kBuffers][kStageTiles][kSets][64];
 };
 
-template <int DT, int D, int NQ, int PT, bool EXACT>
-struct WideWave : RowSums<DT, D, NQ, PT, EXACT, DT == RINGSIM_FLOAT32> {
-  using R = RowSums<DT, D, NQ, PT, EXACT, DT == RINGSIM_FLOAT32>;
+template <int DT, int D, int NQ, int PT, bool EXACT, bool FINE>
+struct WideWave : RowSums<DT, D, NQ, PT, EXACT, FINE> {
+  using R = RowSums<DT, D, NQ, PT, EXACT, FINE>;
   using typename R::B;
   using typename R::H;
   static constexpr int kSets = B::kSets;
@@ -880,11 +881,12 @@ struct WideWave : RowSums<DT, D, NQ, PT, EXACT, DT == RINGSIM_FLOAT32> {
 };
 
 // What one kernel is made for. WIDE: waves have rows of their own, NQ tiles of
-// 16 each; else they share one tile and take turns with the positions.
-template <int DT_, int D_, int NQ_, int PT_, bool WIDE_, bool ONE_, bool EXACT_ = false>
+// 16 each; else they share one tile and take turns with the positions. EXACT and
+// FINE: of wide ones, as in RowSums.
+template <int DT_, int D_, int NQ_, int PT_, bool WIDE_, bool ONE_, bool EXACT_ = false, bool FINE_ = true>
 struct AttentionShape {
   static constexpr int DT = DT_, D = D_, NQ = NQ_, PT = PT_;
-  static constexpr bool WIDE = WIDE_, ONE = ONE_, EXACT = EXACT_;
+  static constexpr bool WIDE = WIDE_, ONE = ONE_, EXACT = EXACT_, FINE = FINE_;
 };
 
 // Where waves that share rows join their parts.
@@ -1012,7 +1014,7 @@ __device__ __forceinline__ void attend(const AttentionArgs& a, const RowTile& ti
   job.stride = kKvStep;
   bool bad;
   {
-    WideWave<S::DT, D, NQ, S::PT, S::EXACT> w;
+    WideWave<S::DT, D, NQ, S::PT, S::EXACT, S::FINE> w;
     int lo, hi;
     wave_span(a, tile, row0, NQ * 16, job, &lo, &hi);
     if (row0 >= tile.rows) hi = lo - 1;
@@ -1234,11 +1236,15 @@ template <int DT, int D>
 hipError_t launch_type(const AttentionArgs& a, const AttentionPlan& plan, hipStream_t s) {
   constexpr int kParts = DT == RINGSIM_FLOAT32 ? 3 : 2;
   if (plan.wide) {
-    constexpr int kTiles = wide_tiles(DT, D);
-    constexpr int kWideParts = DT == RINGSIM_BFLOAT16 ? 1 : kParts;
-    if constexpr (kWideParts < 3)
-      if (a.lse) return launch_shape<AttentionShape<DT, D, kTiles, kWideParts, true, false, true>>(a, s);
-    return launch_shape<AttentionShape<DT, D, kTiles, kWideParts, true, false>>(a, s);
+    constexpr int kWideParts = DT == RINGSIM_BFLOAT16 ? 1 : kParts, kTiles = wide_tiles(DT, D, false);
+    if constexpr (DT == RINGSIM_FLOAT32) {
+      return launch_shape<AttentionShape<DT, D, kTiles, kWideParts, true, false>>(a, s);
+    } else {
+      if (plan.fine)
+        return launch_shape<AttentionShape<DT, D, wide_tiles(DT, D, true), kWideParts, true, false, true>>(a, s);
+      return a.lse ? launch_shape<AttentionShape<DT, D, kTiles, kWideParts, true, false, true, false>>(a, s)
+                   : launch_shape<AttentionShape<DT, D, kTiles, kWideParts, true, false, false, false>>(a, s);
+    }
   }
   return !a.starts && a.each == 1 ? launch_shape<AttentionShape<DT, D, 1, kParts, false, true>>(a, s)
                                   : launch_shape<AttentionShape<DT, D, 1, kParts, false, false>>(a, s);

@@ -140,7 +140,7 @@ bool plan_of(const ringsim_paged_attention_t& a, AttentionPlan* plan, int64_t* c
   *cap = std::min<int64_t>(a.max_pages * c.page_size, kMaxPositions);
   if (a.max_length > 0) *cap = std::min(*cap, a.max_length);
   *plan = plan_attention(a.tokens, a.seqs, a.starts != nullptr, (int)a.heads, (int)c.heads, (int)c.dim, a.dtype, *cap,
-                         a.causal ? a.window : 0);
+                         a.causal ? a.window : 0, a.lse != nullptr);
   return plan->tiles * c.heads <= kMaxBlocks;
 }
 

@@ -61,3 +61,37 @@ def test_two_positions(dtype, call):
             off_by = ((got.double().cpu() - want).abs() - U * (8 * want + 10))
             assert float(off_by.max()) <= 0.0, \
                 f"{call} {dim} {place}: {float(off_by.max())} beyond the bound, {int((off_by > 0).sum())} of {x.numel()}"
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("dim", [64, 96, 128, 192, 256])
+def test_small_columns_of_many_rows_over_few_positions(dim, dtype):
+    """Many rows of a key head that see 128 positions at most lose nothing of a score's small columns: all keys are ones,
+    so that a row of c positions with columns 1 and +-2^-e has an lse of 1 +- 2^-e + log(c).
+
+    Roundings, in units of 2^-24: five of the score (scale * log2(e), its product, ln 2, the product with it, the sum
+    with a logarithm); exp2, 2; sums, one for each of 4 positions, 8 over lanes and waves; the logarithm's 2, ln 2's,
+    the product's and the sum's, 6 of log(c); 2 more of the weights' arguments beside 0."""
+    least = 16 if dtype == torch.bfloat16 else 20
+    x = torch.zeros(3 * 2 * least, dim)
+    for i, other in enumerate((1, 7, 15)):
+        for e in range(1, least + 1):
+            for j, sign in enumerate((1, -1)):
+                x[(i * least + e - 1) * 2 + j, 0] = 1.0
+                x[(i * least + e - 1) * 2 + j, other] = sign * 2.0 ** -e
+    rows, x = x.shape[0], x.to(dtype)
+    cache = rs.kv_cache(1, 1, 16, dim)
+    cache.keys.fill_(0x22)
+    score = x.double().sum(-1)
+    for length, window, pages in ((rows, 0, 8), (128, 0, 8), (700, 128, 44), (700, 27, 44), (3, 0, 1)):
+        say(f"{dim} {dtype} {length} {window}")
+        n = torch.tensor([length], dtype=torch.int32).cuda()
+        table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+        causal = length >= rows
+        got = rs.paged_attention(x.cuda().view(1, rows, 1, dim), cache, table, n, scale=1.0, window=window, causal=causal,
+                                 need_lse=True).lse.view(-1)
+        count = torch.arange(length - rows + 1, length + 1).clamp(max=window or length) if causal else torch.full((rows,), 3)
+        want = score + torch.log(count.double())
+        bound = U * (5 * score.abs() + 12 + count / 4 + 6 * torch.log(count.double()))
+        off_by = (got.double().cpu() - want).abs() - bound
+        assert float(off_by.max()) <= 0.0, f"{dim} {length} {window}: {float(off_by.max())} beyond the bound"
