@@ -57,6 +57,17 @@ int main() {
       {50 * 100, 50, false, 32, 8, 128, BF16, 128, 0, "w", "f"},
       {50 * 100, 50, false, 32, 8, 128, BF16, 129, 0, "w", "w"},
       {50 * 100, 50, false, 32, 8, 128, BF16, 128, 500, "w", "f"},
+      // test_gpu_attention_wide.py (with both ways a window bounds no span), test_gpu_attention_unseen.py
+      {127, 2, true, 2, 1, 128, BF16, 336, 27, "w", "f"},
+      {127, 2, true, 2, 1, 64, F16, 336, 300, "w", "w"},
+      {91, 3, true, 4, 1, 96, F16, 384, 128, "w", "f"},
+      {91, 3, true, 4, 1, 256, BF16, 384, 200, "w", "w"},
+      {57, 2, true, 5, 1, 64, BF16, 208, 0, "w", "w"},
+      {230, 2, true, 4, 2, 128, F16, 272, 150, "w", "w"},
+      {100, 1, false, 1, 1, 64, BF16, RINGSIM_ATTENTION_MAX_LENGTH, 250, "w", "w"},
+      {100, 1, false, 1, 1, 64, F16, RINGSIM_ATTENTION_MAX_LENGTH, 100, "w", "f"},
+      {250, 2, true, 2, 1, 64, BF16, 336, 140, "w", "w"},
+      {141, 2, true, 2, 1, 192, F16, 4512, 0, "ws", "ws"},
   };
   for (const Call& c : calls) {
     for (const bool lse : {false, true}) {
