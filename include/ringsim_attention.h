@@ -62,7 +62,7 @@ typedef struct {
  *     b' = scale * (b cos t + a sin t)
  * (with `inverse` by -t) and copies the columns behind the pairs. Angles are
  * formed and reduced in 64 bits, so that far positions keep their places on
- * the circle; the rotation is in fp32, rounded once. */
+ * the circle, and then rounded to fp32; the rotation is in fp32, rounded once. */
 ringsim_result_t ringsim_rotary(const ringsim_rotary_t* args, ringsim_stream_t stream);
 
 /* Tokens a page holds at most; pages hold a power of two of at least 16. */
@@ -186,19 +186,22 @@ typedef struct {
  * not read, and their outputs stay as they are. `starts` must not decrease;
  * what leads outside q in it is cut off. Positions whose page is negative,
  * beyond the cache or beyond the table, and those from max_length (or
- * RINGSIM_ATTENTION_MAX_LENGTH) on, are left out. What the cache holds in positions that a token does not see does
- * not reach it, NaN included.
+ * RINGSIM_ATTENTION_MAX_LENGTH) on, are left out. What the cache holds in
+ * positions that a token does not see does not reach it, NaN and infinities
+ * included.
  *
  * Products of keys with queries are taken in two to five parts of a query and
  * summed in fp32, infinite from 2^136 on; where the call's sizes give each key
  * many rows of bf16 or fp16 queries, products below 2^-13 of the largest one of
  * neighbouring columns may be left out, else and in fp32 below 2^-18 of it (also
  * with many rows where `lse` is wanted and max_length, or with `causal` the
- * window, leaves a token no more than 128 positions); statistics and sums are
- * fp32. The weights go into the second product in
- * bf16: for bf16 outputs rounded to it where the call's sizes give each key
- * many rows of queries, else in two parts; in two parts for fp16, in three for
- * fp32. lse is formed of the weights before that, in fp32. */
+ * window, leaves a token no more than 128 positions). Statistics and sums are
+ * fp32, of weights up to 2^8: outputs of a token that sees n positions are finite
+ * where their values are below 2^119 / n, and may be infinite or NaN beyond. The
+ * weights go into the second product in bf16: for bf16 outputs rounded to it
+ * where the call's sizes give each key many rows of queries, else in two parts;
+ * in two parts for fp16, in three for fp32. lse is formed of the weights before
+ * that, in fp32. */
 ringsim_result_t ringsim_paged_attention(const ringsim_paged_attention_t* args, ringsim_stream_t stream);
 
 /* Bytes of workspace that the call needs, which depend on its sizes only (0
