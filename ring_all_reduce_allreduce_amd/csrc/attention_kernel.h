@@ -301,8 +301,8 @@ struct RowSums {
     // Exponent of the first part; the last one's has to stay above 2^-127.
     int e = (int)(top >> 23) - 127 - kTermTop;
     e = max(e, kQueryExponent + kTermBits * kTerms - 126);
-    // Two factors, as one might leave fp32's range.
-    const float up = __builtin_ldexpf(1.0f, -e / 2), more = __builtin_ldexpf(1.0f, -e - -e / 2);
+    // -93 to 120, so that 2^-e is a normal number.
+    const float up = __builtin_ldexpf(1.0f, -e);
 #pragma unroll
     for (int set = 0; set < B::kSets; ++set) {
 #pragma unroll
@@ -315,7 +315,7 @@ struct RowSums {
           for (int w = 0; w < 4; ++w) {
             if (term == 0) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) v[4 * w + i] *= up * more;
+              for (int i = 0; i < 4; ++i) v[4 * w + i] *= up;
             }
             const auto now = [&](int i) {
               return FINE && term + 2 < kTerms && __builtin_fabsf(v[4 * w + i]) < kTermLeast ? 0.0f : v[4 * w + i];

@@ -52,8 +52,9 @@ inline bool wide_shares(int64_t items, int64_t units) { return (410 - items) * u
 // Few tiles of many rows, in contexts long enough to matter and too short for
 // shares: waves that share 16 rows each are more workgroups. 8 sequences of 32
 // tokens of 32 heads: 22 us against 16 over 512 positions, 35 against 21 over
-// 1024, 61 against 29 over 2048, but 50 against 45 over 4096 and 68 against 76 over
-// 8192; one of 128 tokens over 1024 34 against 18; 8 of 64 over 1024 36 both.
+// 1024, 61 against 29 over 2048, 50 against 45 over 4096 (33 units: left out,
+// though the two meet behind it) and 68 against 76 over 8192; one of 128 tokens
+// over 1024 34 against 18; 8 of 64 over 1024 36 both.
 inline bool too_few(int64_t items, int64_t units) { return items < 128 && units > 4 && units <= 32; }
 
 // Rows of 16 bits that see few positions, where lse is wanted: the coarse split's
