@@ -182,7 +182,9 @@ def paged_attention(q, cache: KvCache, pages, lengths, *, starts=None, causal: b
     ``max_length``, where a program knows it, says that no sequence is longer
     (default: all that a row of ``pages`` holds) and so into how many parts
     contexts are split. A token that sees nothing gets zeros, and minus
-    infinity in ``lse``, which is returned if given or ``need_lse``."""
+    infinity in ``lse``, which is returned if given or ``need_lse``; it is
+    formed in fp32 from weights that are not rounded, whatever ``q``'s type.
+    Wanting it may change the last bits of ``out`` in 16 bits."""
     if stream is not None:
         with _on(stream):
             return Attention._make(_b.paged_attention(q, cache, pages, lengths, starts, causal, window, scale,

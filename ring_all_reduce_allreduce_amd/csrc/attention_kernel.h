@@ -23,8 +23,10 @@
 // What bounds it: with few rows memory, 17/32 bytes a column of keys and of
 // values. 64 sequences of up to 16384 positions of 8 heads of 128, 636 MB of
 // cache, take 130 us (4.9 TB/s); their loads alone take 117 us, their arithmetic
-// alone 87. With many rows the vector unit beside the matrix one: 3 prompts of
-// 2048 tokens of 32 heads behind up to 4000 positions take 283 us (844 TFLOP/s);
+// alone 87. With many rows staging and the vector unit beside the matrix one: 3
+// prompts of 2048 tokens of 32 heads behind up to 4000 positions take 283 us (844
+// TFLOP/s), about a third of it less where nothing has to be loaded, converted and
+// put into LDS (201 us of then 299) and 42 us less without a softmax;
 // of the 1500 clocks of a pass of 32 positions the matrix unit works in 544 and the
 // vector unit, with exponentials and conversions, in 630 to 730, and with two
 // waves a SIMD the two overlap in part only.

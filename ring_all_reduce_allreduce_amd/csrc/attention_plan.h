@@ -59,7 +59,9 @@ inline bool too_few(int64_t items, int64_t units) { return items < 128 && units 
 
 // Rows of 16 bits that see few positions, where lse is wanted: the coarse split's
 // errors of the scores do not average out in it (1.2e-6 of it over 27 positions,
-// 7e-7 over 128, single rows up to 3e-4 off; the fine split 4e-8 and 4e-6).
+// 7e-7 over 128, single rows up to 3e-4 off; the fine split 4e-8 and 4e-6). bf16
+// tiles are then half as long: two prompts of 2048 tokens of 32 heads of 128 with a
+// window of 128 take 49 us for 37, 50 of 100 tokens 54 for 52.
 inline bool fine_split(int dtype, int64_t positions, bool lse) {
   return lse && dtype != RINGSIM_FLOAT32 && positions <= kKvUnit;
 }
