@@ -92,14 +92,20 @@ inline const at::Tensor& required(PyObject* o, const char* name) {
   return *t;
 }
 
+// A conversion's error: of a number that is too large a wrong value, else its own.
+[[noreturn]] inline void conversion_error() {
+  if (!PyErr_ExceptionMatches(PyExc_OverflowError)) throw PythonError{};
+  PyErr_Clear();
+  throw WrongValue("a number is out of range");
+}
 inline double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) throw PythonError{};
+  if (v == -1.0 && PyErr_Occurred()) conversion_error();
   return v;
 }
 inline long whole(PyObject* o) {
   const long v = PyLong_AsLong(o);
-  if (v == -1 && PyErr_Occurred()) throw PythonError{};
+  if (v == -1 && PyErr_Occurred()) conversion_error();
   return v;
 }
 

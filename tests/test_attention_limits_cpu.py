@@ -5,7 +5,9 @@ import ctypes
 
 import pytest
 
-from tests.test_attention_cpu import BAD, OK, L, _append, _attention, _rotary  # noqa: F401
+import ring_all_reduce_allreduce_amd as rs
+
+from tests.test_attention_cpu import BAD, OK, L, _append, _attention, _host, _rotary  # noqa: F401
 
 MOST = 2 ** 63 - 1
 
@@ -45,3 +47,14 @@ def test_workspaces_do_not_depend_on_the_number_of_pages(L):  # noqa: F811
     n, want = ctypes.c_size_t(0), _bytes(L)
     for pages in (0, 1, MOST):
         assert L.ringsim_paged_attention_workspace(_attention(dict(pages=pages)), n) == OK and n.value == want
+
+
+def test_numbers_out_of_range_are_values_refused():
+    """Of the binding: TypeError or ValueError, as for other wrong arguments."""
+    cache, x, i, f, pages, lengths = _host()
+    for call in (lambda: rs.paged_attention(x, cache, pages, lengths, window=1 << 70),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, max_length=-(1 << 70)),
+                 lambda: rs.paged_attention(x, cache, pages, lengths, scale=10 ** 400),
+                 lambda: rs.rotary(x, i, f, scale=10 ** 400), lambda: rs.kv_append(cache, x, x, i, scale=-10 ** 400)):
+        with pytest.raises(ValueError, match="out of range"):
+            call()
